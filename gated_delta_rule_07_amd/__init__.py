@@ -18,14 +18,22 @@ __all__ = ["kda_chunk_fwd", "kda_chunk_fwd_snapshots", "kda_chunk_fwd_varlen", "
            "kda_chunk_fwd_split_noalloc", "KDA_SPLIT_SCRATCH_BYTES",
            "kda_decode_step", "kda_decode_step_gated",
            "kda_decode_verify",
-           "kda_decode_commit", "kda_status_string", "kda_version",
+           "kda_decode_commit",
+           "kda_qk_norm", "kda_cache_fork", "kda_cache_free", "kda_cache_compact", "kda_cache_copy",
+           "kda_decode_step_paged", "kda_tree_verify", "kda_tree_commit",
+           "kda_status_string", "kda_version",
            "kda_last_hip_error", "library_path", "load_library", "bind", "KdaError",
-           "KDA_F32", "KDA_BF16", "KDA_MAX_SNAPSHOTS", "KDA_MAX_DRAFT"]
+           "KDA_F32", "KDA_BF16", "KDA_MAX_SNAPSHOTS", "KDA_MAX_DRAFT", "KDA_MAX_PAGES", "KDA_MAX_FORKS",
+           "KDA_MAX_PAGED_SEQS", "KDA_MAX_TREE"]
 
 KDA_F32, KDA_BF16 = 0, 1
 KDA_MAX_SNAPSHOTS = 128
 KDA_MAX_DRAFT = 16
 KDA_SPLIT_SCRATCH_BYTES = 64 << 20
+KDA_MAX_PAGES = 65536
+KDA_MAX_FORKS = 1024
+KDA_MAX_PAGED_SEQS = 4096
+KDA_MAX_TREE = 64
 _PKG = Path(__file__).resolve().parent
 _LIB_PATH = _PKG / "libkda.so"
 _lib = None
@@ -89,6 +97,26 @@ def bind(path) -> ctypes.CDLL:
     lib.kda_decode_verify.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, vp]
     lib.kda_decode_commit.restype = i32
     lib.kda_decode_commit.argtypes = [vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp]
+    i64, f32 = ctypes.c_longlong, ctypes.c_float
+    lib.kda_qk_norm.restype = i32
+    lib.kda_qk_norm.argtypes = [vp, i64, vp, i64, i32, i32, vp, vp, f32, f32, vp, vp, i32, i32, vp, i64, vp, i64,
+                                i32, i32, i32, i32, i32, vp]
+    lib.kda_cache_fork.restype = i32
+    lib.kda_cache_fork.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp]
+    lib.kda_cache_free.restype = i32
+    lib.kda_cache_free.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp]
+    lib.kda_cache_compact.restype = i32
+    lib.kda_cache_compact.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp]
+    lib.kda_cache_copy.restype = i32
+    lib.kda_cache_copy.argtypes = [vp, vp, sz, i32, i32, i32, vp, vp, i32, vp]
+    lib.kda_decode_step_paged.restype = i32
+    lib.kda_decode_step_paged.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, vp, i32, vp, vp, vp, i32,
+                                          i32, i32, i32, i32, vp]
+    lib.kda_tree_verify.restype = i32
+    lib.kda_tree_verify.argtypes = [vp, vp, vp, i32, vp, vp, vp, i32, vp, vp, vp, vp, i32, vp,
+                                    i32, i32, i32, i32, i32, vp]
+    lib.kda_tree_commit.restype = i32
+    lib.kda_tree_commit.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_status_string.argtypes = [i32]
     lib.kda_last_hip_error.restype = i32
@@ -479,3 +507,321 @@ def kda_decode_commit(k, alpha, u, n_accept, S, *, stream=None):
     if st != 0:
         raise KdaError(st, "kda_decode_commit")
     return S
+
+
+_NORMS = {"l2": 0, "rms": 1}
+_PAIRINGS = {"halves": 0, "pairs": 1}
+
+
+def _run(name, dev, stream, *args):
+    """Call `name` of the library on `dev` (made current for the call where it is not)."""
+    fn = getattr(load_library(), name)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream.cuda_stream)
+    if st != 0:
+        raise KdaError(st, name)
+
+
+def _dp(t):
+    return None if t is None else t.data_ptr()
+
+
+def _int_list(t, name, dev, shape):
+    _check(t, name, torch.int32, dev)
+    if t.shape != shape:
+        raise ValueError(f"libkda: {name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _head_rows(t, name):
+    """(tokens, heads, d, row stride in elements) of [n,H,d] or [B,T,H,d] rows of dense heads."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"libkda: {name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"libkda: {name} must be on a HIP device, got {t.device}")
+    if t.dim() not in (3, 4):
+        raise ValueError(f"libkda: {name} must be [n,H,d] or [B,T,H,d]")
+    H, d = t.shape[-2:]
+    st = t.stride()
+    n = t.shape[0] if t.dim() == 3 else t.shape[0] * t.shape[1]
+    if n and ((d > 1 and st[-1] != 1) or (H > 1 and st[-2] != d)):
+        raise ValueError(f"libkda: the heads of a token of {name} must be dense")
+    row = st[-3]
+    if t.dim() == 4:
+        if t.shape[1] == 1:
+            row = st[0]
+        elif t.shape[0] > 1 and n and st[0] != t.shape[1] * row:
+            raise ValueError(f"libkda: the token rows of {name} must be evenly spaced")
+    return n, H, d, row
+
+
+def kda_qk_norm(q, k=None, *, norm: str = "l2", q_weight=None, k_weight=None, eps: float = 1e-6, q_scale: float = 1.0,
+                positions=None, inv_freq=None, pairing: str = "halves", q_out=None, k_out=None, out_dtype=None,
+                stream=None):
+    """Queries and keys normalised for each head, and rotated by position: ``(q_out, k_out)``.
+
+    q: [n,H_q,d] or [B,T,H_q,d], k: the same with H_k heads, or None (bf16 or fp32, same dtype; token rows
+    may be slices of wider rows, the heads of a token are dense).  ``norm``: "l2" divides by
+    sqrt(sum x^2 + eps), "rms" by sqrt(mean x^2 + eps); ``q_weight``, ``k_weight``: [d] fp32 factors.  With
+    ``inv_freq`` ([rot/2] fp32) the first rot values of each head turn by ``positions`` ([tokens] int32) times
+    inv_freq, in pairs (i, i + rot/2) ("halves") or (2i, 2i + 1) ("pairs").  Queries are multiplied by ``q_scale``
+    at the end.  The outputs are dense in ``out_dtype`` (the inputs' by default) unless given; each may be its
+    input."""
+    n, Hq, d, qs = _head_rows(q, "q")
+    dev = q.device
+    if norm not in _NORMS or pairing not in _PAIRINGS:
+        raise ValueError('libkda: norm is "l2" or "rms", pairing "halves" or "pairs"')
+    Hk, ks = 0, 0
+    if k is not None:
+        nk, Hk, dk, ks = _head_rows(k, "k")
+        if nk != n or dk != d or k.dtype != q.dtype or k.device != dev or k.shape[:-2] != q.shape[:-2]:
+            raise ValueError("libkda: q and k must agree in tokens, head size, dtype and device")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _check(w, name, torch.float32, dev)
+            if w.shape != (d,):
+                raise ValueError(f"libkda: {name} must be [d]")
+    rot = 0
+    if inv_freq is not None:
+        _check(inv_freq, "inv_freq", torch.float32, dev)
+        rot = 2 * inv_freq.numel()
+    if rot:
+        if positions is None:
+            raise ValueError("libkda: a rotation needs positions")
+        _check(positions, "positions", torch.int32, dev)
+        if positions.numel() != n:
+            raise ValueError("libkda: positions must have one entry per token")
+    out_dtype = out_dtype or (q_out.dtype if q_out is not None else q.dtype)
+    outs, strides = [], []
+    for x, o, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+        if x is None:
+            outs.append(None)
+            strides.append(0)
+            continue
+        if o is None:
+            o = torch.empty(x.shape, dtype=out_dtype, device=dev)
+        elif o.shape != x.shape or o.dtype != out_dtype or o.device != dev:
+            raise ValueError(f"libkda: {name} must be shaped like its input, in the output dtype, on its device")
+        outs.append(o)
+        strides.append(_head_rows(o, name)[3])
+    _run("kda_qk_norm", dev, stream, q.data_ptr(), qs, _dp(k), ks, _dtype_code(q), _NORMS[norm], _dp(q_weight),
+         _dp(k_weight), float(eps), float(q_scale), _dp(positions) if rot else None, _dp(inv_freq) if rot else None, rot,
+         _PAIRINGS[pairing], outs[0].data_ptr(), strides[0], _dp(outs[1]), strides[1], _dtype_code(outs[0]), n, Hq, Hk, d)
+    return outs[0], outs[1]
+
+
+def _table(table, ref):
+    _check(table, "table", torch.int32)
+    _check(ref, "ref", torch.int32, table.device)
+    if table.dim() != 2 or ref.dim() != 1:
+        raise ValueError("libkda: table must be [n_rows,width] and ref [n_pages]")
+    return table.device, table.shape[0], table.shape[1], ref.shape[0]
+
+
+def _move_list(moves, n_moves, room, dev):
+    if moves is None:
+        moves = torch.empty(max(room, 1), 2, dtype=torch.int32, device=dev)
+    else:
+        _check(moves, "moves", torch.int32, dev)
+        if moves.dim() != 2 or moves.shape[1] != 2 or moves.shape[0] < room:
+            raise ValueError(f"libkda: moves must be [.,2] with room for {room} pairs")
+    if n_moves is None:
+        n_moves = torch.empty(1, dtype=torch.int32, device=dev)
+    else:
+        _int_list(n_moves, "n_moves", dev, (1,))
+    return moves, n_moves
+
+
+def kda_cache_fork(table, ref, parents, children, n_private: int = 1, *, moves=None, n_moves=None, stream=None):
+    """Rows ``children`` of the page table become copies of rows ``parents`` (-1: empty rows), in place: the
+    first ``n_private`` entries on free pages of their own, the others shared.  Returns ``(moves, n_moves)``, the
+    page copies that ``kda_cache_copy`` has to carry out on each pool.  table: [n_rows,width] int32; ref:
+    [n_pages] int32; parents, children: [n] int32 on the device.  A fork that cannot be served (no free pages
+    left, the child's row in use) leaves the child's row as it was."""
+    dev, R, W, P = _table(table, ref)
+    n = children.shape[0] if isinstance(children, torch.Tensor) and children.dim() == 1 else -1
+    _int_list(children, "children", dev, (n,))
+    _int_list(parents, "parents", dev, (n,))
+    moves, n_moves = _move_list(moves, n_moves, n * max(int(n_private), 0), dev)
+    _run("kda_cache_fork", dev, stream, table.data_ptr(), ref.data_ptr(), parents.data_ptr(), children.data_ptr(),
+         moves.data_ptr(), n_moves.data_ptr(), n, int(n_private), R, W, P)
+    return moves, n_moves
+
+
+def kda_cache_free(table, ref, rows, *, stream=None):
+    """The rows listed ([n] int32 on the device) hold nothing any more; their pages' refs are counted down."""
+    dev, R, W, P = _table(table, ref)
+    _check(rows, "rows", torch.int32, dev)
+    _run("kda_cache_free", dev, stream, table.data_ptr(), ref.data_ptr(), rows.data_ptr(), rows.numel(), R, W, P)
+
+
+def kda_cache_compact(table, ref, *, table_out=None, ref_out=None, moves=None, n_moves=None, n_live=None, stream=None):
+    """Packs the pages in use into the lowest ones: ``(table_out, ref_out, moves, n_moves, n_live)``.  Pass
+    ``table_out=table`` and ``ref_out=ref`` for an update in place; ``moves`` (room for n_pages // 2 pairs) is what
+    ``kda_cache_copy`` has to carry out on each pool."""
+    dev, R, W, P = _table(table, ref)
+    table_out = torch.empty_like(table) if table_out is None else table_out
+    ref_out = torch.empty_like(ref) if ref_out is None else ref_out
+    _int_list(table_out, "table_out", dev, (R, W))
+    _int_list(ref_out, "ref_out", dev, (P,))
+    moves, n_moves = _move_list(moves, n_moves, P // 2, dev)
+    if n_live is None:
+        n_live = torch.empty(1, dtype=torch.int32, device=dev)
+    else:
+        _int_list(n_live, "n_live", dev, (1,))
+    _run("kda_cache_compact", dev, stream, table.data_ptr(), ref.data_ptr(), table_out.data_ptr(), ref_out.data_ptr(),
+         moves.data_ptr(), n_moves.data_ptr(), n_live.data_ptr(), R, W, P)
+    return table_out, ref_out, moves, n_moves, n_live
+
+
+def kda_cache_copy(pool, moves, n_moves=None, *, src=None, n_layers=None, stream=None):
+    """Page ``moves[i, 1]`` of ``pool`` becomes a copy of page ``moves[i, 0]`` of ``src`` (default: of the pool
+    itself; -1: zeros), for the first ``n_moves`` ([1] int32 on the device; default: all) pairs.  A pool is
+    [n_pages, ...], or [n_layers, n_pages, ...] with ``n_layers`` given; any dtype.  Returns ``pool``."""
+    _check(pool, "pool")
+    dev = pool.device
+    src = pool if src is None else src
+    _check(src, "src", pool.dtype, dev)
+    lead = 1 if n_layers is None else 2
+    L = 1 if n_layers is None else int(n_layers)
+    if pool.dim() <= lead - 1 or src.dim() != pool.dim() or src.shape[lead:] != pool.shape[lead:] or (
+            lead == 2 and (pool.shape[0] != L or src.shape[0] != L)):
+        raise ValueError("libkda: pool and src must be [n_pages,...], or [n_layers,n_pages,...] with n_layers, of one page shape")
+    _check(moves, "moves", torch.int32, dev)
+    if moves.dim() != 2 or moves.shape[1] != 2:
+        raise ValueError("libkda: moves must be [.,2]")
+    if n_moves is not None:
+        _int_list(n_moves, "n_moves", dev, (1,))
+    page = pool.element_size()
+    for m in pool.shape[lead:]:
+        page *= m
+    _run("kda_cache_copy", dev, stream, src.data_ptr(), pool.data_ptr(), page, L, src.shape[lead - 1], pool.shape[lead - 1],
+         moves.data_ptr(), _dp(n_moves), moves.shape[0])
+    return pool
+
+
+def _state_pool(pool, H, dk, dv, dev):
+    _check(pool, "pool", torch.float32, dev)
+    if pool.dim() != 4 or pool.shape[1:] != (H, dk, dv):
+        raise ValueError("libkda: pool must be [n_pages,H,d_k,d_v]")
+    return pool.shape[0]
+
+
+def kda_decode_step_paged(q, k, v, alpha, beta, pool, pages_in, pages_out=None, *, z=None, A=None, o=None,
+                          o_dtype=torch.float32, stream=None):
+    """Decode one token per (sequence, head) on a pool of state pages: the state on page ``pages_in[b]`` of
+    ``pool`` ([n_pages,H,d_k,d_v] fp32) goes to page ``pages_out[b]`` (default: the same page).  ``alpha`` None: the
+    gate inputs z and A of ``kda_decode_step_gated``.  A sequence whose page is out of range (padding: -1), or is
+    written by another sequence of the call, is passed over: its row of ``o`` and the pool are left as they were.
+    Returns ``o``."""
+    _check(q, "q")
+    dev = q.device
+    for t, n in ((k, "k"), (v, "v")):
+        _check(t, n, q.dtype, dev)
+    _check(beta, "beta", torch.float32, dev)
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("libkda: decode q/k/v must be [B,H,d]")
+    B, H, dk = q.shape
+    dv = v.shape[-1]
+    if alpha is not None:
+        if z is not None or A is not None:
+            raise ValueError("libkda: give alpha, or z and A")
+        _check(alpha, "alpha", torch.float32, dev)
+    else:
+        _check(z, "z", q.dtype, dev)
+        _check(A, "A", torch.float32, dev)
+        if A.shape != (H,):
+            raise ValueError("libkda: A must be [H]")
+    gate = alpha if alpha is not None else z
+    if k.shape != q.shape or gate.shape != q.shape or v.shape[:2] != (B, H) or beta.shape != (B, H):
+        raise ValueError("libkda: inconsistent shapes")
+    P = _state_pool(pool, H, dk, dv, dev)
+    _int_list(pages_in, "pages_in", dev, (B,))
+    if pages_out is not None:
+        _int_list(pages_out, "pages_out", dev, (B,))
+    if o is None:
+        o = torch.empty(B, H, dv, device=dev, dtype=o_dtype)
+    else:
+        _check(o, "o", None, dev)
+        if o.shape != (B, H, dv):
+            raise ValueError("libkda: o must be [B,H,d_v]")
+    _run("kda_decode_step_paged", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), _dp(alpha), _dp(z),
+         _dp(A), beta.data_ptr(), pool.data_ptr(), P, pages_in.data_ptr(), _dp(pages_out), o.data_ptr(), _dtype_code(o),
+         B, H, dk, dv)
+    return o
+
+
+def kda_tree_verify(q, k, v, alpha, beta, pool, pages, parents, n_nodes=None, *, o=None, u=None, o_dtype=torch.float32,
+                    stream=None):
+    """Run a tree of drafted tokens against each sequence's state without changing it: ``(o, u)``.
+
+    q, k: [B,K,H,d_k]; v: [B,K,H,d_v]; alpha: [B,K,H,d_k]; beta: [B,K,H]; pool: [n_pages,H,d_k,d_v] fp32, ``pages``
+    [B] int32 the page of each sequence (None: page b).  ``parents`` [B,K] int32: the node that node t follows (its
+    index is smaller), -1 for the state itself; ``n_nodes`` [B] int32: how many nodes each tree has (None: K).  o:
+    [B,K,H,d_v], the output after the path to each node; u: [B,H,K,d_v] fp32, what ``kda_tree_commit`` needs.  Rows
+    behind a tree's last node, and those of a sequence whose page is out of range, are left as they were."""
+    _check(q, "q")
+    dev = q.device
+    for t, n in ((k, "k"), (v, "v")):
+        _check(t, n, q.dtype, dev)
+    _check(alpha, "alpha", torch.float32, dev)
+    _check(beta, "beta", torch.float32, dev)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("libkda: draft q/k/v must be [B,K,H,d]")
+    B, K, H, dk = q.shape
+    dv = v.shape[-1]
+    if k.shape != q.shape or alpha.shape != q.shape or v.shape[:3] != q.shape[:3] or beta.shape != (B, K, H):
+        raise ValueError("libkda: inconsistent shapes")
+    P = _state_pool(pool, H, dk, dv, dev)
+    if pages is not None:
+        _int_list(pages, "pages", dev, (B,))
+    _int_list(parents, "parents", dev, (B, K))
+    if n_nodes is not None:
+        _int_list(n_nodes, "n_nodes", dev, (B,))
+    if o is None:
+        o = torch.empty(B, K, H, dv, device=dev, dtype=o_dtype)
+    else:
+        _check(o, "o", None, dev)
+        if o.shape != (B, K, H, dv):
+            raise ValueError("libkda: o must be [B,K,H,d_v]")
+    if u is None:
+        u = torch.empty(B, H, K, dv, device=dev, dtype=torch.float32)
+    else:
+        _check(u, "u", torch.float32, dev)
+        if u.shape != (B, H, K, dv):
+            raise ValueError("libkda: u must be [B,H,K,d_v]")
+    _run("kda_tree_verify", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), alpha.data_ptr(),
+         beta.data_ptr(), pool.data_ptr(), P, _dp(pages), parents.data_ptr(), _dp(n_nodes), o.data_ptr(), _dtype_code(o),
+         u.data_ptr(), B, K, H, dk, dv)
+    return o, u
+
+
+def kda_tree_commit(k, alpha, u, parents, last, pool, pages_in, pages_out=None, n_nodes=None, *, stream=None):
+    """Advance each sequence's state over the accepted path of its tree: page ``pages_out[b]`` (default: the same
+    page) receives the state after the nodes from the root to ``last[b]`` ([B] int32; out of range: nothing was
+    accepted), from the state on page ``pages_in[b]`` (None: page b).  k, alpha, parents, n_nodes: the arguments
+    of ``kda_tree_verify``; u: its output.  Pages out of range or shared are treated as
+    ``kda_decode_step_paged`` does.  Returns ``pool``."""
+    _check(k, "k")
+    dev = k.device
+    _check(alpha, "alpha", torch.float32, dev)
+    _check(u, "u", torch.float32, dev)
+    if k.dim() != 4 or u.dim() != 4:
+        raise ValueError("libkda: draft k must be [B,K,H,d_k] and u [B,H,K,d_v]")
+    B, K, H, dk = k.shape
+    dv = u.shape[-1]
+    if alpha.shape != k.shape or u.shape != (B, H, K, dv):
+        raise ValueError("libkda: inconsistent shapes")
+    P = _state_pool(pool, H, dk, dv, dev)
+    _int_list(parents, "parents", dev, (B, K))
+    _int_list(last, "last", dev, (B,))
+    for t, n in ((n_nodes, "n_nodes"), (pages_in, "pages_in"), (pages_out, "pages_out")):
+        if t is not None:
+            _int_list(t, n, dev, (B,))
+    _run("kda_tree_commit", dev, stream, k.data_ptr(), _dtype_code(k), alpha.data_ptr(), u.data_ptr(), parents.data_ptr(),
+         _dp(n_nodes), last.data_ptr(), pool.data_ptr(), P, _dp(pages_in), _dp(pages_out), B, K, H, dk, dv)
+    return pool

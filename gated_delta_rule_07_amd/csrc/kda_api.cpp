@@ -11,50 +11,16 @@
 #include <mutex>
 
 #include "../../include/kda.h"
+#include "kda_check.h"
 #include "kda_launch.h"
 
 namespace {
 
+using namespace kda::check;
+
 thread_local int g_last_hip_error = 0;
 
-constexpr int kVersion = 200;  // 0.2.0
-
-bool dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
-
-// A C caller may pass any int where the header says kda_dtype or kda_status;
-// reading such a value as the C++ enum type is undefined, so it is read as the
-// integer it is.
-// (Taken by reference: passing it by value would already read it as the enum.)
-template <typename E>
-int raw_enum(const E& e) {
-  static_assert(sizeof(E) == sizeof(int), "enum size");
-  int v;
-  memcpy(&v, &e, sizeof v);
-  return v;
-}
-bool dtype_ok(int d) { return d == KDA_F32 || d == KDA_BF16; }
-int io_of(int d) { return d == KDA_BF16 ? 1 : 0; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Span {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-Span span(const void* p, size_t bytes) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Span{a, a + bytes};
-}
-bool overlap(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
-
-// Element counts fit in size_t and every row index used by the kernels fits in
-// an int64; the kernels index tokens with 64-bit arithmetic.
-bool sizes_ok(long long B, long long T, long long H, long long dk, long long dv) {
-  const long long lim = (1LL << 40);
-  if (B * H > (1LL << 26)) return false;
-  if (B * T * H > lim / 128) return false;
-  (void)dk;
-  (void)dv;
-  return true;
-}
+constexpr int kVersion = 300;  // 0.3.0
 
 // Prefill kernel choice.  bf16 q/k/v with d_k in {64,128}, d_v % 32 == 0 and
 // chunk 32 or 64 run 32-token chunks: by the two-stage prefill (chunk records
@@ -356,6 +322,10 @@ hipError_t scratch_of_current_device(void** out) {
 }
 
 }  // namespace
+
+namespace kda {
+void set_last_hip_error(int e) { g_last_hip_error = e; }
+}  // namespace kda
 
 extern "C" {
 

@@ -15,6 +15,10 @@
 // rows); the two reductions over rows run in registers, then across lanes with
 // cross-lane shuffles and across waves through LDS.  No matrix cores: the
 // products are matrix-vector shaped.
+//
+// Paged: the same step with each sequence's state read from one page of a pool
+// and written to another (or the same).  A sequence without a valid page, or
+// whose pages another sequence writes, leaves the pool and its row of o alone.
 #include "kda_device.h"
 #include "kda_launch.h"
 
@@ -61,12 +65,13 @@ __device__ __forceinline__ void store4<__bf16>(__bf16* p, const float (&f)[4]) {
   *reinterpret_cast<bf16x4*>(p) = h;
 }
 
-template <typename IO, int DK, int DV>
+template <typename IO, int DK, int DV, bool PAGED>
 __global__ __launch_bounds__(256) void kda_decode_kernel(DecodeParams p) {
   using C = DCfg<DK, DV>;
   __shared__ float sk[DK], sq[DK], sa[DK];
   __shared__ f32x4 sred[C::NW][C::NCG][2];
   __shared__ float skq[C::NW];
+  __shared__ int srace[C::NW];
   const int tid = threadIdx.x;
   const int bh = blockIdx.x;
   const int cg = tid % C::NCG, rg = tid / C::NCG;
@@ -74,7 +79,17 @@ __global__ __launch_bounds__(256) void kda_decode_kernel(DecodeParams p) {
   const IO* k = static_cast<const IO*>(p.k) + (size_t)bh * DK;
   const IO* v = static_cast<const IO*>(p.v) + (size_t)bh * DV;
   const float* alpha = p.alpha + (size_t)bh * DK;
-  float* S = p.S + (size_t)bh * DK * DV;
+  const float* S = p.S + (size_t)bh * DK * DV;
+  float* So = p.S + (size_t)bh * DK * DV;
+  [[maybe_unused]] int b = 0, in = 0, out = 0;
+  if constexpr (PAGED) {
+    b = bh / p.H;
+    in = p.pages_in[b];
+    out = p.pages_out ? p.pages_out[b] : in;
+    if (!page_ok(in, p.n_pages) || !page_ok(out, p.n_pages)) return;
+    S = p.S + ((size_t)in * p.H + bh % p.H) * DK * DV;
+    So = p.S + ((size_t)out * p.H + bh % p.H) * DK * DV;
+  }
 
   // Issue the state stream first: DK/RG float4 loads per thread, all independent.
   // Plain loads and non-temporal stores: measured on the B=256, H=32 workload,
@@ -96,7 +111,18 @@ __global__ __launch_bounds__(256) void kda_decode_kernel(DecodeParams p) {
   float vv[4];
   load4<IO>(v + 4 * cg, vv);
   const float beta = p.beta[bh];
+  if constexpr (PAGED) {
+    const bool races = page_races(p.pages_in, p.pages_out, p.n_pages, p.B, b, in, out, tid, C::NT);
+    const bool any = __any(races);
+    if (tid % 64 == 0) srace[tid / 64] = any;
+  }
   __syncthreads();
+  if constexpr (PAGED) {
+    int races = 0;
+#pragma unroll
+    for (int w = 0; w < C::NW; ++w) races |= srace[w];
+    if (races) return;  // (the same for the whole workgroup)
+  }
 
   // Decay rows, then the two row reductions x = Sbar^T k, y = Sbar^T q (and k^T q).
   f32x4 x = (f32x4)0.0f, y = (f32x4)0.0f;
@@ -144,7 +170,7 @@ __global__ __launch_bounds__(256) void kda_decode_kernel(DecodeParams p) {
   for (int r = 0; r < C::RPT; ++r) {
     const int i = rg + C::RG * r;
     const f32x4 nv = s[r] + sk[i] * d;
-    __builtin_nontemporal_store(nv, reinterpret_cast<f32x4*>(S + (size_t)i * DV + 4 * cg));
+    __builtin_nontemporal_store(nv, reinterpret_cast<f32x4*>(So + (size_t)i * DV + 4 * cg));
   }
   if (rg == 0) {
     float ov[4];
@@ -158,7 +184,10 @@ __global__ __launch_bounds__(256) void kda_decode_kernel(DecodeParams p) {
 template <typename IO, int DK, int DV>
 hipError_t launch_one(const DecodeParams& p, hipStream_t s) {
   using C = DCfg<DK, DV>;
-  hipLaunchKernelGGL((kda_decode_kernel<IO, DK, DV>), dim3((unsigned)(p.B * p.H)), dim3(C::NT), 0, s, p);
+  if (p.pages_in)
+    hipLaunchKernelGGL((kda_decode_kernel<IO, DK, DV, true>), dim3((unsigned)(p.B * p.H)), dim3(C::NT), 0, s, p);
+  else
+    hipLaunchKernelGGL((kda_decode_kernel<IO, DK, DV, false>), dim3((unsigned)(p.B * p.H)), dim3(C::NT), 0, s, p);
   return hipGetLastError();
 }
 

@@ -137,7 +137,28 @@ struct DecodeParams {
   int o_f32;
   const void* z;  // fused gate (see PrefillParams); null: alpha is given
   const float* A;
+  // Paged: S is a pool of n_pages states [H][dk][dv]; sequence b's state is read
+  // from page pages_in[b] and written to page pages_out[b] (null: the same page).
+  const int* pages_in;
+  const int* pages_out;
+  int n_pages;
 };
+
+// The pages of one sequence of a call that writes pages, and one thread's share
+// of the check whether another sequence of the call would race with it: `step`
+// threads of a workgroup each look at the sequences `first`, first + step, ...
+// A sequence whose page (read or written) another one with valid pages writes
+// is not run.
+__device__ __forceinline__ bool page_ok(int page, int n_pages) { return page >= 0 && page < n_pages; }
+__device__ __forceinline__ bool page_races(const int* pages_in, const int* pages_out, int n_pages, int B, int b, int in,
+                                           int out, int first, int step) {
+  bool races = false;
+  for (int j = first; j < B; j += step) {
+    const int ij = pages_in ? pages_in[j] : j, oj = pages_out ? pages_out[j] : ij;
+    races |= j != b && page_ok(ij, n_pages) && page_ok(oj, n_pages) && (oj == in || oj == out);
+  }
+  return races;
+}
 
 // io_dtype: 0 = fp32, 1 = bf16.  `slab` is the number of state columns one
 // workgroup owns (16, 32 or 64).  Returns hipErrorInvalidValue when no kernel is
@@ -229,6 +250,93 @@ struct CommitParams {
 bool spec_supported(int io_dtype, int dk, int dv);
 hipError_t launch_verify(const VerifyParams& p, int io_dtype, hipStream_t s);
 hipError_t launch_commit(const CommitParams& p, int io_dtype, hipStream_t s);
+
+// Trees of drafted tokens over a pool of state pages.
+constexpr int kMaxTree = 64;
+struct TreeParams {
+  const void* q;  // [B][K][H][dk]
+  const void* k;
+  const void* v;  // [B][K][H][dv]
+  const float* alpha;
+  const float* beta;  // [B][K][H]
+  const float* pool;  // [n_pages][H][dk][dv]
+  const int* pages;    // [B]; null: page b
+  const int* parents;  // [B][K]
+  const int* n_nodes;  // [B]; null: K
+  void* o;             // [B][K][H][dv]
+  float* u;            // [B][H][K][dv]
+  int n_pages, B, K, H, dk, dv;
+  int o_f32;
+};
+struct TreeCommitParams {
+  const void* k;  // [B][K][H][dk]
+  const float* alpha;
+  const float* u;       // [B][H][K][dv]
+  const int* parents;   // [B][K]
+  const int* n_nodes;   // [B]; null: K
+  const int* last;      // [B]
+  float* pool;          // [n_pages][H][dk][dv]
+  const int* pages_in;  // [B]; null: page b
+  const int* pages_out;  // [B]; null: pages_in
+  int n_pages, B, K, H, dk, dv;
+};
+bool tree_supported(int io_dtype, int dk, int dv);
+hipError_t launch_tree_verify(const TreeParams& p, int io_dtype, hipStream_t s);
+hipError_t launch_tree_commit(const TreeCommitParams& p, int io_dtype, hipStream_t s);
+
+// Norms of queries and keys for each head, with rotation.
+struct HeadsParams {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  long long q_stride, k_stride, q_out_stride, k_out_stride;  // elements between tokens
+  const float* q_weight;  // [d] or null
+  const float* k_weight;
+  const int* positions;   // [n] (rot > 0)
+  const float* inv_freq;  // [rot / 2]
+  float eps, q_scale;
+  int rms, adjacent, rot;
+  int n, Hq, Hk, d;
+};
+hipError_t launch_heads(const HeadsParams& p, int io_dtype, int out_dtype, hipStream_t s);
+
+// The cache of state pages: tables, reference counts and move lists.
+constexpr int kMaxPages = 65536, kMaxForks = 1024, kMaxPagedSeqs = 4096;
+struct ForkParams {
+  int* table;  // [n_rows][width]
+  int* ref;    // [n_pages]
+  const int* parents;
+  const int* children;
+  int* moves;  // [n * n_private][2]
+  int* n_moves;
+  int n, n_private, n_rows, width, n_pages;
+};
+struct CompactParams {
+  const int* table;
+  const int* ref;
+  int* table_out;
+  int* ref_out;
+  int* moves;  // [n_pages / 2][2]
+  int* n_moves;
+  int* n_live;
+  int n_rows, width, n_pages;
+};
+struct CopyParams {
+  const char* src;
+  char* dst;
+  size_t page_bytes;
+  int n_layers, n_src, n_dst;
+  const int* moves;
+  const int* n_moves;  // null: max_moves
+  int max_moves;
+  int same;            // src and dst are one pool
+};
+hipError_t launch_cache_fork(const ForkParams& p, hipStream_t s);
+hipError_t launch_cache_free(int* table, int* ref, const int* rows, int n, int n_rows, int width, int n_pages,
+                             hipStream_t s);
+hipError_t launch_cache_compact(const CompactParams& p, hipStream_t s);
+hipError_t launch_cache_copy(const CopyParams& p, hipStream_t s);
 
 bool decode_supported(int io_dtype, int dk, int dv);
 hipError_t launch_decode(const DecodeParams& p, int io_dtype, hipStream_t s);

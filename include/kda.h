@@ -351,6 +351,225 @@ kda_status kda_decode_commit(const void* k, kda_dtype qkv_dtype, const float* al
                              const int* n_accept, float* S,
                              int B, int K, int H, int d_k, int d_v, hipStream_t stream);
 
+/* ---- norms of queries and keys ------------------------------------------------------- */
+
+typedef enum {
+  KDA_NORM_L2 = 0, /* x / sqrt(sum_i x_i^2 + eps) */
+  KDA_NORM_RMS = 1 /* x / sqrt(mean_i x_i^2 + eps) */
+} kda_norm;
+
+typedef enum {
+  KDA_PAIR_HALVES = 0, /* values i and i + rot/2 turn together */
+  KDA_PAIR_ADJACENT = 1 /* values 2i and 2i + 1 turn together */
+} kda_pairing;
+
+/*
+ * Normalises queries and keys for each token and head and, where asked, turns
+ * their first `rot` values by the token's position, in one pass: what a layer
+ * does to its projections before kda_chunk_fwd or kda_decode_step read them
+ * (those calls take keys as they are given).  For a query or key x of one head,
+ *     y = w . x / sqrt(sum_i x_i^2 + eps)           (KDA_NORM_RMS: the mean)
+ *     (a, b) -> (a cos f - b sin f, b cos f + a sin f),  f = pos * inv_freq[i],
+ *                                                    for the rot/2 pairs i
+ * and queries are then multiplied by q_scale.  Norms, weights and rotation are
+ * formed in fp32, the angle f and its reduction in fp64 (so far positions keep
+ * their precision), and the result is rounded once to the output's type.
+ *
+ *   q          : n rows of H_q heads of d values, dtype; row t starts at q + t * q_stride
+ *   k          : n rows of H_k heads of d values, dtype, k_stride apart (NULL when H_k = 0)
+ *                (strides in elements: rows may be slices of a fused projection's rows;
+ *                heads and values inside a row are dense)
+ *   q_weight, k_weight: [d] fp32, or NULL for ones                     (read)
+ *   eps        : finite and >= 0.  With eps = 0 a head of zeros gives NaN.
+ *   positions  : [n] int32, any value; inv_freq: [rot / 2] fp32         (read)
+ *                (both NULL when rot = 0)
+ *   rot        : a multiple of 16 in [0, d]
+ *   q_out, k_out: as q and k, with q_out_stride and k_out_stride, out_dtype (written)
+ *   d          : a multiple of 8 in [8, 256];  H_q >= 1, H_k >= 0;  n >= 0 (0: nothing is done)
+ *
+ * Pointers are 16-byte aligned and row strides a multiple of 16 bytes
+ * (KDA_ERR_MISALIGNED), at least H * d elements unless n <= 1 (KDA_ERR_SHAPE).
+ * q_out may be q itself with the same stride and type, and so may k_out be k;
+ * any other common byte of an output and another array is KDA_ERR_ALIAS (rows
+ * that lie between each other's without touching, as in a fused projection, are
+ * fine).  Unknown norm, pairing or dtype: KDA_ERR_DTYPE; d or rot as above:
+ * KDA_ERR_UNSUPPORTED; eps: KDA_ERR_SHAPE.  The sum of squares is formed in
+ * fp32: |x| should stay below 1e18.
+ */
+kda_status kda_qk_norm(const void* q, long long q_stride, const void* k, long long k_stride, kda_dtype dtype,
+                       kda_norm norm, const float* q_weight, const float* k_weight, float eps, float q_scale,
+                       const int* positions, const float* inv_freq, int rot, kda_pairing pairing,
+                       void* q_out, long long q_out_stride, void* k_out, long long k_out_stride,
+                       kda_dtype out_dtype, int n, int H_q, int H_k, int d, hipStream_t stream);
+
+/* ---- a cache of state pages ------------------------------------------------------------
+ *
+ * A server keeps the states of its sequences in a pool of pages, one page per
+ * state of a layer: pool [n_layers][n_pages][page_bytes], where a layer's part
+ * is the [n_pages][H][d_k][d_v] fp32 array that kda_decode_step_paged reads.  A
+ * page's number is the same on every layer.
+ *   table : [n_rows][width] int32, one row per sequence slot of the server: the
+ *           pages it holds.  A row's first n_private entries are states that
+ *           its decode steps write (usually one, the running state); the others
+ *           are recorded states (kda_chunk_fwd_snapshots) that rows may share.
+ *           An entry outside [0, n_pages) holds no page; the calls write -1.
+ *   ref   : [n_pages] int32, how many entries hold each page; a page with
+ *           ref <= 0 is free.
+ *   moves : [.][2] int32, (source page, destination page) pairs, and *n_moves,
+ *           their number: what kda_cache_copy then carries out on a pool.  A
+ *           source of -1 stands for zeros.
+ * All of these are DEVICE arrays; entries out of range never make a kernel
+ * access memory out of range.  The calls change only the arrays named as
+ * written, in stream order, and can be captured into a graph and replayed.
+ * Two calls that write the same table, ref or pool must be ordered by the
+ * caller.  n_rows, width >= 1 and n_rows * width <= 2^26, else KDA_ERR_SHAPE.
+ */
+
+#define KDA_MAX_PAGES 65536       /* most pages of a pool */
+#define KDA_MAX_FORKS 1024        /* most rows one kda_cache_fork call starts */
+#define KDA_MAX_PAGED_SEQS 4096   /* most sequences of one call on pages that writes pages */
+
+/*
+ * Starts rows as copies of others (several samples of one prompt, a beam's
+ * survivors) or anew.  For fork i, row children[i] of the table becomes a copy
+ * of row parents[i] as it was before the call: each page in the parent's first
+ * n_private entries is replaced by a free page, lowest first, and listed in
+ * moves; the other pages are shared.  parents[i] = -1 starts an empty row: its
+ * first n_private entries get free pages with a source of -1 in moves (zeros),
+ * the others -1.  Every page's ref counts the entries that came to hold it.
+ *
+ *   table, ref       : as above                                   (updated in place)
+ *   parents, children: [n] int32, 0 <= n <= KDA_MAX_FORKS         (read)
+ *   n_private        : 0 .. width
+ *   moves            : room for n * n_private pairs, n_moves: [1]  (written; what
+ *                      moves holds past *n_moves is unspecified)
+ *
+ * Forks are served in order while free pages last: the first fork whose pages
+ * are not there, and every later one, leaves its child's row as it was.  So
+ * does a fork whose child's row holds a page (or lies out of range), whose
+ * parent is neither -1 nor a row, or whose child an earlier fork names.
+ */
+kda_status kda_cache_fork(int* table, int* ref, const int* parents, const int* children, int* moves, int* n_moves,
+                          int n, int n_private, int n_rows, int width, int n_pages, hipStream_t stream);
+
+/*
+ * Ends rows: each entry of the rows listed becomes -1 and its page's ref is
+ * counted down (never below 0).  rows: [n] int32, n >= 0; a row out of range is
+ * passed over, a row listed twice is freed once.  No page is touched.
+ */
+kda_status kda_cache_free(int* table, int* ref, const int* rows, int n, int n_rows, int width, int n_pages,
+                          hipStream_t stream);
+
+/*
+ * Packs the pool: with n_live pages in use (ref > 0), each of them above n_live
+ * moves to a free page below it, the lowest to the lowest, so that pages
+ * [n_live, n_pages) are free and their memory can be handed back once
+ * kda_cache_copy has carried out moves.
+ *
+ *   table, ref        : as above                                        (read)
+ *   table_out, ref_out: the table and refs after the moves; each may be its input
+ *                       (in place).  Entries that held a free page become -1.  Until
+ *                       the moves run, and after, the old table's pages that moved
+ *                       still hold their states.                        (written)
+ *   moves             : room for n_pages / 2 pairs (at least one); n_moves, n_live: [1]
+ *                       (written; moves past *n_moves is unspecified)
+ */
+kda_status kda_cache_compact(const int* table, const int* ref, int* table_out, int* ref_out, int* moves, int* n_moves,
+                             int* n_live, int n_rows, int width, int n_pages, hipStream_t stream);
+
+/*
+ * Carries out the moves on every layer: page `destination` of dst becomes a copy
+ * of page `source` of src, or zeros.  src and dst are pools of n_layers layers
+ * with n_src_pages and n_dst_pages pages of page_bytes bytes (a multiple of 16)
+ * each; they may be the same pool, or share no byte (KDA_ERR_ALIAS).
+ *
+ *   moves   : [max_moves][2] int32, 0 <= max_moves <= KDA_MAX_PAGES  (read)
+ *   n_moves : [1] int32, clamped to [0, max_moves], or NULL for max_moves (read)
+ *
+ * The copies happen at once, in no order.  A move with a page out of range, or
+ * onto its own source, is passed over, and so is every move that would race
+ * with another one: two or more that name one destination, and in one pool a
+ * move whose source is the destination of another one.  Lists written by
+ * kda_cache_fork and kda_cache_compact hold no such move.
+ */
+kda_status kda_cache_copy(const void* src, void* dst, size_t page_bytes, int n_layers, int n_src_pages, int n_dst_pages,
+                          const int* moves, const int* n_moves, int max_moves, hipStream_t stream);
+
+/*
+ * kda_decode_step on pages: one step of the recurrence for each of B sequences,
+ * from the state on page pages_in[b] of the pool to page pages_out[b].
+ *
+ *   q, k, v, beta, o: as kda_decode_step
+ *   alpha    : [B][H][d_k] fp32, or NULL with the gate inputs z ([B][H][d_k] in
+ *              qkv_dtype) and A ([H] fp32) of kda_decode_step_gated; z and A are
+ *              NULL when alpha is given (KDA_ERR_NULL when neither is)
+ *   pool     : [n_pages][H][d_k][d_v] fp32                 (read and written)
+ *   pages_in : [B] int32, DEVICE memory (read)
+ *   pages_out: [B] int32, DEVICE memory (read), or NULL: each state is updated in
+ *              place.  Another page keeps the state before the step as well (a
+ *              fork without a copy of its own).
+ *   B        : 1 .. KDA_MAX_PAGED_SEQS, n_pages: 1 .. KDA_MAX_PAGES
+ *
+ * A sequence with a page outside [0, n_pages) is passed over -- its row of o and
+ * the pool are left as they were -- which is how a captured batch is padded; and
+ * so is, rather than let them race, every sequence that reads or writes a page
+ * that another sequence of the call (with both pages in range) writes.
+ * Results equal kda_decode_step's on the same state bit for bit.
+ */
+kda_status kda_decode_step_paged(const void* q, const void* k, const void* v, kda_dtype qkv_dtype, const float* alpha,
+                                 const void* z, const float* A, const float* beta, float* pool, int n_pages,
+                                 const int* pages_in, const int* pages_out, void* o, kda_dtype o_dtype, int B, int H,
+                                 int d_k, int d_v, hipStream_t stream);
+
+/* ---- trees of drafted tokens ----------------------------------------------------------- */
+
+/* Most nodes of one sequence's tree of drafted tokens. */
+#define KDA_MAX_TREE 64
+
+/*
+ * kda_decode_verify for a tree of drafted tokens, over a cache of state pages:
+ * node t of sequence b follows node parents[b][t], or the sequence's state when
+ * that is -1, and its outputs are those of the recurrence run along its path
+ * from the root.  The state is read once for the whole tree and not changed.
+ *
+ *   q, k   : [B][K][H][d_k] qkv_dtype     v: [B][K][H][d_v] qkv_dtype   (read)
+ *   alpha  : [B][K][H][d_k] fp32          beta: [B][K][H] fp32          (read)
+ *   pool   : [n_pages][H][d_k][d_v] fp32                                (read)
+ *   pages  : [B] int32, DEVICE memory, the page of each sequence's state; NULL:
+ *            page b (a dense [B][H][d_k][d_v] state; n_pages >= B)       (read)
+ *   parents: [B][K] int32, DEVICE memory; -1 <= parents[b][t] < t, any other value
+ *            is taken as -1                                             (read)
+ *   n_nodes: [B] int32, DEVICE memory, the nodes of each tree, clamped to [0, K];
+ *            NULL: K                                                    (read)
+ *   o      : [B][K][H][d_v] o_dtype, o_t along the path to node t     (written)
+ *   u      : [B][H][K][d_v] fp32, the write vectors kda_tree_commit needs (written)
+ *   K      : 1 .. KDA_MAX_TREE;  n_pages: 1 .. KDA_MAX_PAGES
+ *
+ * Rows of o and u behind a tree's last node, and every row of a sequence whose
+ * page lies outside [0, n_pages), are left as they were.  o and u may overlap
+ * nothing else (KDA_ERR_ALIAS).  All arithmetic is fp32; alpha may be any value
+ * in [0, 1].
+ */
+kda_status kda_tree_verify(const void* q, const void* k, const void* v, kda_dtype qkv_dtype, const float* alpha,
+                           const float* beta, const float* pool, int n_pages, const int* pages, const int* parents,
+                           const int* n_nodes, void* o, kda_dtype o_dtype, float* u, int B, int K, int H, int d_k,
+                           int d_v, hipStream_t stream);
+
+/*
+ * Commits the accepted path of each tree: page pages_out[b] receives the state
+ * after the tokens on the path from the root to node last[b] (inclusive), from
+ * the state on page pages_in[b], in one read and one write of it.
+ *
+ *   k, alpha, parents, n_nodes, u: the arguments and output of kda_tree_verify  (read)
+ *   last     : [B] int32, DEVICE memory; a value outside [0, n_nodes[b]) accepts
+ *              nothing (the state as it was)                             (read)
+ *   pool, pages_in, pages_out, B: as kda_decode_step_paged, with its rules for pages
+ *              out of range and shared pages; pages_in NULL: page b (n_pages >= B)
+ */
+kda_status kda_tree_commit(const void* k, kda_dtype qkv_dtype, const float* alpha, const float* u, const int* parents,
+                           const int* n_nodes, const int* last, float* pool, int n_pages, const int* pages_in,
+                           const int* pages_out, int B, int K, int H, int d_k, int d_v, hipStream_t stream);
+
 /* Human-readable text for a status code (static storage; never NULL). */
 const char* kda_status_string(kda_status s);
 
