@@ -511,51 +511,83 @@ def kda_decode_commit(k, alpha, u, n_accept, S, *, stream=None):
 
 _NORMS = {"l2": 0, "rms": 1}
 _PAIRINGS = {"halves": 0, "pairs": 1}
+_CODES = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
+_I32, _F32 = torch.int32, torch.float32
+
+# The calls below serve single tokens too, where a step's time is the time to issue
+# it: their checks read each property of a tensor once, and say what is wrong with
+# it only when something is.
 
 
-def _run(name, dev, stream, *args):
-    """Call `name` of the library on `dev` (made current for the call where it is not)."""
-    fn = getattr(load_library(), name)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        st = fn(*args, stream.cuda_stream)
+def _raw_stream(index):
+    """The current stream of device `index`, as the pointer the C ABI takes."""
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    _raw_stream = torch._C._cuda_getCurrentRawStream  # noqa: F811  (the same, without a Stream object)
+
+
+def _run(name, index, stream, *args):
+    """Call `name` of the library on device `index` (made current for the call where it is not)."""
+    fn = getattr(_lib or load_library(), name)
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        st = fn(*args, s)
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args, stream.cuda_stream)
+        with torch.cuda.device(index):
+            st = fn(*args, s)
     if st != 0:
         raise KdaError(st, name)
 
 
-def _dp(t):
-    return None if t is None else t.data_ptr()
+def _device_of(t, name):
+    """The index of t's device; t has to be a tensor on a HIP device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"libkda: {name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"libkda: {name} must be on a HIP device, got {t.device}")
+    return t.get_device()
 
 
-def _int_list(t, name, dev, shape):
-    _check(t, name, torch.int32, dev)
-    if t.shape != shape:
-        raise ValueError(f"libkda: {name} must be {list(shape)}, got {list(t.shape)}")
+def _need(t, name, dtype, index, shape):
+    """The address of t, which has to be a dense tensor of this dtype and shape on device `index`."""
+    try:
+        if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _check(t, name, dtype, torch.device("cuda", index))
+    raise ValueError(f"libkda: {name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _may(t, name, dtype, index, shape):
+    return None if t is None else _need(t, name, dtype, index, shape)
+
+
+def _io_code(t, name):
+    """kda_dtype of a bf16 or fp32 tensor."""
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"libkda: {name} must be bfloat16 or float32, got {t.dtype}")
+    return code
 
 
 def _head_rows(t, name):
     """(tokens, heads, d, row stride in elements) of [n,H,d] or [B,T,H,d] rows of dense heads."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"libkda: {name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"libkda: {name} must be on a HIP device, got {t.device}")
-    if t.dim() not in (3, 4):
-        raise ValueError(f"libkda: {name} must be [n,H,d] or [B,T,H,d]")
-    H, d = t.shape[-2:]
-    st = t.stride()
-    n = t.shape[0] if t.dim() == 3 else t.shape[0] * t.shape[1]
-    if n and ((d > 1 and st[-1] != 1) or (H > 1 and st[-2] != d)):
-        raise ValueError(f"libkda: the heads of a token of {name} must be dense")
-    row = st[-3]
-    if t.dim() == 4:
-        if t.shape[1] == 1:
-            row = st[0]
-        elif t.shape[0] > 1 and n and st[0] != t.shape[1] * row:
+    shape, st = t.shape, t.stride()
+    if len(shape) == 3:
+        n, H, d = shape
+        row = st[0]
+    elif len(shape) == 4:
+        B, T, H, d = shape
+        n, row = B * T, st[1] if T > 1 else st[0]
+        if B > 1 and T > 1 and st[0] != T * row:
             raise ValueError(f"libkda: the token rows of {name} must be evenly spaced")
+    else:
+        raise ValueError(f"libkda: {name} must be [n,H,d] or [B,T,H,d]")
+    if n and ((st[-1] != 1 and d > 1) or (st[-2] != d and H > 1)):
+        raise ValueError(f"libkda: the heads of a token of {name} must be dense")
     return n, H, d, row
 
 
@@ -567,73 +599,71 @@ def kda_qk_norm(q, k=None, *, norm: str = "l2", q_weight=None, k_weight=None, ep
     q: [n,H_q,d] or [B,T,H_q,d], k: the same with H_k heads, or None (bf16 or fp32, same dtype; token rows
     may be slices of wider rows, the heads of a token are dense).  ``norm``: "l2" divides by
     sqrt(sum x^2 + eps), "rms" by sqrt(mean x^2 + eps); ``q_weight``, ``k_weight``: [d] fp32 factors.  With
-    ``inv_freq`` ([rot/2] fp32) the first rot values of each head turn by ``positions`` ([tokens] int32) times
+    ``inv_freq`` ([rot/2] fp32) the first rot values of each head turn by ``positions`` (one int32 per token) times
     inv_freq, in pairs (i, i + rot/2) ("halves") or (2i, 2i + 1) ("pairs").  Queries are multiplied by ``q_scale``
     at the end.  The outputs are dense in ``out_dtype`` (the inputs' by default) unless given; each may be its
     input."""
+    dev = _device_of(q, "q")
     n, Hq, d, qs = _head_rows(q, "q")
-    dev = q.device
-    if norm not in _NORMS or pairing not in _PAIRINGS:
-        raise ValueError('libkda: norm is "l2" or "rms", pairing "halves" or "pairs"')
-    Hk, ks = 0, 0
+    code = _io_code(q, "q")
+    try:
+        nm, pr = _NORMS[norm], _PAIRINGS[pairing]
+    except (KeyError, TypeError):
+        raise ValueError('libkda: norm is "l2" or "rms", pairing "halves" or "pairs"') from None
+    kp, Hk, ks = None, 0, 0
     if k is not None:
-        nk, Hk, dk, ks = _head_rows(k, "k")
-        if nk != n or dk != d or k.dtype != q.dtype or k.device != dev or k.shape[:-2] != q.shape[:-2]:
+        if _device_of(k, "k") != dev or k.dtype is not q.dtype or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != d:
             raise ValueError("libkda: q and k must agree in tokens, head size, dtype and device")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _check(w, name, torch.float32, dev)
-            if w.shape != (d,):
-                raise ValueError(f"libkda: {name} must be [d]")
-    rot = 0
-    if inv_freq is not None:
-        _check(inv_freq, "inv_freq", torch.float32, dev)
+        _, Hk, _, ks = _head_rows(k, "k")
+        kp = k.data_ptr()
+    qw, kw = _may(q_weight, "q_weight", _F32, dev, (d,)), _may(k_weight, "k_weight", _F32, dev, (d,))
+    rot, pos, freq = 0, None, None
+    if inv_freq is not None and inv_freq.numel():
         rot = 2 * inv_freq.numel()
-    if rot:
+        freq = _need(inv_freq, "inv_freq", _F32, dev, (rot // 2,))
         if positions is None:
             raise ValueError("libkda: a rotation needs positions")
-        _check(positions, "positions", torch.int32, dev)
+        pos = _need(positions, "positions", _I32, dev, positions.shape)
         if positions.numel() != n:
             raise ValueError("libkda: positions must have one entry per token")
-    out_dtype = out_dtype or (q_out.dtype if q_out is not None else q.dtype)
-    outs, strides = [], []
+    if out_dtype is None:
+        out_dtype = q.dtype if q_out is None else q_out.dtype
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=out_dtype, device=q.device)
     for x, o, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
         if x is None:
-            outs.append(None)
-            strides.append(0)
-            continue
-        if o is None:
-            o = torch.empty(x.shape, dtype=out_dtype, device=dev)
-        elif o.shape != x.shape or o.dtype != out_dtype or o.device != dev:
+            if o is not None:
+                raise ValueError("libkda: k_out without k")
+        elif o.dtype is not out_dtype or o.get_device() != dev or o.shape != x.shape:
             raise ValueError(f"libkda: {name} must be shaped like its input, in the output dtype, on its device")
-        outs.append(o)
-        strides.append(_head_rows(o, name)[3])
-    _run("kda_qk_norm", dev, stream, q.data_ptr(), qs, _dp(k), ks, _dtype_code(q), _NORMS[norm], _dp(q_weight),
-         _dp(k_weight), float(eps), float(q_scale), _dp(positions) if rot else None, _dp(inv_freq) if rot else None, rot,
-         _PAIRINGS[pairing], outs[0].data_ptr(), strides[0], _dp(outs[1]), strides[1], _dtype_code(outs[0]), n, Hq, Hk, d)
-    return outs[0], outs[1]
+    qos = _head_rows(q_out, "q_out")[3]
+    kop, kos = (None, 0) if k is None else (k_out.data_ptr(), _head_rows(k_out, "k_out")[3])
+    _run("kda_qk_norm", dev, stream, q.data_ptr(), qs, kp, ks, code, nm, qw, kw, eps, q_scale, pos, freq, rot, pr,
+         q_out.data_ptr(), qos, kop, kos, _io_code(q_out, "q_out"), n, Hq, Hk, d)
+    return q_out, k_out
 
 
 def _table(table, ref):
-    _check(table, "table", torch.int32)
-    _check(ref, "ref", torch.int32, table.device)
-    if table.dim() != 2 or ref.dim() != 1:
+    """(device, n_rows, width, n_pages, addresses of table and ref)."""
+    dev = _device_of(table, "table")
+    if table.dim() != 2 or not isinstance(ref, torch.Tensor) or ref.dim() != 1:
         raise ValueError("libkda: table must be [n_rows,width] and ref [n_pages]")
-    return table.device, table.shape[0], table.shape[1], ref.shape[0]
+    R, W = table.shape
+    P = ref.shape[0]
+    return dev, R, W, P, _need(table, "table", _I32, dev, (R, W)), _need(ref, "ref", _I32, dev, (P,))
 
 
-def _move_list(moves, n_moves, room, dev):
+def _move_list(moves, n_moves, room, t):
+    """moves and n_moves, made on t's device where they are not given, and their addresses."""
+    dev = t.get_device()
     if moves is None:
-        moves = torch.empty(max(room, 1), 2, dtype=torch.int32, device=dev)
-    else:
-        _check(moves, "moves", torch.int32, dev)
-        if moves.dim() != 2 or moves.shape[1] != 2 or moves.shape[0] < room:
-            raise ValueError(f"libkda: moves must be [.,2] with room for {room} pairs")
+        moves = torch.empty(max(room, 1), 2, dtype=_I32, device=t.device)
     if n_moves is None:
-        n_moves = torch.empty(1, dtype=torch.int32, device=dev)
-    else:
-        _int_list(n_moves, "n_moves", dev, (1,))
-    return moves, n_moves
+        n_moves = torch.empty(1, dtype=_I32, device=t.device)
+    mp, np_ = _need(moves, "moves", _I32, dev, (max(moves.shape[0], room), 2)), _need(n_moves, "n_moves", _I32, dev, (1,))
+    return moves, n_moves, mp, np_
 
 
 def kda_cache_fork(table, ref, parents, children, n_private: int = 1, *, moves=None, n_moves=None, stream=None):
@@ -642,39 +672,32 @@ def kda_cache_fork(table, ref, parents, children, n_private: int = 1, *, moves=N
     page copies that ``kda_cache_copy`` has to carry out on each pool.  table: [n_rows,width] int32; ref:
     [n_pages] int32; parents, children: [n] int32 on the device.  A fork that cannot be served (no free pages
     left, the child's row in use) leaves the child's row as it was."""
-    dev, R, W, P = _table(table, ref)
-    n = children.shape[0] if isinstance(children, torch.Tensor) and children.dim() == 1 else -1
-    _int_list(children, "children", dev, (n,))
-    _int_list(parents, "parents", dev, (n,))
-    moves, n_moves = _move_list(moves, n_moves, n * max(int(n_private), 0), dev)
-    _run("kda_cache_fork", dev, stream, table.data_ptr(), ref.data_ptr(), parents.data_ptr(), children.data_ptr(),
-         moves.data_ptr(), n_moves.data_ptr(), n, int(n_private), R, W, P)
+    dev, R, W, P, tp, rp = _table(table, ref)
+    n = children.numel() if isinstance(children, torch.Tensor) else -1
+    cp, pp = _need(children, "children", _I32, dev, (n,)), _need(parents, "parents", _I32, dev, (n,))
+    moves, n_moves, mp, np_ = _move_list(moves, n_moves, n * max(n_private, 0), table)
+    _run("kda_cache_fork", dev, stream, tp, rp, pp, cp, mp, np_, n, n_private, R, W, P)
     return moves, n_moves
 
 
 def kda_cache_free(table, ref, rows, *, stream=None):
     """The rows listed ([n] int32 on the device) hold nothing any more; their pages' refs are counted down."""
-    dev, R, W, P = _table(table, ref)
-    _check(rows, "rows", torch.int32, dev)
-    _run("kda_cache_free", dev, stream, table.data_ptr(), ref.data_ptr(), rows.data_ptr(), rows.numel(), R, W, P)
+    dev, R, W, P, tp, rp = _table(table, ref)
+    n = rows.numel() if isinstance(rows, torch.Tensor) else -1
+    _run("kda_cache_free", dev, stream, tp, rp, _need(rows, "rows", _I32, dev, (n,)), n, R, W, P)
 
 
 def kda_cache_compact(table, ref, *, table_out=None, ref_out=None, moves=None, n_moves=None, n_live=None, stream=None):
     """Packs the pages in use into the lowest ones: ``(table_out, ref_out, moves, n_moves, n_live)``.  Pass
     ``table_out=table`` and ``ref_out=ref`` for an update in place; ``moves`` (room for n_pages // 2 pairs) is what
     ``kda_cache_copy`` has to carry out on each pool."""
-    dev, R, W, P = _table(table, ref)
+    dev, R, W, P, tp, rp = _table(table, ref)
     table_out = torch.empty_like(table) if table_out is None else table_out
     ref_out = torch.empty_like(ref) if ref_out is None else ref_out
-    _int_list(table_out, "table_out", dev, (R, W))
-    _int_list(ref_out, "ref_out", dev, (P,))
-    moves, n_moves = _move_list(moves, n_moves, P // 2, dev)
-    if n_live is None:
-        n_live = torch.empty(1, dtype=torch.int32, device=dev)
-    else:
-        _int_list(n_live, "n_live", dev, (1,))
-    _run("kda_cache_compact", dev, stream, table.data_ptr(), ref.data_ptr(), table_out.data_ptr(), ref_out.data_ptr(),
-         moves.data_ptr(), n_moves.data_ptr(), n_live.data_ptr(), R, W, P)
+    n_live = torch.empty(1, dtype=_I32, device=table.device) if n_live is None else n_live
+    to, ro = _need(table_out, "table_out", _I32, dev, (R, W)), _need(ref_out, "ref_out", _I32, dev, (P,))
+    moves, n_moves, mp, np_ = _move_list(moves, n_moves, max(P // 2, 1), table)
+    _run("kda_cache_compact", dev, stream, tp, rp, to, ro, mp, np_, _need(n_live, "n_live", _I32, dev, (1,)), R, W, P)
     return table_out, ref_out, moves, n_moves, n_live
 
 
@@ -682,33 +705,26 @@ def kda_cache_copy(pool, moves, n_moves=None, *, src=None, n_layers=None, stream
     """Page ``moves[i, 1]`` of ``pool`` becomes a copy of page ``moves[i, 0]`` of ``src`` (default: of the pool
     itself; -1: zeros), for the first ``n_moves`` ([1] int32 on the device; default: all) pairs.  A pool is
     [n_pages, ...], or [n_layers, n_pages, ...] with ``n_layers`` given; any dtype.  Returns ``pool``."""
-    _check(pool, "pool")
-    dev = pool.device
+    dev = _device_of(pool, "pool")
     src = pool if src is None else src
-    _check(src, "src", pool.dtype, dev)
-    lead = 1 if n_layers is None else 2
-    L = 1 if n_layers is None else int(n_layers)
-    if pool.dim() <= lead - 1 or src.dim() != pool.dim() or src.shape[lead:] != pool.shape[lead:] or (
-            lead == 2 and (pool.shape[0] != L or src.shape[0] != L)):
+    _device_of(src, "src")
+    lead, L = (1, 1) if n_layers is None else (2, n_layers)
+    shape, other = pool.shape, src.shape
+    if len(shape) < lead or other[lead:] != shape[lead:] or len(other) != len(shape) or (
+            lead == 2 and (shape[0] != L or other[0] != L)):
         raise ValueError("libkda: pool and src must be [n_pages,...], or [n_layers,n_pages,...] with n_layers, of one page shape")
-    _check(moves, "moves", torch.int32, dev)
-    if moves.dim() != 2 or moves.shape[1] != 2:
-        raise ValueError("libkda: moves must be [.,2]")
-    if n_moves is not None:
-        _int_list(n_moves, "n_moves", dev, (1,))
-    page = pool.element_size()
-    for m in pool.shape[lead:]:
-        page *= m
-    _run("kda_cache_copy", dev, stream, src.data_ptr(), pool.data_ptr(), page, L, src.shape[lead - 1], pool.shape[lead - 1],
-         moves.data_ptr(), _dp(n_moves), moves.shape[0])
+    pp, sp = _need(pool, "pool", pool.dtype, dev, shape), _need(src, "src", pool.dtype, dev, other)
+    most = moves.shape[0] if isinstance(moves, torch.Tensor) and moves.dim() == 2 else -1
+    mp, np_ = _need(moves, "moves", _I32, dev, (most, 2)), _may(n_moves, "n_moves", _I32, dev, (1,))
+    page = pool.element_size() * shape[lead:].numel()
+    _run("kda_cache_copy", dev, stream, sp, pp, page, L, other[lead - 1], shape[lead - 1], mp, np_, most)
     return pool
 
 
 def _state_pool(pool, H, dk, dv, dev):
-    _check(pool, "pool", torch.float32, dev)
-    if pool.dim() != 4 or pool.shape[1:] != (H, dk, dv):
-        raise ValueError("libkda: pool must be [n_pages,H,d_k,d_v]")
-    return pool.shape[0]
+    """(pages, address) of a pool of states."""
+    n = pool.shape[0] if isinstance(pool, torch.Tensor) and pool.dim() == 4 else -1
+    return n, _need(pool, "pool", _F32, dev, (n, H, dk, dv))
 
 
 def kda_decode_step_paged(q, k, v, alpha, beta, pool, pages_in, pages_out=None, *, z=None, A=None, o=None,
@@ -718,40 +734,27 @@ def kda_decode_step_paged(q, k, v, alpha, beta, pool, pages_in, pages_out=None, 
     gate inputs z and A of ``kda_decode_step_gated``.  A sequence whose page is out of range (padding: -1), or is
     written by another sequence of the call, is passed over: its row of ``o`` and the pool are left as they were.
     Returns ``o``."""
-    _check(q, "q")
-    dev = q.device
-    for t, n in ((k, "k"), (v, "v")):
-        _check(t, n, q.dtype, dev)
-    _check(beta, "beta", torch.float32, dev)
-    if q.dim() != 3 or v.dim() != 3:
+    dev = _device_of(q, "q")
+    if q.dim() != 3 or not isinstance(v, torch.Tensor) or v.dim() != 3:
         raise ValueError("libkda: decode q/k/v must be [B,H,d]")
-    B, H, dk = q.shape
-    dv = v.shape[-1]
+    shape, dt = q.shape, q.dtype
+    B, H, dk = shape
+    dv = v.shape[2]
+    code = _io_code(q, "q")
+    qp, kp, vp = _need(q, "q", dt, dev, shape), _need(k, "k", dt, dev, shape), _need(v, "v", dt, dev, (B, H, dv))
     if alpha is not None:
         if z is not None or A is not None:
             raise ValueError("libkda: give alpha, or z and A")
-        _check(alpha, "alpha", torch.float32, dev)
+        ap, zp, Ap = _need(alpha, "alpha", _F32, dev, shape), None, None
     else:
-        _check(z, "z", q.dtype, dev)
-        _check(A, "A", torch.float32, dev)
-        if A.shape != (H,):
-            raise ValueError("libkda: A must be [H]")
-    gate = alpha if alpha is not None else z
-    if k.shape != q.shape or gate.shape != q.shape or v.shape[:2] != (B, H) or beta.shape != (B, H):
-        raise ValueError("libkda: inconsistent shapes")
-    P = _state_pool(pool, H, dk, dv, dev)
-    _int_list(pages_in, "pages_in", dev, (B,))
-    if pages_out is not None:
-        _int_list(pages_out, "pages_out", dev, (B,))
+        ap, zp, Ap = None, _need(z, "z", dt, dev, shape), _need(A, "A", _F32, dev, (H,))
+    bp = _need(beta, "beta", _F32, dev, (B, H))
+    P, poolp = _state_pool(pool, H, dk, dv, dev)
+    ip, op = _need(pages_in, "pages_in", _I32, dev, (B,)), _may(pages_out, "pages_out", _I32, dev, (B,))
     if o is None:
-        o = torch.empty(B, H, dv, device=dev, dtype=o_dtype)
-    else:
-        _check(o, "o", None, dev)
-        if o.shape != (B, H, dv):
-            raise ValueError("libkda: o must be [B,H,d_v]")
-    _run("kda_decode_step_paged", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), _dp(alpha), _dp(z),
-         _dp(A), beta.data_ptr(), pool.data_ptr(), P, pages_in.data_ptr(), _dp(pages_out), o.data_ptr(), _dtype_code(o),
-         B, H, dk, dv)
+        o = torch.empty(B, H, dv, device=q.device, dtype=o_dtype)
+    _run("kda_decode_step_paged", dev, stream, qp, kp, vp, code, ap, zp, Ap, bp, poolp, P, ip, op,
+         _need(o, "o", o.dtype, dev, (B, H, dv)), _io_code(o, "o"), B, H, dk, dv)
     return o
 
 
@@ -764,39 +767,23 @@ def kda_tree_verify(q, k, v, alpha, beta, pool, pages, parents, n_nodes=None, *,
     index is smaller), -1 for the state itself; ``n_nodes`` [B] int32: how many nodes each tree has (None: K).  o:
     [B,K,H,d_v], the output after the path to each node; u: [B,H,K,d_v] fp32, what ``kda_tree_commit`` needs.  Rows
     behind a tree's last node, and those of a sequence whose page is out of range, are left as they were."""
-    _check(q, "q")
-    dev = q.device
-    for t, n in ((k, "k"), (v, "v")):
-        _check(t, n, q.dtype, dev)
-    _check(alpha, "alpha", torch.float32, dev)
-    _check(beta, "beta", torch.float32, dev)
-    if q.dim() != 4 or v.dim() != 4:
+    dev = _device_of(q, "q")
+    if q.dim() != 4 or not isinstance(v, torch.Tensor) or v.dim() != 4:
         raise ValueError("libkda: draft q/k/v must be [B,K,H,d]")
-    B, K, H, dk = q.shape
-    dv = v.shape[-1]
-    if k.shape != q.shape or alpha.shape != q.shape or v.shape[:3] != q.shape[:3] or beta.shape != (B, K, H):
-        raise ValueError("libkda: inconsistent shapes")
-    P = _state_pool(pool, H, dk, dv, dev)
-    if pages is not None:
-        _int_list(pages, "pages", dev, (B,))
-    _int_list(parents, "parents", dev, (B, K))
-    if n_nodes is not None:
-        _int_list(n_nodes, "n_nodes", dev, (B,))
+    shape, dt = q.shape, q.dtype
+    B, K, H, dk = shape
+    dv = v.shape[3]
+    code = _io_code(q, "q")
+    qp, kp, vp = _need(q, "q", dt, dev, shape), _need(k, "k", dt, dev, shape), _need(v, "v", dt, dev, (B, K, H, dv))
+    ap, bp = _need(alpha, "alpha", _F32, dev, shape), _need(beta, "beta", _F32, dev, (B, K, H))
+    P, poolp = _state_pool(pool, H, dk, dv, dev)
+    pg, pa, nn = _may(pages, "pages", _I32, dev, (B,)), _need(parents, "parents", _I32, dev, (B, K)), _may(n_nodes, "n_nodes", _I32, dev, (B,))
     if o is None:
-        o = torch.empty(B, K, H, dv, device=dev, dtype=o_dtype)
-    else:
-        _check(o, "o", None, dev)
-        if o.shape != (B, K, H, dv):
-            raise ValueError("libkda: o must be [B,K,H,d_v]")
+        o = torch.empty(B, K, H, dv, device=q.device, dtype=o_dtype)
     if u is None:
-        u = torch.empty(B, H, K, dv, device=dev, dtype=torch.float32)
-    else:
-        _check(u, "u", torch.float32, dev)
-        if u.shape != (B, H, K, dv):
-            raise ValueError("libkda: u must be [B,H,K,d_v]")
-    _run("kda_tree_verify", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), alpha.data_ptr(),
-         beta.data_ptr(), pool.data_ptr(), P, _dp(pages), parents.data_ptr(), _dp(n_nodes), o.data_ptr(), _dtype_code(o),
-         u.data_ptr(), B, K, H, dk, dv)
+        u = torch.empty(B, H, K, dv, device=q.device, dtype=_F32)
+    _run("kda_tree_verify", dev, stream, qp, kp, vp, code, ap, bp, poolp, P, pg, pa, nn, _need(o, "o", o.dtype, dev, (B, K, H, dv)),
+         _io_code(o, "o"), _need(u, "u", _F32, dev, (B, H, K, dv)), B, K, H, dk, dv)
     return o, u
 
 
@@ -806,22 +793,16 @@ def kda_tree_commit(k, alpha, u, parents, last, pool, pages_in, pages_out=None, 
     accepted), from the state on page ``pages_in[b]`` (None: page b).  k, alpha, parents, n_nodes: the arguments
     of ``kda_tree_verify``; u: its output.  Pages out of range or shared are treated as
     ``kda_decode_step_paged`` does.  Returns ``pool``."""
-    _check(k, "k")
-    dev = k.device
-    _check(alpha, "alpha", torch.float32, dev)
-    _check(u, "u", torch.float32, dev)
-    if k.dim() != 4 or u.dim() != 4:
+    dev = _device_of(k, "k")
+    if k.dim() != 4 or not isinstance(u, torch.Tensor) or u.dim() != 4:
         raise ValueError("libkda: draft k must be [B,K,H,d_k] and u [B,H,K,d_v]")
-    B, K, H, dk = k.shape
-    dv = u.shape[-1]
-    if alpha.shape != k.shape or u.shape != (B, H, K, dv):
-        raise ValueError("libkda: inconsistent shapes")
-    P = _state_pool(pool, H, dk, dv, dev)
-    _int_list(parents, "parents", dev, (B, K))
-    _int_list(last, "last", dev, (B,))
-    for t, n in ((n_nodes, "n_nodes"), (pages_in, "pages_in"), (pages_out, "pages_out")):
-        if t is not None:
-            _int_list(t, n, dev, (B,))
-    _run("kda_tree_commit", dev, stream, k.data_ptr(), _dtype_code(k), alpha.data_ptr(), u.data_ptr(), parents.data_ptr(),
-         _dp(n_nodes), last.data_ptr(), pool.data_ptr(), P, _dp(pages_in), _dp(pages_out), B, K, H, dk, dv)
+    shape = k.shape
+    B, K, H, dk = shape
+    dv = u.shape[3]
+    code = _io_code(k, "k")
+    kp, ap, up = _need(k, "k", k.dtype, dev, shape), _need(alpha, "alpha", _F32, dev, shape), _need(u, "u", _F32, dev, (B, H, K, dv))
+    P, poolp = _state_pool(pool, H, dk, dv, dev)
+    pa, lp = _need(parents, "parents", _I32, dev, (B, K)), _need(last, "last", _I32, dev, (B,))
+    nn, ip, op = (_may(t, name, _I32, dev, (B,)) for t, name in ((n_nodes, "n_nodes"), (pages_in, "pages_in"), (pages_out, "pages_out")))
+    _run("kda_tree_commit", dev, stream, kp, code, ap, up, pa, nn, lp, poolp, P, ip, op, B, K, H, dk, dv)
     return pool

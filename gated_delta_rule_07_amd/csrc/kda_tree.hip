@@ -16,14 +16,17 @@
 // channel that has decayed to nothing (or alpha = 0) needs no care.
 //
 // kda_tree_verify_kernel, one workgroup of four waves per (sequence, head):
-//   1. keys, queries and decays of the tree's nodes go to LDS, the state to
-//      registers, all loads in flight at once;
+//   1. the keys, queries and decays of the tree's nodes, the state and the values
+//      are loaded, all in flight at once; the first three go to LDS;
 //   2. one group of d_k / 8 lanes per node walks up its path: c, d and P_t;
 //   3. the 2K x d_k by d_k x d_v product runs on the fp32 matrix cores.  Each wave
 //      owns d_v / 4 columns and holds the state as the B operand straight from
 //      its loads; the A operands P_t k_t and P_t q_t are formed as they are read;
-//   4. each wave substitutes through its columns level by level.  Nodes of one
-//      level do not depend on each other and are spread over the wave's lanes.
+//   4. each wave substitutes through its columns, level after level of the tree,
+//      on the values as the matrix cores left them: a lane holds every fourth
+//      run of four nodes.  The nodes of a level write their u to LDS, and every
+//      node below takes the term of its ancestor there, so a level costs one
+//      exchange however long the paths are.
 #include "kda_device.h"
 #include "kda_launch.h"
 
@@ -37,7 +40,6 @@ struct TCfg {
   static constexpr int NTL = DV >= 128 ? 2 : 1;        // 16-column tiles of a state wave
   static constexpr int CW = 16 * NTL;                  // its columns
   static constexpr int NW = DV / CW;                   // state waves (of 4)
-  static constexpr int SUB = 64 / CW;                  // nodes one wave substitutes at once
   static constexpr int PAD = 16;                       // bytes between LDS rows: 16 rows cover all banks
   static constexpr int KROW = DK * (int)sizeof(IO) + PAD;
   static constexpr int AROW = DK * 4 + PAD;
@@ -46,34 +48,46 @@ struct TCfg {
   static_assert(NW <= 4 && NW * CW == DV, "state waves");
 };
 
-// The verify kernel's LDS, in bytes, for K nodes.  x (the 2K products with the
-// state) takes the place of the keys, queries and decays.
+// The verify kernel's LDS, in bytes, for K nodes.  u takes the place of the keys,
+// queries and decays.
 struct TLay {
-  int k, q, a, x, cd, anc, self, beta, par, depth, slot, total;
+  int k, q, a, u, cd, anc, self, beta, par, depth, total;
   __host__ __device__ static int r16(int n) { return (n + 15) & ~15; }
   __host__ __device__ TLay(int K, int krow, int arow, int dv) {
     const int pairs = K * (K - 1) / 2;
     k = 0;
     q = k + K * krow;
     a = q + K * krow;
-    x = 0;
+    u = 0;
     int o = a + K * arow;
-    if (o < 2 * K * dv * 4) o = 2 * K * dv * 4;
+    if (o < (K + 1) * dv * 4) o = (K + 1) * dv * 4;
     cd = r16(o);
     anc = cd + r16(8 * pairs);
     self = anc + r16(pairs);
     beta = self + r16(4 * K);
     par = beta + r16(4 * K);
     depth = par + r16(4 * K);
-    slot = depth + r16(4 * K);
-    total = slot + 4 * kMaxTree + 16;  // at most 4 K slots (levels padded to whole turns), and their number
+    total = depth + r16(4 * K);
   }
 };
 
+// beta_t c, d and the ancestor of node t's hop j upwards (0: its parent; j < t) stand at
+// pair_row(j, K) + t: K - 1 - j entries for each j.
+__device__ __forceinline__ int pair_row(int j, int K) { return j * (K - 2) - j * (j - 1) / 2 - 1; }
+
+// The sum of x over each aligned group of G lanes, in every one of them.
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float x) {
+  const int y = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true);
+  return x + __builtin_bit_cast(float, y);
+}
 template <int G>
 __device__ __forceinline__ float group_sum(float x) {
-#pragma unroll
-  for (int m = 1; m < G; m *= 2) x += __shfl_xor(x, m);
+  static_assert(G == 2 || G == 4 || G == 8 || G == 16, "lanes of a group");
+  x = add_dpp<0xB1>(x);                          // lane ^ 1
+  if constexpr (G >= 4) x = add_dpp<0x4E>(x);    // lane ^ 2
+  if constexpr (G >= 8) x = add_dpp<0x141>(x);   // the other four of eight
+  if constexpr (G >= 16) x = add_dpp<0x140>(x);  // the other eight of sixteen
   return x;
 }
 
@@ -82,6 +96,14 @@ __device__ __forceinline__ f32x4 lds4(const __bf16* p) {
   const u32x2 w = *reinterpret_cast<const u32x2*>(p);
   return f32x4{__builtin_bit_cast(float, w.x << 16), __builtin_bit_cast(float, w.x & 0xffff0000u),
                __builtin_bit_cast(float, w.y << 16), __builtin_bit_cast(float, w.y & 0xffff0000u)};
+}
+
+// A barrier that waits for LDS only: loads from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// What this wave wrote to LDS is seen by its own later reads.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 template <typename IO, int DK, int DV, int MAXK>
@@ -97,49 +119,83 @@ __global__ __launch_bounds__(kTreeThreads) void kda_tree_verify_kernel(TreeParam
   if (n == 0 || !page_ok(page, p.n_pages)) return;
   const size_t row0 = (size_t)b * K * p.H + h;  // node t: row row0 + t H of the [B][K][H][d] arrays
 
-  int* par = reinterpret_cast<int*>(sm + L.par);
-  float* beta = reinterpret_cast<float*>(sm + L.beta);
-  if (tid < n) {
-    const int up = p.parents[(size_t)b * K + tid];
-    par[tid] = up >= -1 && up < tid ? up : -1;
-    beta[tid] = p.beta[row0 + (size_t)tid * p.H];
-  }
-  // keys, queries and decays, 16 bytes a load, then the state
+  // keys, queries and decays, 16 bytes a load (indices clamped into the tree's rows)
   constexpr int CK = DK * (int)sizeof(IO) / 16, CA = DK * 4 / 16;  // loads of a row
-  for (int e = tid; e < n * CK; e += kTreeThreads) {
-    const int t = e / CK, c = 16 * (e % CK);
-    const size_t at = (row0 + (size_t)t * p.H) * DK * sizeof(IO) + c;
-    *reinterpret_cast<u32x4*>(sm + L.k + t * C::KROW + c) = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.k) + at);
-    *reinterpret_cast<u32x4*>(sm + L.q + t * C::KROW + c) = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.q) + at);
+  constexpr int EK = (MAXK * CK + kTreeThreads - 1) / kTreeThreads, EA = (MAXK * CA + kTreeThreads - 1) / kTreeThreads;
+  u32x4 rk[EK], rq[EK];
+  f32x4 ra[EA];
+  const int tn = min(tid, n - 1);
+  const int up = p.parents[(size_t)b * K + tn];
+  const float bt = p.beta[row0 + (size_t)tn * p.H];
+#pragma unroll
+  for (int j = 0; j < EK; ++j) {
+    if (j * kTreeThreads >= n * CK) continue;
+    const int e = min(tid + j * kTreeThreads, n * CK - 1);
+    const size_t at = (row0 + (size_t)(e / CK) * p.H) * (DK * sizeof(IO)) + 16 * (e % CK);
+    rk[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.k) + at);
+    rq[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.q) + at);
   }
-  for (int e = tid; e < n * CA; e += kTreeThreads) {
-    const int t = e / CA, c = e % CA;
-    *reinterpret_cast<f32x4*>(sm + L.a + t * C::AROW + 16 * c) =
-        *reinterpret_cast<const f32x4*>(p.alpha + (row0 + (size_t)t * p.H) * DK + 4 * c);
+#pragma unroll
+  for (int j = 0; j < EA; ++j) {
+    if (j * kTreeThreads >= n * CA) continue;
+    const int e = min(tid + j * kTreeThreads, n * CA - 1);
+    ra[j] = *reinterpret_cast<const f32x4*>(p.alpha + (row0 + (size_t)(e / CA) * p.H) * DK + 4 * (e % CA));
   }
+  __builtin_amdgcn_sched_barrier(0);  // (loads are counted in order: the small ones come first)
+
+  // the state, as the matrix cores' B operand: slot (lg, e) of step kk is row 16 kk + 4 lg + e
+  typedef float colf __attribute__((ext_vector_type(C::NTL)));
+  typedef IO colio __attribute__((ext_vector_type(C::NTL)));
   const int ln = lane % 16, lg = lane / 16;
   const bool stw = wave < C::NW;  // a state wave
   const int col = C::CW * wave + C::NTL * ln;  // its lane's first column
-  float s[DK / 16][4][C::NTL];  // rows 16 kk + 4 lg + e
+  constexpr int NT = (MAXK + 15) / 16;
+  colf s[DK / 16][4];
+  colio rv[NT][4];
   if (stw) {
     const float* S = p.pool + ((size_t)page * p.H + h) * DK * DV + col;
 #pragma unroll
     for (int kk = 0; kk < DK / 16; ++kk)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        typedef float row __attribute__((ext_vector_type(C::NTL)));
-        const row w = *reinterpret_cast<const row*>(S + (size_t)(16 * kk + 4 * lg + e) * DV);
+      for (int e = 0; e < 4; ++e) s[kk][e] = *reinterpret_cast<const colf*>(S + (size_t)(16 * kk + 4 * lg + e) * DV);
 #pragma unroll
-        for (int j = 0; j < C::NTL; ++j) s[kk][e][j] = w[j];
-      }
+    for (int m = 0; m < NT; ++m) {
+      if (16 * m >= n) continue;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        rv[m][r] = *reinterpret_cast<const colio*>(
+            static_cast<const IO*>(p.v) + (row0 + (size_t)min(16 * m + 4 * lg + r, n - 1) * p.H) * DV + col);
+    }
   }
-  __syncthreads();
+  __builtin_amdgcn_sched_barrier(0);
+
+  int* par = reinterpret_cast<int*>(sm + L.par);
+  float* beta = reinterpret_cast<float*>(sm + L.beta);
+  if (tid < n) {
+    par[tid] = up >= -1 && up < tid ? up : -1;
+    beta[tid] = bt;
+  }
+#pragma unroll
+  for (int j = 0; j < EK; ++j) {
+    if (j * kTreeThreads >= n * CK) continue;
+    const int e = min(tid + j * kTreeThreads, n * CK - 1);  // (a clamped index stores what is there)
+    *reinterpret_cast<u32x4*>(sm + L.k + (e / CK) * C::KROW + 16 * (e % CK)) = rk[j];
+    *reinterpret_cast<u32x4*>(sm + L.q + (e / CK) * C::KROW + 16 * (e % CK)) = rq[j];
+  }
+#pragma unroll
+  for (int j = 0; j < EA; ++j) {
+    if (j * kTreeThreads >= n * CA) continue;
+    const int e = min(tid + j * kTreeThreads, n * CA - 1);
+    *reinterpret_cast<f32x4*>(sm + L.a + (e / CA) * C::AROW + 16 * (e % CA)) = ra[j];
+  }
+  lds_barrier();
 
   auto krow = [&](int t) { return reinterpret_cast<const IO*>(sm + L.k + t * C::KROW); };
   auto qrow = [&](int t) { return reinterpret_cast<const IO*>(sm + L.q + t * C::KROW); };
   auto arow = [&](int t) { return reinterpret_cast<float*>(sm + L.a + t * C::AROW); };
 
-  // up each node's path; a lane holds channels 4 gl + {0..3} and DK/2 + 4 gl + {0..3}
+  // up each node's path; a lane holds channels 4 gl + {0..3} and DK/2 + 4 gl + {0..3},
+  // and reads the next ancestor's row while it works on one
   constexpr int NPG = (MAXK + C::GROUPS - 1) / C::GROUPS;
   const int gl = tid % C::GL, grp = tid / C::GL;
   const int i0 = 4 * gl, i1 = DK / 2 + 4 * gl;
@@ -152,17 +208,31 @@ __global__ __launch_bounds__(kTreeThreads) void kda_tree_verify_kernel(TreeParam
   for (int it = 0; it < NPG; ++it) {
     const int t = it * C::GROUPS + grp;
     if (t >= n) continue;
+    int r = par[t], rc = max(r, 0);
     const f32x4 k0 = lds4(krow(t) + i0), k1 = lds4(krow(t) + i1);
     const f32x4 q0 = lds4(qrow(t) + i0), q1 = lds4(qrow(t) + i1);
     f32x4 g0 = lds4(arow(t) + i0), g1 = lds4(arow(t) + i1);
+    f32x4 kr0 = lds4(krow(rc) + i0), kr1 = lds4(krow(rc) + i1), ar0 = lds4(arow(rc) + i0), ar1 = lds4(arow(rc) + i1);
+    int rn = par[rc];
+    const float be = beta[t];
     float dt = 0.0f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) dt += k0[e] * q0[e] + k1[e] * q1[e];
     dt = group_sum<C::GL>(dt);
-    const int off = t * (t - 1) / 2;
     int hops = 0;
-    for (int r = par[t]; r >= 0; r = par[r], ++hops) {
-      const f32x4 w0 = g0 * lds4(krow(r) + i0), w1 = g1 * lds4(krow(r) + i1);
+    while (r >= 0) {
+      const f32x4 w0 = g0 * kr0, w1 = g1 * kr1;
+      g0 *= ar0;
+      g1 *= ar1;
+      const int at = pair_row(hops, K) + t;
+      const unsigned char who = (unsigned char)r;
+      r = rn;
+      rc = max(r, 0);
+      kr0 = lds4(krow(rc) + i0);
+      kr1 = lds4(krow(rc) + i1);
+      ar0 = lds4(arow(rc) + i0);
+      ar1 = lds4(arow(rc) + i1);
+      rn = par[rc];
       float cs = 0.0f, ds = 0.0f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -172,11 +242,10 @@ __global__ __launch_bounds__(kTreeThreads) void kda_tree_verify_kernel(TreeParam
       cs = group_sum<C::GL>(cs);
       ds = group_sum<C::GL>(ds);
       if (gl == 0) {
-        cd[off + hops] = float2{cs, ds};
-        anc[off + hops] = (unsigned char)r;
+        cd[at] = float2{be * cs, ds};
+        anc[at] = who;
       }
-      g0 *= lds4(arow(r) + i0);
-      g1 *= lds4(arow(r) + i1);
+      ++hops;
     }
     if (gl == 0) {
       self[t] = dt;
@@ -185,7 +254,7 @@ __global__ __launch_bounds__(kTreeThreads) void kda_tree_verify_kernel(TreeParam
     P[it][0] = g0;
     P[it][1] = g1;
   }
-  __syncthreads();
+  lds_barrier();
   // P takes the decays' place
 #pragma unroll
   for (int it = 0; it < NPG; ++it) {
@@ -194,38 +263,21 @@ __global__ __launch_bounds__(kTreeThreads) void kda_tree_verify_kernel(TreeParam
     *reinterpret_cast<f32x4*>(arow(t) + i0) = P[it][0];
     *reinterpret_cast<f32x4*>(arow(t) + i1) = P[it][1];
   }
-  // the order of substitution: level after level, each padded to whole turns of SUB nodes
-  signed char* slot = reinterpret_cast<signed char*>(sm + L.slot);
-  int* nslots = reinterpret_cast<int*>(sm + L.slot + 4 * kMaxTree);
-  if (wave == 3) {
-    const int dpt = lane < n ? depth[lane] : -1;
-    for (int e = lane; e < 4 * kMaxTree; e += 64) slot[e] = -1;
-    int base = 0, left = n;
-    for (int lev = 0; left > 0; ++lev) {
-      const unsigned long long m = __ballot(dpt == lev);
-      if (dpt == lev) slot[base + __popcll(m & ((1ull << lane) - 1))] = (signed char)lane;
-      const int cnt = __popcll(m);
-      left -= cnt;
-      base += (cnt + C::SUB - 1) / C::SUB * C::SUB;
-    }
-    if (lane == 0) *nslots = base;
-  }
-  __syncthreads();
+  lds_barrier();
 
-  // products with the state
-  constexpr int NT = (MAXK + 15) / 16;
-  f32x4 xk[NT][C::NTL], xq[NT][C::NTL];
+  // products with the state: x (of the keys) and y (of the queries), of node 16 m + 4 lg + r
+  f32x4 xa[NT][C::NTL], ya[NT][C::NTL];
 #pragma unroll
   for (int m = 0; m < NT; ++m)
 #pragma unroll
-    for (int j = 0; j < C::NTL; ++j) xk[m][j] = xq[m][j] = (f32x4)0.0f;
+    for (int j = 0; j < C::NTL; ++j) xa[m][j] = ya[m][j] = (f32x4)0.0f;
   if (stw) {
 #pragma unroll
-    for (int kk = 0; kk < DK / 16; ++kk) {
+    for (int m = 0; m < NT; ++m) {
+      if (16 * m >= n) continue;
+      const int t = min(16 * m + ln, n - 1);  // (a row past the last node only feeds its own row of the result)
 #pragma unroll
-      for (int m = 0; m < NT; ++m) {
-        if (16 * m >= n) continue;
-        const int t = min(16 * m + ln, n - 1);  // (a row past the last node only feeds its own row of the result)
+      for (int kk = 0; kk < DK / 16; ++kk) {
         const int i = 16 * kk + 4 * lg;
         const f32x4 pt = lds4(arow(t) + i);
         const f32x4 pk = pt * lds4(krow(t) + i), pq = pt * lds4(qrow(t) + i);
@@ -233,57 +285,103 @@ __global__ __launch_bounds__(kTreeThreads) void kda_tree_verify_kernel(TreeParam
         for (int e = 0; e < 4; ++e)
 #pragma unroll
           for (int j = 0; j < C::NTL; ++j) {
-            xk[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(pk[e], s[kk][e][j], xk[m][j], 0, 0, 0);
-            xq[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(pq[e], s[kk][e][j], xq[m][j], 0, 0, 0);
+            xa[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(pk[e], s[kk][e][j], xa[m][j], 0, 0, 0);
+            ya[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(pq[e], s[kk][e][j], ya[m][j], 0, 0, 0);
           }
       }
     }
   }
-  __syncthreads();  // keys, queries and decays are done with: x takes their place
+  lds_barrier();  // keys, queries and decays are done with: u takes their place
   if (!stw) return;
-  float* x = reinterpret_cast<float*>(sm + L.x);
+
+  // substitution, a level of the tree at a time: x, from beta (v - x) on, is a node's u
+  // as soon as the levels above it are done
+  float* us = reinterpret_cast<float*>(sm + L.u) + (size_t)(K + 1) * C::CW * wave + C::NTL * ln;  // [K + 1][CW] of this wave
+  float x[NT][4][C::NTL], y[NT][4][C::NTL];
+  int dep[NT][4], lowest[NT];  // lowest: the deepest of the lane's four nodes
+  int deepest = 0;
+#pragma unroll
+  for (int m = 0; m < NT; ++m) {
+    lowest[m] = -1;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 16 * m + 4 * lg + r, tc = min(t, n - 1);
+      dep[m][r] = t < n ? depth[tc] : -1;
+      lowest[m] = max(lowest[m], dep[m][r]);
+      const float be = beta[tc];
+#pragma unroll
+      for (int j = 0; j < C::NTL; ++j) {
+        x[m][r][j] = be * (to_f32(rv[m][r][j]) - xa[m][j][r]);
+        y[m][r][j] = ya[m][j][r];
+      }
+    }
+    deepest = max(deepest, lowest[m]);
+  }
+  deepest = max(deepest, __shfl_xor(deepest, 16));
+  deepest = max(deepest, __shfl_xor(deepest, 32));
+  for (int lev = 0; lev < deepest; ++lev) {
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+      if (!__any(lowest[m] >= lev)) continue;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {  // (what deeper nodes write here is written again at their level; row K is a spare)
+        colf w;
+#pragma unroll
+        for (int j = 0; j < C::NTL; ++j) w[j] = x[m][r][j];
+        *reinterpret_cast<colf*>(us + min(16 * m + 4 * lg + r, K) * C::CW) = w;
+      }
+    }
+    wave_lds_order();
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+      if (!__any(lowest[m] > lev)) continue;
+      float2 w[4];
+      int row[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 16 * m + 4 * lg + r;
+        const int at = dep[m][r] > lev ? pair_row(dep[m][r] - 1 - lev, K) + t : 0;
+        w[r] = cd[at];
+        row[r] = anc[at];
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const bool below = dep[m][r] > lev;
+        const colf ua = *reinterpret_cast<const colf*>(us + (below ? row[r] : 0) * C::CW);
+#pragma unroll
+        for (int j = 0; j < C::NTL; ++j) {
+          x[m][r][j] = below ? x[m][r][j] - w[r].x * ua[j] : x[m][r][j];
+          y[m][r][j] = below ? y[m][r][j] + w[r].y * ua[j] : y[m][r][j];
+        }
+      }
+    }
+    wave_lds_order();
+  }
 #pragma unroll
   for (int m = 0; m < NT; ++m) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = 16 * m + 4 * lg + r;
       if (t >= n) continue;
-      const IO* v = static_cast<const IO*>(p.v) + (row0 + (size_t)t * p.H) * DV + col;
+      const float se = self[t];
+      colf ut, ot;
 #pragma unroll
       for (int j = 0; j < C::NTL; ++j) {
-        x[t * DV + col + j] = to_f32(v[j]) - xk[m][j][r];
-        x[(K + t) * DV + col + j] = xq[m][j][r];
+        ut[j] = x[m][r][j];
+        ot[j] = y[m][r][j] + se * x[m][r][j];
+      }
+      const size_t at = (row0 + (size_t)t * p.H) * DV + col;
+      *reinterpret_cast<colf*>(p.u + (((size_t)b * p.H + h) * K + t) * DV + col) = ut;
+      if (p.o_f32) {
+        *reinterpret_cast<colf*>(static_cast<float*>(p.o) + at) = ot;
+      } else {
+        typedef __bf16 colb __attribute__((ext_vector_type(C::NTL)));
+        colb ob;
+#pragma unroll
+        for (int j = 0; j < C::NTL; ++j) ob[j] = (__bf16)ot[j];
+        *reinterpret_cast<colb*>(static_cast<__bf16*>(p.o) + at) = ob;
       }
     }
-  }
-  // (from here on a wave only reads what it wrote itself)
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-
-  const int c = C::CW * wave + lane % C::CW, sub = lane / C::CW;
-  const int turns = *nslots / C::SUB;
-  for (int i = 0; i < turns; ++i) {
-    const int t = slot[i * C::SUB + sub];
-    if (t >= 0) {
-      float xt = x[t * DV + c], yt = x[(K + t) * DV + c];
-      const int off = t * (t - 1) / 2, hops = depth[t];
-#pragma unroll 4
-      for (int j = 0; j < hops; ++j) {
-        const float2 w = cd[off + j];
-        const float us = x[(int)anc[off + j] * DV + c];
-        xt -= w.x * us;
-        yt += w.y * us;
-      }
-      const float ut = beta[t] * xt;
-      yt += self[t] * ut;
-      x[t * DV + c] = ut;
-      const size_t orow = row0 + (size_t)t * p.H;
-      if (p.o_f32) static_cast<float*>(p.o)[orow * DV + c] = yt;
-      else static_cast<__bf16*>(p.o)[orow * DV + c] = (__bf16)yt;
-      p.u[(((size_t)b * p.H + h) * K + t) * DV + c] = ut;
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
   }
 }
 
