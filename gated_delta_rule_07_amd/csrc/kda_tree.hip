@@ -40,40 +40,34 @@ struct TCfg {
   static constexpr int NTL = DV >= 128 ? 2 : 1;        // 16-column tiles of a state wave
   static constexpr int CW = 16 * NTL;                  // its columns
   static constexpr int NW = DV / CW;                   // state waves (of 4)
-  static constexpr int PAD = 16;                       // bytes between LDS rows: 16 rows cover all banks
-  static constexpr int KROW = DK * (int)sizeof(IO) + PAD;
-  static constexpr int AROW = DK * 4 + PAD;
+  // a node's row in LDS: key, query, decays, and 16 bytes by which 16 rows cover all banks
+  static constexpr int QAT = DK * (int)sizeof(IO), AAT = 2 * QAT, ROW = AAT + DK * 4 + 16;
   static constexpr int GL = DK / 8;                    // lanes of a node's group
   static constexpr int GROUPS = kTreeThreads / GL;
   static_assert(NW <= 4 && NW * CW == DV, "state waves");
 };
 
-// The verify kernel's LDS, in bytes, for K nodes.  u takes the place of the keys,
-// queries and decays.
+// The verify kernel's LDS, in bytes, for K nodes.  Row K stands for the state the tree
+// starts from: no key, and no decay.  u takes the place of the rows.
 struct TLay {
-  int k, q, a, u, cd, anc, self, beta, par, depth, total;
+  int rows, u, cd, anc, self, beta, par, depth, total;
   __host__ __device__ static int r16(int n) { return (n + 15) & ~15; }
-  __host__ __device__ TLay(int K, int krow, int arow, int dv) {
+  __host__ __device__ TLay(int K, int row, int dv) {
     const int pairs = K * (K - 1) / 2;
-    k = 0;
-    q = k + K * krow;
-    a = q + K * krow;
-    u = 0;
-    int o = a + K * arow;
-    if (o < (K + 1) * dv * 4) o = (K + 1) * dv * 4;
-    cd = r16(o);
+    rows = u = 0;
+    cd = r16((K + 1) * (row > dv * 4 ? row : dv * 4));
     anc = cd + r16(8 * pairs);
     self = anc + r16(pairs);
     beta = self + r16(4 * K);
     par = beta + r16(4 * K);
-    depth = par + r16(4 * K);
+    depth = par + r16(4 * K + 4);
     total = depth + r16(4 * K);
   }
 };
 
 // beta_t c, d and the ancestor of node t's hop j upwards (0: its parent; j < t) stand at
-// pair_row(j, K) + t: K - 1 - j entries for each j.
-__device__ __forceinline__ int pair_row(int j, int K) { return j * (K - 2) - j * (j - 1) / 2 - 1; }
+// first_pair(t) + j.
+__device__ __forceinline__ int first_pair(int t) { return t * (t - 1) / 2; }
 
 // The sum of x over each aligned group of G lanes, in every one of them.
 template <int CTRL>
@@ -107,19 +101,20 @@ __device__ __forceinline__ void wave_lds_order() {
 }
 
 template <typename IO, int DK, int DV, int MAXK>
-__global__ __launch_bounds__(kTreeThreads) void kda_tree_verify_kernel(TreeParams p) {
+__global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 3 : 1) void kda_tree_verify_kernel(TreeParams p) {
   using C = TCfg<IO, DK, DV>;
   extern __shared__ u32x4 tree_lds[];
   char* sm = reinterpret_cast<char*>(tree_lds);
   const int K = p.K, tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
-  const TLay L(K, C::KROW, C::AROW, DV);
+  const TLay L(K, C::ROW, DV);
   const int b = blockIdx.x / p.H, h = blockIdx.x % p.H;
   const int n = p.n_nodes ? min(max(p.n_nodes[b], 0), K) : K;
   const int page = p.pages ? p.pages[b] : b;
   if (n == 0 || !page_ok(page, p.n_pages)) return;
   const size_t row0 = (size_t)b * K * p.H + h;  // node t: row row0 + t H of the [B][K][H][d] arrays
 
-  // keys, queries and decays, 16 bytes a load (indices clamped into the tree's rows)
+  // keys, queries and decays, 16 bytes a load (indices clamped into the tree's rows, and
+  // no branch: one around a load makes the compiler wait for it)
   constexpr int CK = DK * (int)sizeof(IO) / 16, CA = DK * 4 / 16;  // loads of a row
   constexpr int EK = (MAXK * CK + kTreeThreads - 1) / kTreeThreads, EA = (MAXK * CA + kTreeThreads - 1) / kTreeThreads;
   u32x4 rk[EK], rq[EK];
@@ -129,16 +124,14 @@ __global__ __launch_bounds__(kTreeThreads) void kda_tree_verify_kernel(TreeParam
   const float bt = p.beta[row0 + (size_t)tn * p.H];
 #pragma unroll
   for (int j = 0; j < EK; ++j) {
-    if (j * kTreeThreads >= n * CK) continue;
-    const int e = min(tid + j * kTreeThreads, n * CK - 1);
+    const unsigned e = min(tid + j * kTreeThreads, n * CK - 1);
     const size_t at = (row0 + (size_t)(e / CK) * p.H) * (DK * sizeof(IO)) + 16 * (e % CK);
     rk[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.k) + at);
     rq[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.q) + at);
   }
 #pragma unroll
   for (int j = 0; j < EA; ++j) {
-    if (j * kTreeThreads >= n * CA) continue;
-    const int e = min(tid + j * kTreeThreads, n * CA - 1);
+    const unsigned e = min(tid + j * kTreeThreads, n * CA - 1);
     ra[j] = *reinterpret_cast<const f32x4*>(p.alpha + (row0 + (size_t)(e / CA) * p.H) * DK + 4 * (e % CA));
   }
   __builtin_amdgcn_sched_barrier(0);  // (loads are counted in order: the small ones come first)
@@ -147,55 +140,57 @@ __global__ __launch_bounds__(kTreeThreads) void kda_tree_verify_kernel(TreeParam
   typedef float colf __attribute__((ext_vector_type(C::NTL)));
   typedef IO colio __attribute__((ext_vector_type(C::NTL)));
   const int ln = lane % 16, lg = lane / 16;
-  const bool stw = wave < C::NW;  // a state wave
-  const int col = C::CW * wave + C::NTL * ln;  // its lane's first column
+  const bool stw = C::NW == 4 || wave < C::NW;  // a state wave (the others load what the last one does)
+  const int col = C::CW * min(wave, C::NW - 1) + C::NTL * ln;  // its lane's first column
   constexpr int NT = (MAXK + 15) / 16;
   colf s[DK / 16][4];
   colio rv[NT][4];
-  if (stw) {
-    const float* S = p.pool + ((size_t)page * p.H + h) * DK * DV + col;
+  const float* S = p.pool + ((size_t)page * p.H + h) * DK * DV + col;
 #pragma unroll
-    for (int kk = 0; kk < DK / 16; ++kk)
+  for (int kk = 0; kk < DK / 16; ++kk)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[kk][e] = *reinterpret_cast<const colf*>(S + (size_t)(16 * kk + 4 * lg + e) * DV);
+    for (int e = 0; e < 4; ++e) s[kk][e] = *reinterpret_cast<const colf*>(S + (size_t)(16 * kk + 4 * lg + e) * DV);
 #pragma unroll
-    for (int m = 0; m < NT; ++m) {
-      if (16 * m >= n) continue;
+  for (int m = 0; m < NT; ++m) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        rv[m][r] = *reinterpret_cast<const colio*>(
-            static_cast<const IO*>(p.v) + (row0 + (size_t)min(16 * m + 4 * lg + r, n - 1) * p.H) * DV + col);
-    }
+    for (int r = 0; r < 4; ++r)
+      rv[m][r] = *reinterpret_cast<const colio*>(
+          static_cast<const IO*>(p.v) + (row0 + (size_t)min(16 * m + 4 * lg + r, n - 1) * p.H) * DV + col);
   }
   __builtin_amdgcn_sched_barrier(0);
 
   int* par = reinterpret_cast<int*>(sm + L.par);
   float* beta = reinterpret_cast<float*>(sm + L.beta);
   if (tid < n) {
-    par[tid] = up >= -1 && up < tid ? up : -1;
+    par[tid] = up >= 0 && up < tid ? up : K;
     beta[tid] = bt;
+  }
+  if (tid == 0) par[K] = K;
+  // (24-bit products: a 32-bit one becomes a 64-bit multiply-add whose unused half may
+  // wait for a load)
+  auto row = [&](int t) { return sm + L.rows + __umul24(t, C::ROW); };
+  auto krow = [&](int t) { return reinterpret_cast<const IO*>(row(t)); };
+  auto qrow = [&](int t) { return reinterpret_cast<const IO*>(row(t) + C::QAT); };
+  auto arow = [&](int t) { return reinterpret_cast<float*>(row(t) + C::AAT); };
+  for (int i = tid; i < DK; i += kTreeThreads) {
+    const_cast<IO*>(krow(K))[i] = (IO)0.0f;
+    arow(K)[i] = 1.0f;
   }
 #pragma unroll
   for (int j = 0; j < EK; ++j) {
-    if (j * kTreeThreads >= n * CK) continue;
-    const int e = min(tid + j * kTreeThreads, n * CK - 1);  // (a clamped index stores what is there)
-    *reinterpret_cast<u32x4*>(sm + L.k + (e / CK) * C::KROW + 16 * (e % CK)) = rk[j];
-    *reinterpret_cast<u32x4*>(sm + L.q + (e / CK) * C::KROW + 16 * (e % CK)) = rq[j];
+    const unsigned e = min(tid + j * kTreeThreads, n * CK - 1);  // (a clamped index stores what is there)
+    *reinterpret_cast<u32x4*>(row(e / CK) + 16 * (e % CK)) = rk[j];
+    *reinterpret_cast<u32x4*>(row(e / CK) + C::QAT + 16 * (e % CK)) = rq[j];
   }
 #pragma unroll
   for (int j = 0; j < EA; ++j) {
-    if (j * kTreeThreads >= n * CA) continue;
-    const int e = min(tid + j * kTreeThreads, n * CA - 1);
-    *reinterpret_cast<f32x4*>(sm + L.a + (e / CA) * C::AROW + 16 * (e % CA)) = ra[j];
+    const unsigned e = min(tid + j * kTreeThreads, n * CA - 1);
+    *reinterpret_cast<f32x4*>(row(e / CA) + C::AAT + 16 * (e % CA)) = ra[j];
   }
   lds_barrier();
 
-  auto krow = [&](int t) { return reinterpret_cast<const IO*>(sm + L.k + t * C::KROW); };
-  auto qrow = [&](int t) { return reinterpret_cast<const IO*>(sm + L.q + t * C::KROW); };
-  auto arow = [&](int t) { return reinterpret_cast<float*>(sm + L.a + t * C::AROW); };
-
-  // up each node's path; a lane holds channels 4 gl + {0..3} and DK/2 + 4 gl + {0..3},
-  // and reads the next ancestor's row while it works on one
+  // up each node's path; a lane holds channels 4 gl + {0..3} and DK/2 + 4 gl + {0..3}, and
+  // reads the next ancestor's row while it works on one
   constexpr int NPG = (MAXK + C::GROUPS - 1) / C::GROUPS;
   const int gl = tid % C::GL, grp = tid / C::GL;
   const int i0 = 4 * gl, i1 = DK / 2 + 4 * gl;
@@ -208,36 +203,36 @@ __global__ __launch_bounds__(kTreeThreads) void kda_tree_verify_kernel(TreeParam
   for (int it = 0; it < NPG; ++it) {
     const int t = it * C::GROUPS + grp;
     if (t >= n) continue;
-    int r = par[t], rc = max(r, 0);
+    int r = par[t];
     const f32x4 k0 = lds4(krow(t) + i0), k1 = lds4(krow(t) + i1);
     const f32x4 q0 = lds4(qrow(t) + i0), q1 = lds4(qrow(t) + i1);
     f32x4 g0 = lds4(arow(t) + i0), g1 = lds4(arow(t) + i1);
-    f32x4 kr0 = lds4(krow(rc) + i0), kr1 = lds4(krow(rc) + i1), ar0 = lds4(arow(rc) + i0), ar1 = lds4(arow(rc) + i1);
-    int rn = par[rc];
+    f32x4 kr0 = lds4(krow(r) + i0), kr1 = lds4(krow(r) + i1), ar0 = lds4(arow(r) + i0), ar1 = lds4(arow(r) + i1);
+    int rn = par[r];
     const float be = beta[t];
     float dt = 0.0f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) dt += k0[e] * q0[e] + k1[e] * q1[e];
     dt = group_sum<C::GL>(dt);
-    int hops = 0;
-    while (r >= 0) {
+    int at = first_pair(t);
+    while (r < K) {
       const f32x4 w0 = g0 * kr0, w1 = g1 * kr1;
       g0 *= ar0;
       g1 *= ar1;
-      const int at = pair_row(hops, K) + t;
       const unsigned char who = (unsigned char)r;
       r = rn;
-      rc = max(r, 0);
-      kr0 = lds4(krow(rc) + i0);
-      kr1 = lds4(krow(rc) + i1);
-      ar0 = lds4(arow(rc) + i0);
-      ar1 = lds4(arow(rc) + i1);
-      rn = par[rc];
+      kr0 = lds4(krow(r) + i0);
+      kr1 = lds4(krow(r) + i1);
+      ar0 = lds4(arow(r) + i0);
+      ar1 = lds4(arow(r) + i1);
+      rn = par[r];
       float cs = 0.0f, ds = 0.0f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        cs += w0[e] * k0[e] + w1[e] * k1[e];
-        ds += w0[e] * q0[e] + w1[e] * q1[e];
+        cs += w0[e] * k0[e];
+        ds += w0[e] * q0[e];
+        cs += w1[e] * k1[e];
+        ds += w1[e] * q1[e];
       }
       cs = group_sum<C::GL>(cs);
       ds = group_sum<C::GL>(ds);
@@ -245,11 +240,11 @@ __global__ __launch_bounds__(kTreeThreads) void kda_tree_verify_kernel(TreeParam
         cd[at] = float2{be * cs, ds};
         anc[at] = who;
       }
-      ++hops;
+      ++at;
     }
     if (gl == 0) {
       self[t] = dt;
-      depth[t] = hops;
+      depth[t] = at - first_pair(t);
     }
     P[it][0] = g0;
     P[it][1] = g1;
@@ -298,16 +293,16 @@ __global__ __launch_bounds__(kTreeThreads) void kda_tree_verify_kernel(TreeParam
   // as soon as the levels above it are done
   float* us = reinterpret_cast<float*>(sm + L.u) + (size_t)(K + 1) * C::CW * wave + C::NTL * ln;  // [K + 1][CW] of this wave
   float x[NT][4][C::NTL], y[NT][4][C::NTL];
-  int dep[NT][4], lowest[NT];  // lowest: the deepest of the lane's four nodes
+  int dep[NT][4], top[NT][4];  // a node's depth, and where its hop to the root stands in cd and anc
   int deepest = 0;
 #pragma unroll
   for (int m = 0; m < NT; ++m) {
-    lowest[m] = -1;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = 16 * m + 4 * lg + r, tc = min(t, n - 1);
       dep[m][r] = t < n ? depth[tc] : -1;
-      lowest[m] = max(lowest[m], dep[m][r]);
+      deepest = max(deepest, dep[m][r]);
+      top[m][r] = first_pair(tc) + max(dep[m][r], 0) - 1;
       const float be = beta[tc];
 #pragma unroll
       for (int j = 0; j < C::NTL; ++j) {
@@ -315,16 +310,17 @@ __global__ __launch_bounds__(kTreeThreads) void kda_tree_verify_kernel(TreeParam
         y[m][r][j] = ya[m][j][r];
       }
     }
-    deepest = max(deepest, lowest[m]);
   }
   deepest = max(deepest, __shfl_xor(deepest, 16));
   deepest = max(deepest, __shfl_xor(deepest, 32));
+  // (no branches on single nodes: every load of a level is in flight at once.  What a node
+  // writes before its level is written again there, row K is a spare, and a node at or above
+  // the level reads some pair and row and drops them)
   for (int lev = 0; lev < deepest; ++lev) {
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
-      if (!__any(lowest[m] >= lev)) continue;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {  // (what deeper nodes write here is written again at their level; row K is a spare)
+      for (int r = 0; r < 4; ++r) {
         colf w;
 #pragma unroll
         for (int j = 0; j < C::NTL; ++j) w[j] = x[m][r][j];
@@ -332,26 +328,27 @@ __global__ __launch_bounds__(kTreeThreads) void kda_tree_verify_kernel(TreeParam
       }
     }
     wave_lds_order();
+    float2 w[NT][4];
+    int row[NT][4];
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
-      if (!__any(lowest[m] > lev)) continue;
-      float2 w[4];
-      int row[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int t = 16 * m + 4 * lg + r;
-        const int at = dep[m][r] > lev ? pair_row(dep[m][r] - 1 - lev, K) + t : 0;
-        w[r] = cd[at];
-        row[r] = anc[at];
+        const int at = max(top[m][r] - lev, 0);
+        w[m][r] = cd[at];
+        row[m][r] = anc[at];
       }
+    }
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const bool below = dep[m][r] > lev;
-        const colf ua = *reinterpret_cast<const colf*>(us + (below ? row[r] : 0) * C::CW);
+        const colf ua = *reinterpret_cast<const colf*>(us + (below ? row[m][r] : 0) * C::CW);
 #pragma unroll
         for (int j = 0; j < C::NTL; ++j) {
-          x[m][r][j] = below ? x[m][r][j] - w[r].x * ua[j] : x[m][r][j];
-          y[m][r][j] = below ? y[m][r][j] + w[r].y * ua[j] : y[m][r][j];
+          x[m][r][j] = below ? x[m][r][j] - w[m][r].x * ua[j] : x[m][r][j];
+          y[m][r][j] = below ? y[m][r][j] + w[m][r].y * ua[j] : y[m][r][j];
         }
       }
     }
@@ -462,7 +459,7 @@ __global__ __launch_bounds__(256) void kda_tree_commit_kernel(TreeCommitParams p
 template <typename IO, int DK, int DV, int MAXK>
 hipError_t verify_k(const TreeParams& p, hipStream_t s) {
   using C = TCfg<IO, DK, DV>;
-  const int lds = TLay(p.K, C::KROW, C::AROW, DV).total;
+  const int lds = TLay(p.K, C::ROW, DV).total;
   if (lds > 65536) {  // more than the default has to be asked for
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&kda_tree_verify_kernel<IO, DK, DV, MAXK>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
