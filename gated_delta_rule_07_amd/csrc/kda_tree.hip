@@ -18,15 +18,19 @@
 // kda_tree_verify_kernel, one workgroup of four waves per (sequence, head):
 //   1. the keys, queries and decays of the tree's nodes, the state and the values
 //      are loaded, all in flight at once; the first three go to LDS;
-//   2. one group of d_k / 8 lanes per node walks up its path: c, d and P_t;
+//   2. one group of d_k / 8 lanes per node walks up its path: c, d and P_t.  They
+//      fill two K x K matrices, C (beta_t c, strictly below the diagonal because a
+//      node follows its parent) and D (d, with k_t . q_t on it), zero elsewhere;
 //   3. the 2K x d_k by d_k x d_v product runs on the fp32 matrix cores.  Each wave
 //      owns d_v / 4 columns and holds the state as the B operand straight from
 //      its loads; the A operands P_t k_t and P_t q_t are formed as they are read;
-//   4. each wave substitutes through its columns, level after level of the tree,
-//      on the values as the matrix cores left them: a lane holds every fourth
-//      run of four nodes.  The nodes of a level write their u to LDS, and every
-//      node below takes the term of its ancestor there, so a level costs one
-//      exchange however long the paths are.
+//   4. U = (I + C)^-1 beta (V - X) and O = Y + D U, in blocks of 16 nodes, on the
+//      matrix cores too: the 16 x 16 inverses on the diagonal are one lane per
+//      column, and a block's result, as the matrix cores leave it, is the next
+//      product's B operand.  (Substituting level after level of the tree through
+//      LDS instead took 8 of 20 us on deep trees of 63 nodes.)
+//      Zero times a value that is not finite would spread one node's NaN to nodes
+//      that do not follow it, so such inputs take the sums along the paths.
 #include "kda_device.h"
 #include "kda_launch.h"
 
@@ -34,6 +38,7 @@ namespace kda {
 namespace {
 
 constexpr int kTreeThreads = 256;
+constexpr int kInvRow = 20, kInvBytes = 16 * kInvRow * 4;  // a 16 x 16 inverse, rows 4 banks apart
 
 template <typename IO, int DK, int DV>
 struct TCfg {
@@ -50,24 +55,20 @@ struct TCfg {
 // The verify kernel's LDS, in bytes, for K nodes.  Row K stands for the state the tree
 // starts from: no key, and no decay.  u takes the place of the rows.
 struct TLay {
-  int rows, u, cd, anc, self, beta, par, depth, total;
+  int rows, u, c, d, inv, beta, par, flag, total;
   __host__ __device__ static int r16(int n) { return (n + 15) & ~15; }
-  __host__ __device__ TLay(int K, int row, int dv) {
-    const int pairs = K * (K - 1) / 2;
+  // mrow: the bytes of a row of C and D; nblk: 16-node blocks
+  __host__ __device__ TLay(int K, int row, int dv, int mrow, int nblk) {
     rows = u = 0;
-    cd = r16((K + 1) * (row > dv * 4 ? row : dv * 4));
-    anc = cd + r16(8 * pairs);
-    self = anc + r16(pairs);
-    beta = self + r16(4 * K);
+    c = r16((K + 1) * row > K * dv * 4 ? (K + 1) * row : K * dv * 4);
+    d = c + 16 * nblk * mrow;
+    inv = d + 16 * nblk * mrow;
+    beta = inv + nblk * kInvBytes;
     par = beta + r16(4 * K);
-    depth = par + r16(4 * K + 4);
-    total = depth + r16(4 * K);
+    flag = par + r16(4 * K + 4);
+    total = flag + 16;
   }
 };
-
-// beta_t c, d and the ancestor of node t's hop j upwards (0: its parent; j < t) stand at
-// first_pair(t) + j.
-__device__ __forceinline__ int first_pair(int t) { return t * (t - 1) / 2; }
 
 // The sum of x over each aligned group of G lanes, in every one of them.
 template <int CTRL>
@@ -100,13 +101,17 @@ __device__ __forceinline__ void wave_lds_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// Values up to here take the products with C, D and the inverses.
+constexpr float kPlain = 1e18f;
+
 template <typename IO, int DK, int DV, int MAXK>
-__global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 3 : 1) void kda_tree_verify_kernel(TreeParams p) {
+__global__ __launch_bounds__(kTreeThreads, MAXK <= 32 && sizeof(IO) == 2 ? 3 : 1) void kda_tree_verify_kernel(TreeParams p) {
   using C = TCfg<IO, DK, DV>;
   extern __shared__ u32x4 tree_lds[];
   char* sm = reinterpret_cast<char*>(tree_lds);
   const int K = p.K, tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
-  const TLay L(K, C::ROW, DV);
+  constexpr int NT = (MAXK + 15) / 16, MROW = 16 * NT + 4;  // blocks of 16 nodes; floats between rows of C and D
+  const TLay L(K, C::ROW, DV, 4 * MROW, NT);
   const int b = blockIdx.x / p.H, h = blockIdx.x % p.H;
   const int n = p.n_nodes ? min(max(p.n_nodes[b], 0), K) : K;
   const int page = p.pages ? p.pages[b] : b;
@@ -142,7 +147,6 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 3 : 1) void kda_tree_ver
   const int ln = lane % 16, lg = lane / 16;
   const bool stw = C::NW == 4 || wave < C::NW;  // a state wave (the others load what the last one does)
   const int col = C::CW * min(wave, C::NW - 1) + C::NTL * ln;  // its lane's first column
-  constexpr int NT = (MAXK + 15) / 16;
   colf s[DK / 16][4];
   colio rv[NT][4];
   const float* S = p.pool + ((size_t)page * p.H + h) * DK * DV + col;
@@ -172,6 +176,13 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 3 : 1) void kda_tree_ver
   auto krow = [&](int t) { return reinterpret_cast<const IO*>(row(t)); };
   auto qrow = [&](int t) { return reinterpret_cast<const IO*>(row(t) + C::QAT); };
   auto arow = [&](int t) { return reinterpret_cast<float*>(row(t) + C::AAT); };
+  float* cm = reinterpret_cast<float*>(sm + L.c);
+  float* dm = reinterpret_cast<float*>(sm + L.d);
+  int* flag = reinterpret_cast<int*>(sm + L.flag);
+  if (tid == 0) *flag = 0;
+#pragma unroll
+  for (int i = 0; i < (2 * 16 * NT * MROW / 4 + kTreeThreads - 1) / kTreeThreads; ++i)
+    if (tid + i * kTreeThreads < 2 * 16 * NT * MROW / 4) reinterpret_cast<f32x4*>(cm)[tid + i * kTreeThreads] = (f32x4)0.0f;
   for (int i = tid; i < DK; i += kTreeThreads) {
     const_cast<IO*>(krow(K))[i] = (IO)0.0f;
     arow(K)[i] = 1.0f;
@@ -195,10 +206,6 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 3 : 1) void kda_tree_ver
   const int gl = tid % C::GL, grp = tid / C::GL;
   const int i0 = 4 * gl, i1 = DK / 2 + 4 * gl;
   f32x4 P[NPG][2];
-  float2* cd = reinterpret_cast<float2*>(sm + L.cd);
-  unsigned char* anc = reinterpret_cast<unsigned char*>(sm + L.anc);
-  float* self = reinterpret_cast<float*>(sm + L.self);
-  int* depth = reinterpret_cast<int*>(sm + L.depth);
 #pragma unroll
   for (int it = 0; it < NPG; ++it) {
     const int t = it * C::GROUPS + grp;
@@ -214,12 +221,12 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 3 : 1) void kda_tree_ver
 #pragma unroll
     for (int e = 0; e < 4; ++e) dt += k0[e] * q0[e] + k1[e] * q1[e];
     dt = group_sum<C::GL>(dt);
-    int at = first_pair(t);
+    bool fine = true;
     while (r < K) {
       const f32x4 w0 = g0 * kr0, w1 = g1 * kr1;
       g0 *= ar0;
       g1 *= ar1;
-      const unsigned char who = (unsigned char)r;
+      const int who = t * MROW + r;
       r = rn;
       kr0 = lds4(krow(r) + i0);
       kr1 = lds4(krow(r) + i1);
@@ -237,14 +244,14 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 3 : 1) void kda_tree_ver
       cs = group_sum<C::GL>(cs);
       ds = group_sum<C::GL>(ds);
       if (gl == 0) {
-        cd[at] = float2{be * cs, ds};
-        anc[at] = who;
+        cm[who] = be * cs;
+        dm[who] = ds;
       }
-      ++at;
+      fine &= fabsf(be * cs) <= kPlain && fabsf(ds) <= kPlain;
     }
     if (gl == 0) {
-      self[t] = dt;
-      depth[t] = at - first_pair(t);
+      dm[t * MROW + t] = dt;
+      if (!(fine && fabsf(dt) <= kPlain)) *flag = 1;
     }
     P[it][0] = g0;
     P[it][1] = g1;
@@ -259,6 +266,29 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 3 : 1) void kda_tree_ver
     *reinterpret_cast<f32x4*>(arow(t) + i1) = P[it][1];
   }
   lds_barrier();
+
+  // wave m inverts I + C of block m: column ln of the inverse, row after row
+  if (wave < NT && 16 * wave < n) {
+    const float* cb = cm + 16 * wave * MROW + 16 * wave;
+    float inv[16];
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+      float a = t == ln ? 1.0f : 0.0f;
+#pragma unroll
+      for (int e = 0; e < t; e += 4) {
+        const f32x4 c4 = *reinterpret_cast<const f32x4*>(cb + t * MROW + e);
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+          if (e + f < t) a -= c4[f] * inv[e + f];
+      }
+      inv[t] = a;
+    }
+    float* to = reinterpret_cast<float*>(sm + L.inv + wave * kInvBytes) + ln;
+    if (lg == 0) {
+#pragma unroll
+      for (int t = 0; t < 16; ++t) to[t * kInvRow] = inv[t];
+    }
+  }
 
   // products with the state: x (of the keys) and y (of the queries), of node 16 m + 4 lg + r
   f32x4 xa[NT][C::NTL], ya[NT][C::NTL];
@@ -289,70 +319,89 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 3 : 1) void kda_tree_ver
   lds_barrier();  // keys, queries and decays are done with: u takes their place
   if (!stw) return;
 
-  // substitution, a level of the tree at a time: x, from beta (v - x) on, is a node's u
-  // as soon as the levels above it are done
-  float* us = reinterpret_cast<float*>(sm + L.u) + (size_t)(K + 1) * C::CW * wave + C::NTL * ln;  // [K + 1][CW] of this wave
-  float x[NT][4][C::NTL], y[NT][4][C::NTL];
-  int dep[NT][4], top[NT][4];  // a node's depth, and where its hop to the root stands in cd and anc
-  int deepest = 0;
+  bool fine = *flag == 0;
 #pragma unroll
   for (int m = 0; m < NT; ++m) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int t = 16 * m + 4 * lg + r, tc = min(t, n - 1);
-      dep[m][r] = t < n ? depth[tc] : -1;
-      deepest = max(deepest, dep[m][r]);
-      top[m][r] = first_pair(tc) + max(dep[m][r], 0) - 1;
-      const float be = beta[tc];
+      const int t = 16 * m + 4 * lg + r;
+      const float be = beta[min(t, n - 1)];
 #pragma unroll
       for (int j = 0; j < C::NTL; ++j) {
-        x[m][r][j] = be * (to_f32(rv[m][r][j]) - xa[m][j][r]);
-        y[m][r][j] = ya[m][j][r];
+        const float x = be * (to_f32(rv[m][r][j]) - xa[m][j][r]);
+        xa[m][j][r] = t < n ? x : 0.0f;
+        fine &= fabsf(xa[m][j][r]) <= kPlain;
       }
     }
   }
-  deepest = max(deepest, __shfl_xor(deepest, 16));
-  deepest = max(deepest, __shfl_xor(deepest, 32));
-  // (no branches on single nodes: every load of a level is in flight at once.  What a node
-  // writes before its level is written again there, row K is a spare, and a node at or above
-  // the level reads some pair and row and drops them)
-  for (int lev = 0; lev < deepest; ++lev) {
+  if (__all(fine)) {
+    // block after block of nodes: xa turns into u, ya into o
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
+      if (16 * m >= n) continue;
+      const float* crow = cm + (16 * m + ln) * MROW + 4 * lg;
+      const float* drow = dm + (16 * m + ln) * MROW + 4 * lg;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        colf w;
+      for (int mm = 0; mm < m; ++mm) {
+        const f32x4 c4 = *reinterpret_cast<const f32x4*>(crow + 16 * mm), d4 = *reinterpret_cast<const f32x4*>(drow + 16 * mm);
 #pragma unroll
-        for (int j = 0; j < C::NTL; ++j) w[j] = x[m][r][j];
-        *reinterpret_cast<colf*>(us + min(16 * m + 4 * lg + r, K) * C::CW) = w;
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int j = 0; j < C::NTL; ++j) {
+            xa[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(-c4[r], xa[mm][j][r], xa[m][j], 0, 0, 0);
+            ya[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(d4[r], xa[mm][j][r], ya[m][j], 0, 0, 0);
+          }
+      }
+      const f32x4 i4 = *reinterpret_cast<const f32x4*>(sm + L.inv + m * kInvBytes + 4 * (ln * kInvRow + 4 * lg));
+      const f32x4 d4 = *reinterpret_cast<const f32x4*>(drow + 16 * m);
+      f32x4 um[C::NTL];
+#pragma unroll
+      for (int j = 0; j < C::NTL; ++j) um[j] = (f32x4)0.0f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int j = 0; j < C::NTL; ++j) um[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(i4[r], xa[m][j][r], um[j], 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < C::NTL; ++j) {
+        xa[m][j] = um[j];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) ya[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(d4[r], um[j][r], ya[m][j], 0, 0, 0);
       }
     }
+  } else {
+    // node after node, along its path: [K][CW] of this wave in LDS
+    float* us = reinterpret_cast<float*>(sm + L.u) + (size_t)K * C::CW * wave;
+#pragma unroll
+    for (int m = 0; m < NT; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int j = 0; j < C::NTL; ++j)
+          if (16 * m + 4 * lg + r < n) us[(16 * m + 4 * lg + r) * C::CW + C::NTL * ln + j] = xa[m][j][r];
     wave_lds_order();
-    float2 w[NT][4];
-    int row[NT][4];
-#pragma unroll
-    for (int m = 0; m < NT; ++m) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int at = max(top[m][r] - lev, 0);
-        w[m][r] = cd[at];
-        row[m][r] = anc[at];
+    for (int t = 0; t < n; ++t) {
+      if (lane < C::CW) {
+        float x = us[t * C::CW + lane];
+        for (int a = par[t]; a < K; a = par[a]) x -= cm[t * MROW + a] * us[a * C::CW + lane];
+        us[t * C::CW + lane] = x;
       }
+      wave_lds_order();
     }
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const bool below = dep[m][r] > lev;
-        const colf ua = *reinterpret_cast<const colf*>(us + (below ? row[m][r] : 0) * C::CW);
+        const int t = 16 * m + 4 * lg + r;
+        if (t >= n) continue;
+        for (int a = t; a < K; a = par[a]) {
+          const float w = dm[t * MROW + a];
 #pragma unroll
-        for (int j = 0; j < C::NTL; ++j) {
-          x[m][r][j] = below ? x[m][r][j] - w[m][r].x * ua[j] : x[m][r][j];
-          y[m][r][j] = below ? y[m][r][j] + w[m][r].y * ua[j] : y[m][r][j];
+          for (int j = 0; j < C::NTL; ++j) ya[m][j][r] += w * us[a * C::CW + C::NTL * ln + j];
         }
+#pragma unroll
+        for (int j = 0; j < C::NTL; ++j) xa[m][j][r] = us[t * C::CW + C::NTL * ln + j];
       }
     }
-    wave_lds_order();
   }
 #pragma unroll
   for (int m = 0; m < NT; ++m) {
@@ -360,12 +409,11 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 3 : 1) void kda_tree_ver
     for (int r = 0; r < 4; ++r) {
       const int t = 16 * m + 4 * lg + r;
       if (t >= n) continue;
-      const float se = self[t];
       colf ut, ot;
 #pragma unroll
       for (int j = 0; j < C::NTL; ++j) {
-        ut[j] = x[m][r][j];
-        ot[j] = y[m][r][j] + se * x[m][r][j];
+        ut[j] = xa[m][j][r];
+        ot[j] = ya[m][j][r];
       }
       const size_t at = (row0 + (size_t)t * p.H) * DV + col;
       *reinterpret_cast<colf*>(p.u + (((size_t)b * p.H + h) * K + t) * DV + col) = ut;
@@ -459,7 +507,8 @@ __global__ __launch_bounds__(256) void kda_tree_commit_kernel(TreeCommitParams p
 template <typename IO, int DK, int DV, int MAXK>
 hipError_t verify_k(const TreeParams& p, hipStream_t s) {
   using C = TCfg<IO, DK, DV>;
-  const int lds = TLay(p.K, C::ROW, DV).total;
+  constexpr int NT = (MAXK + 15) / 16;
+  const int lds = TLay(p.K, C::ROW, DV, 4 * (16 * NT + 4), NT).total;
   if (lds > 65536) {  // more than the default has to be asked for
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&kda_tree_verify_kernel<IO, DK, DV, MAXK>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);

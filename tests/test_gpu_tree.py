@@ -198,3 +198,52 @@ def test_runs_twice_alike_and_side_by_side(gpu):
     torch.cuda.synchronize()
     for g in got:
         assert all(torch.equal(a, b) for a, b in zip(g, want))
+
+
+@pytest.mark.parametrize("where,value", [("v", float("nan")), ("v", float("inf")), ("v", 1e30), ("q", float("nan")), ("k", float("inf")),
+                                         ("alpha", float("nan")), ("beta", float("inf"))])
+@pytest.mark.parametrize("K", [14, 40])
+def test_values_that_are_not_finite_stay_on_their_paths(gpu, where, value, K):
+    """A drafted node whose values are not finite (or are huge) spoils the nodes that follow it, and no others:
+    those keep the bounds."""
+    kda = _kda()
+    rng = np.random.default_rng(K)
+    B, H, bad = 3, 2, 2
+    d, pool = _drafts(gpu, B, K, H, 64, 64, torch.float32, 4, 40 + K)
+    parents = [sm.random_tree(rng, K, 9) for _ in range(B)]
+    d[where][1, bad, 1] = value
+    o, u = kda.kda_tree_verify(d["q"], d["k"], d["v"], d["alpha"], d["beta"], pool, _i([3, 0, 2], gpu), _i(parents, gpu))
+    below = [t == bad for t in range(K)]
+    for t in range(K):
+        below[t] |= parents[1][t] >= 0 and below[parents[1][t]]
+    assert 1 < sum(below) < K
+    x, ho, hu, hp = {n: _host(t) for n, t in d.items()}, _host(o), _host(u), _host(pool)
+    for b, page in enumerate([3, 0, 2]):
+        for h in range(H):
+            clean = [t for t in range(K) if not ((b, h) == (1, 1) and (t == bad if where == "q" else below[t]))]
+            with np.errstate(all="ignore"):
+                r = sm.tree_run(hp[page, h], *(x[n][b, :, h] for n in ("q", "k", "v", "alpha", "beta")), parents[b])
+            sm.within(ho[b, clean, h], r["o"][clean], r["eo"][clean], sm.U, f"o of ({b}, {h})")
+            sm.within(hu[b, h][clean], r["u"][clean], r["eu"][clean], sm.U, f"u of ({b}, {h})")
+    if value != 1e30:  # and the node itself is not finite
+        assert not np.isfinite(ho[1, bad, 1]).all()
+
+
+def test_a_state_that_is_not_finite(gpu):
+    """A NaN in one column of the state spoils that column of every node, and no other."""
+    kda = _kda()
+    K = 20
+    d, pool = _drafts(gpu, 1, K, 1, 64, 128, torch.bfloat16, 1, 2)
+    par = [sm.random_tree(np.random.default_rng(1), K, 5)]
+    clean, _ = kda.kda_tree_verify(d["q"], d["k"], d["v"], d["alpha"], d["beta"], pool, None, _i(par, gpu))
+    pool[0, 0, 7, 33] = float("nan")
+    o, _ = kda.kda_tree_verify(d["q"], d["k"], d["v"], d["alpha"], d["beta"], pool, None, _i(par, gpu))
+    assert torch.isnan(o[..., 33]).all()
+    keep = torch.arange(128, device=gpu) != 33
+    assert torch.isfinite(o[..., keep]).all()
+    # (another order of the same sums: the bounds of both)
+    x = {n: _host(t) for n, t in d.items()}
+    pool[0, 0, 7, 33] = 0.0
+    r = sm.tree_run(_host(pool)[0, 0], *(x[n][0, :, 0] for n in ("q", "k", "v", "alpha", "beta")), par[0])
+    sm.within(_host(o)[0, :, 0][:, _host(keep).astype(bool)], r["o"][:, _host(keep).astype(bool)], r["eo"][:, _host(keep).astype(bool)], sm.U)
+    sm.within(_host(clean)[0, :, 0][:, _host(keep).astype(bool)], r["o"][:, _host(keep).astype(bool)], r["eo"][:, _host(keep).astype(bool)], sm.U)
