@@ -230,6 +230,7 @@ kda_status kda_tree_verify(const void* q, const void* k, const void* v, kda_dtyp
   if (B < 1 || H < 1 || K < 1 || K > KDA_MAX_TREE || n_pages < 1 || n_pages > KDA_MAX_PAGES) return KDA_ERR_SHAPE;
   if (!dim_ok(d_k) || !dim_ok(d_v)) return KDA_ERR_UNSUPPORTED;
   if (!sizes_ok(B, K, H, d_k, d_v) || !sizes_ok(n_pages, 1, H, d_k, d_v) || (!pages && n_pages < B)) return KDA_ERR_SHAPE;
+  if ((long long)K * H * std::max(d_k, d_v) >= (1LL << 30)) return KDA_ERR_SHAPE;  // (offsets within a sequence)
   if (!q || !k || !v || !alpha || !beta || !pool || !parents || !o || !u) return KDA_ERR_NULL;
   const void* ptrs[] = {q, k, v, alpha, beta, pool, pages, parents, n_nodes, o, u};
   for (const void* ptr : ptrs)

@@ -18,12 +18,13 @@
 // kda_tree_verify_kernel, one workgroup of four waves per (sequence, head):
 //   1. the keys, queries and decays of the tree's nodes, the state and the values
 //      are loaded, all in flight at once; the first three go to LDS;
-//   2. one group of d_k / 8 lanes per node walks up its path: c, d and P_t.  They
-//      fill two K x K matrices, C (beta_t c, strictly below the diagonal because a
+//   2. one group of d_k / 8 lanes per node walks up its path with the node's key
+//      and query, decayed on the way: c, d, and at the root P_t k_t and P_t q_t, which
+//      take the place of the rows in LDS.  c and d fill two K x K matrices, C (beta_t c, strictly below the diagonal because a
 //      node follows its parent) and D (d, with k_t . q_t on it), zero elsewhere;
 //   3. the 2K x d_k by d_k x d_v product runs on the fp32 matrix cores.  Each wave
 //      owns d_v / 4 columns and holds the state as the B operand straight from
-//      its loads; the A operands P_t k_t and P_t q_t are formed as they are read;
+//      its loads;
 //   4. U = (I + C)^-1 beta (V - X) and O = Y + D U, in blocks of 16 nodes, on the
 //      matrix cores too: the 16 x 16 inverses on the diagonal are one lane per
 //      column, and a block's result, as the matrix cores leave it, is the next
@@ -47,6 +48,7 @@ struct TCfg {
   static constexpr int NW = DV / CW;                   // state waves (of 4)
   // a node's row in LDS: key, query, decays, and 16 bytes by which 16 rows cover all banks
   static constexpr int QAT = DK * (int)sizeof(IO), AAT = 2 * QAT, ROW = AAT + DK * 4 + 16;
+  static constexpr int PROW = 8 * DK + 16;             // the same of a row of P_t k_t and P_t q_t
   static constexpr int GL = DK / 8;                    // lanes of a node's group
   static constexpr int GROUPS = kTreeThreads / GL;
   static_assert(NW <= 4 && NW * CW == DV, "state waves");
@@ -116,7 +118,13 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 && sizeof(IO) == 2 ? 3 : 1
   const int n = p.n_nodes ? min(max(p.n_nodes[b], 0), K) : K;
   const int page = p.pages ? p.pages[b] : b;
   if (n == 0 || !page_ok(page, p.n_pages)) return;
-  const size_t row0 = (size_t)b * K * p.H + h;  // node t: row row0 + t H of the [B][K][H][d] arrays
+  // node t: row row0 + t H of the [B][K][H][d] arrays; within a sequence 32 bits of bytes
+  const size_t row0 = (size_t)b * K * p.H + h;
+  const char* qb = static_cast<const char*>(p.q) + row0 * (DK * sizeof(IO));
+  const char* kb = static_cast<const char*>(p.k) + row0 * (DK * sizeof(IO));
+  const char* ab = reinterpret_cast<const char*>(p.alpha + row0 * DK);
+  const char* vb = static_cast<const char*>(p.v) + row0 * (DV * sizeof(IO));
+  const unsigned H = p.H;
 
   // keys, queries and decays, 16 bytes a load (indices clamped into the tree's rows, and
   // no branch: one around a load makes the compiler wait for it)
@@ -130,14 +138,14 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 && sizeof(IO) == 2 ? 3 : 1
 #pragma unroll
   for (int j = 0; j < EK; ++j) {
     const unsigned e = min(tid + j * kTreeThreads, n * CK - 1);
-    const size_t at = (row0 + (size_t)(e / CK) * p.H) * (DK * sizeof(IO)) + 16 * (e % CK);
-    rk[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.k) + at);
-    rq[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p.q) + at);
+    const unsigned at = e / CK * H * (unsigned)(DK * sizeof(IO)) + 16 * (e % CK);
+    rk[j] = *reinterpret_cast<const u32x4*>(kb + at);
+    rq[j] = *reinterpret_cast<const u32x4*>(qb + at);
   }
 #pragma unroll
   for (int j = 0; j < EA; ++j) {
     const unsigned e = min(tid + j * kTreeThreads, n * CA - 1);
-    ra[j] = *reinterpret_cast<const f32x4*>(p.alpha + (row0 + (size_t)(e / CA) * p.H) * DK + 4 * (e % CA));
+    ra[j] = *reinterpret_cast<const f32x4*>(ab + (e / CA * H * (unsigned)(DK * 4) + 16 * (e % CA)));
   }
   __builtin_amdgcn_sched_barrier(0);  // (loads are counted in order: the small ones come first)
 
@@ -159,7 +167,7 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 && sizeof(IO) == 2 ? 3 : 1
 #pragma unroll
     for (int r = 0; r < 4; ++r)
       rv[m][r] = *reinterpret_cast<const colio*>(
-          static_cast<const IO*>(p.v) + (row0 + (size_t)min(16 * m + 4 * lg + r, n - 1) * p.H) * DV + col);
+          vb + ((unsigned)min(16 * m + 4 * lg + r, n - 1) * H * (unsigned)(DV * sizeof(IO)) + (unsigned)(col * sizeof(IO))));
   }
   __builtin_amdgcn_sched_barrier(0);
 
@@ -200,70 +208,72 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 && sizeof(IO) == 2 ? 3 : 1
   }
   lds_barrier();
 
-  // up each node's path; a lane holds channels 4 gl + {0..3} and DK/2 + 4 gl + {0..3}, and
-  // reads the next ancestor's row while it works on one
+  // up each node's path; a lane holds channels 4 gl + {0..3} and DK/2 + 4 gl + {0..3} of
+  // the node's key and query, decayed so far, and reads the next ancestor's row while it
+  // works on one
   constexpr int NPG = (MAXK + C::GROUPS - 1) / C::GROUPS;
   const int gl = tid % C::GL, grp = tid / C::GL;
   const int i0 = 4 * gl, i1 = DK / 2 + 4 * gl;
-  f32x4 P[NPG][2];
+  f32x4 pk[NPG][2], pq[NPG][2];
 #pragma unroll
   for (int it = 0; it < NPG; ++it) {
     const int t = it * C::GROUPS + grp;
     if (t >= n) continue;
     int r = par[t];
-    const f32x4 k0 = lds4(krow(t) + i0), k1 = lds4(krow(t) + i1);
-    const f32x4 q0 = lds4(qrow(t) + i0), q1 = lds4(qrow(t) + i1);
-    f32x4 g0 = lds4(arow(t) + i0), g1 = lds4(arow(t) + i1);
+    f32x4 k0 = lds4(krow(t) + i0), k1 = lds4(krow(t) + i1), q0 = lds4(qrow(t) + i0), q1 = lds4(qrow(t) + i1);
+    const f32x4 a0 = lds4(arow(t) + i0), a1 = lds4(arow(t) + i1);
     f32x4 kr0 = lds4(krow(r) + i0), kr1 = lds4(krow(r) + i1), ar0 = lds4(arow(r) + i0), ar1 = lds4(arow(r) + i1);
     int rn = par[r];
     const float be = beta[t];
     float dt = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) dt += k0[e] * q0[e] + k1[e] * q1[e];
+    for (int e = 0; e < 4; ++e) {
+      dt += k0[e] * q0[e];
+      dt += k1[e] * q1[e];
+    }
     dt = group_sum<C::GL>(dt);
+    k0 *= a0, k1 *= a1, q0 *= a0, q1 *= a1;
     bool fine = true;
     while (r < K) {
-      const f32x4 w0 = g0 * kr0, w1 = g1 * kr1;
-      g0 *= ar0;
-      g1 *= ar1;
-      const int who = t * MROW + r;
-      r = rn;
-      kr0 = lds4(krow(r) + i0);
-      kr1 = lds4(krow(r) + i1);
-      ar0 = lds4(arow(r) + i0);
-      ar1 = lds4(arow(r) + i1);
-      rn = par[r];
       float cs = 0.0f, ds = 0.0f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        cs += w0[e] * k0[e];
-        ds += w0[e] * q0[e];
-        cs += w1[e] * k1[e];
-        ds += w1[e] * q1[e];
+        cs += k0[e] * kr0[e];
+        ds += q0[e] * kr0[e];
+        cs += k1[e] * kr1[e];
+        ds += q1[e] * kr1[e];
       }
-      cs = group_sum<C::GL>(cs);
+      k0 *= ar0, k1 *= ar1, q0 *= ar0, q1 *= ar1;
+      const int at = t * MROW + r;
+      r = rn;
+      kr0 = lds4(krow(r) + i0), kr1 = lds4(krow(r) + i1);
+      ar0 = lds4(arow(r) + i0), ar1 = lds4(arow(r) + i1);
+      rn = par[r];
+      cs = be * group_sum<C::GL>(cs);
       ds = group_sum<C::GL>(ds);
       if (gl == 0) {
-        cm[who] = be * cs;
-        dm[who] = ds;
+        cm[at] = cs;
+        dm[at] = ds;
       }
-      fine &= fabsf(be * cs) <= kPlain && fabsf(ds) <= kPlain;
+      fine &= fabsf(cs) <= kPlain && fabsf(ds) <= kPlain;
     }
     if (gl == 0) {
       dm[t * MROW + t] = dt;
       if (!(fine && fabsf(dt) <= kPlain)) *flag = 1;
     }
-    P[it][0] = g0;
-    P[it][1] = g1;
+    pk[it][0] = k0, pk[it][1] = k1, pq[it][0] = q0, pq[it][1] = q1;
   }
   lds_barrier();
-  // P takes the decays' place
+  // P_t k_t and P_t q_t take the rows' place
+  auto prow = [&](int t) { return reinterpret_cast<float*>(sm + L.rows + __umul24(t, C::PROW)); };
 #pragma unroll
   for (int it = 0; it < NPG; ++it) {
     const int t = it * C::GROUPS + grp;
     if (t >= n) continue;
-    *reinterpret_cast<f32x4*>(arow(t) + i0) = P[it][0];
-    *reinterpret_cast<f32x4*>(arow(t) + i1) = P[it][1];
+    *reinterpret_cast<f32x4*>(prow(t) + i0) = pk[it][0];
+    *reinterpret_cast<f32x4*>(prow(t) + i1) = pk[it][1];
+    *reinterpret_cast<f32x4*>(prow(t) + DK + i0) = pq[it][0];
+    *reinterpret_cast<f32x4*>(prow(t) + DK + i1) = pq[it][1];
   }
   lds_barrier();
 
@@ -304,14 +314,13 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 && sizeof(IO) == 2 ? 3 : 1
 #pragma unroll
       for (int kk = 0; kk < DK / 16; ++kk) {
         const int i = 16 * kk + 4 * lg;
-        const f32x4 pt = lds4(arow(t) + i);
-        const f32x4 pk = pt * lds4(krow(t) + i), pq = pt * lds4(qrow(t) + i);
+        const f32x4 ak = lds4(prow(t) + i), aq = lds4(prow(t) + DK + i);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
           for (int j = 0; j < C::NTL; ++j) {
-            xa[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(pk[e], s[kk][e][j], xa[m][j], 0, 0, 0);
-            ya[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(pq[e], s[kk][e][j], ya[m][j], 0, 0, 0);
+            xa[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(ak[e], s[kk][e][j], xa[m][j], 0, 0, 0);
+            ya[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(aq[e], s[kk][e][j], ya[m][j], 0, 0, 0);
           }
       }
     }
@@ -403,6 +412,7 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 && sizeof(IO) == 2 ? 3 : 1
       }
     }
   }
+  float* ub = p.u + ((size_t)b * p.H + h) * K * DV;
 #pragma unroll
   for (int m = 0; m < NT; ++m) {
 #pragma unroll
@@ -415,16 +425,16 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 && sizeof(IO) == 2 ? 3 : 1
         ut[j] = xa[m][j][r];
         ot[j] = ya[m][j][r];
       }
-      const size_t at = (row0 + (size_t)t * p.H) * DV + col;
-      *reinterpret_cast<colf*>(p.u + (((size_t)b * p.H + h) * K + t) * DV + col) = ut;
+      const unsigned at = (unsigned)t * H * DV + col;
+      *reinterpret_cast<colf*>(ub + (t * DV + col)) = ut;
       if (p.o_f32) {
-        *reinterpret_cast<colf*>(static_cast<float*>(p.o) + at) = ot;
+        *reinterpret_cast<colf*>(static_cast<float*>(p.o) + row0 * DV + at) = ot;
       } else {
         typedef __bf16 colb __attribute__((ext_vector_type(C::NTL)));
         colb ob;
 #pragma unroll
         for (int j = 0; j < C::NTL; ++j) ob[j] = (__bf16)ot[j];
-        *reinterpret_cast<colb*>(static_cast<__bf16*>(p.o) + at) = ob;
+        *reinterpret_cast<colb*>(static_cast<__bf16*>(p.o) + row0 * DV + at) = ob;
       }
     }
   }

@@ -543,7 +543,7 @@ kda_status kda_decode_step_paged(const void* q, const void* k, const void* v, kd
  *            NULL: K                                                    (read)
  *   o      : [B][K][H][d_v] o_dtype, o_t along the path to node t     (written)
  *   u      : [B][H][K][d_v] fp32, the write vectors kda_tree_commit needs (written)
- *   K      : 1 .. KDA_MAX_TREE;  n_pages: 1 .. KDA_MAX_PAGES
+ *   K      : 1 .. KDA_MAX_TREE;  n_pages: 1 .. KDA_MAX_PAGES;  K H max(d_k, d_v) < 2^30
  *
  * Rows of o and u behind a tree's last node, and every row of a sequence whose
  * page lies outside [0, n_pages), are left as they were.  o and u may overlap
