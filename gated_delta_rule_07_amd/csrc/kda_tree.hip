@@ -38,20 +38,20 @@
 namespace kda {
 namespace {
 
-constexpr int kTreeThreads = 256;
+constexpr int kTreeThreads = 512;
 constexpr int kInvRow = 20, kInvBytes = 16 * kInvRow * 4;  // a 16 x 16 inverse, rows 4 banks apart
 
 template <typename IO, int DK, int DV>
 struct TCfg {
-  static constexpr int NTL = DV >= 128 ? 2 : 1;        // 16-column tiles of a state wave
+  static constexpr int NTL = 1;        // 16-column tiles of a state wave
   static constexpr int CW = 16 * NTL;                  // its columns
-  static constexpr int NW = DV / CW;                   // state waves (of 4)
+  static constexpr int NW = DV / CW;                   // state waves (of 8)
   // a node's row in LDS: key, query, decays, and 16 bytes by which 16 rows cover all banks
   static constexpr int QAT = DK * (int)sizeof(IO), AAT = 2 * QAT, ROW = AAT + DK * 4 + 16;
   static constexpr int PROW = 8 * DK + 16;             // the same of a row of P_t k_t and P_t q_t
   static constexpr int GL = DK / 8;                    // lanes of a node's group
   static constexpr int GROUPS = kTreeThreads / GL;
-  static_assert(NW <= 4 && NW * CW == DV, "state waves");
+  static_assert(NW <= kTreeThreads / 64 && NW * CW == DV, "state waves");
 };
 
 // The verify kernel's LDS, in bytes, for K nodes.  Row K stands for the state the tree
@@ -107,7 +107,7 @@ __device__ __forceinline__ void wave_lds_order() {
 constexpr float kPlain = 1e18f;
 
 template <typename IO, int DK, int DV, int MAXK>
-__global__ __launch_bounds__(kTreeThreads, MAXK <= 32 && sizeof(IO) == 2 ? 3 : 1) void kda_tree_verify_kernel(TreeParams p) {
+__global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 4 : 2) void kda_tree_verify_kernel(TreeParams p) {
   using C = TCfg<IO, DK, DV>;
   extern __shared__ u32x4 tree_lds[];
   char* sm = reinterpret_cast<char*>(tree_lds);
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 && sizeof(IO) == 2 ? 3 : 1
   typedef float colf __attribute__((ext_vector_type(C::NTL)));
   typedef IO colio __attribute__((ext_vector_type(C::NTL)));
   const int ln = lane % 16, lg = lane / 16;
-  const bool stw = C::NW == 4 || wave < C::NW;  // a state wave (the others load what the last one does)
+  const bool stw = C::NW == kTreeThreads / 64 || wave < C::NW;  // a state wave (the others load what the last one does)
   const int col = C::CW * min(wave, C::NW - 1) + C::NTL * ln;  // its lane's first column
   colf s[DK / 16][4];
   colio rv[NT][4];
@@ -162,13 +162,6 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 && sizeof(IO) == 2 ? 3 : 1
   for (int kk = 0; kk < DK / 16; ++kk)
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[kk][e] = *reinterpret_cast<const colf*>(S + (size_t)(16 * kk + 4 * lg + e) * DV);
-#pragma unroll
-  for (int m = 0; m < NT; ++m) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      rv[m][r] = *reinterpret_cast<const colio*>(
-          vb + ((unsigned)min(16 * m + 4 * lg + r, n - 1) * H * (unsigned)(DV * sizeof(IO)) + (unsigned)(col * sizeof(IO))));
-  }
   __builtin_amdgcn_sched_barrier(0);
 
   int* par = reinterpret_cast<int*>(sm + L.par);
@@ -209,8 +202,7 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 && sizeof(IO) == 2 ? 3 : 1
   lds_barrier();
 
   // up each node's path; a lane holds channels 4 gl + {0..3} and DK/2 + 4 gl + {0..3} of
-  // the node's key and query, decayed so far, and reads the next ancestor's row while it
-  // works on one
+  // the node's key and query, decayed so far
   constexpr int NPG = (MAXK + C::GROUPS - 1) / C::GROUPS;
   const int gl = tid % C::GL, grp = tid / C::GL;
   const int i0 = 4 * gl, i1 = DK / 2 + 4 * gl;
@@ -222,8 +214,6 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 && sizeof(IO) == 2 ? 3 : 1
     int r = par[t];
     f32x4 k0 = lds4(krow(t) + i0), k1 = lds4(krow(t) + i1), q0 = lds4(qrow(t) + i0), q1 = lds4(qrow(t) + i1);
     const f32x4 a0 = lds4(arow(t) + i0), a1 = lds4(arow(t) + i1);
-    f32x4 kr0 = lds4(krow(r) + i0), kr1 = lds4(krow(r) + i1), ar0 = lds4(arow(r) + i0), ar1 = lds4(arow(r) + i1);
-    int rn = par[r];
     const float be = beta[t];
     float dt = 0.0f;
 #pragma unroll
@@ -235,6 +225,10 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 && sizeof(IO) == 2 ? 3 : 1
     k0 *= a0, k1 *= a1, q0 *= a0, q1 *= a1;
     bool fine = true;
     while (r < K) {
+      const f32x4 kr0 = lds4(krow(r) + i0), kr1 = lds4(krow(r) + i1);
+      const f32x4 ar0 = lds4(arow(r) + i0), ar1 = lds4(arow(r) + i1);
+      const int at = t * MROW + r;
+      r = par[r];
       float cs = 0.0f, ds = 0.0f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -244,11 +238,6 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 && sizeof(IO) == 2 ? 3 : 1
         ds += q1[e] * kr1[e];
       }
       k0 *= ar0, k1 *= ar1, q0 *= ar0, q1 *= ar1;
-      const int at = t * MROW + r;
-      r = rn;
-      kr0 = lds4(krow(r) + i0), kr1 = lds4(krow(r) + i1);
-      ar0 = lds4(arow(r) + i0), ar1 = lds4(arow(r) + i1);
-      rn = par[r];
       cs = be * group_sum<C::GL>(cs);
       ds = group_sum<C::GL>(ds);
       if (gl == 0) {
@@ -277,6 +266,14 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 && sizeof(IO) == 2 ? 3 : 1
   }
   lds_barrier();
 
+  // the values, on their way while the products run
+#pragma unroll
+  for (int m = 0; m < NT; ++m) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      rv[m][r] = *reinterpret_cast<const colio*>(
+          vb + ((unsigned)min(16 * m + 4 * lg + r, n - 1) * H * (unsigned)(DV * sizeof(IO)) + (unsigned)(col * sizeof(IO))));
+  }
   // wave m inverts I + C of block m: column ln of the inverse, row after row
   if (wave < NT && 16 * wave < n) {
     const float* cb = cm + 16 * wave * MROW + 16 * wave;
