@@ -524,15 +524,17 @@ def _raw_stream(index):
     return torch.cuda.current_stream(index).cuda_stream
 
 
-if hasattr(torch._C, "_cuda_getCurrentRawStream"):
-    _raw_stream = torch._C._cuda_getCurrentRawStream  # noqa: F811  (the same, without a Stream object)
+_current_device = torch.cuda.current_device
+if hasattr(torch._C, "_cuda_getCurrentRawStream") and hasattr(torch._C, "_cuda_getDevice"):
+    # the same without a Stream object, and without asking whether HIP is set up (a tensor is there)
+    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice  # noqa: F811
 
 
 def _run(name, index, stream, *args):
     """Call `name` of the library on device `index` (made current for the call where it is not)."""
     fn = getattr(_lib or load_library(), name)
     s = _raw_stream(index) if stream is None else stream.cuda_stream
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         st = fn(*args, s)
     else:
         with torch.cuda.device(index):
@@ -550,15 +552,21 @@ def _device_of(t, name):
     return t.get_device()
 
 
-def _need(t, name, dtype, index, shape):
+def _need_in_words(t, name, dtype, index, shape):
     """The address of t, which has to be a dense tensor of this dtype and shape on device `index`."""
-    try:
-        if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
     _check(t, name, dtype, torch.device("cuda", index))
-    raise ValueError(f"libkda: {name} must be {list(shape)}, got {list(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"libkda: {name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+try:  # the same in one compiled call; without it only the time of a call grows
+    from . import _kda_args
+except ImportError:
+    _need = _need_in_words
+else:
+    _kda_args.set_refuse(_need_in_words)
+    _need = _kda_args.need
 
 
 def _may(t, name, dtype, index, shape):
@@ -575,6 +583,8 @@ def _io_code(t, name):
 
 def _head_rows(t, name):
     """(tokens, heads, d, row stride in elements) of [n,H,d] or [B,T,H,d] rows of dense heads."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"libkda: {name} must be a torch.Tensor")
     shape, st = t.shape, t.stride()
     if len(shape) == 3:
         n, H, d = shape
@@ -605,18 +615,19 @@ def kda_qk_norm(q, k=None, *, norm: str = "l2", q_weight=None, k_weight=None, ep
     input."""
     dev = _device_of(q, "q")
     n, Hq, d, qs = _head_rows(q, "q")
+    dt = q.dtype
     code = _io_code(q, "q")
-    try:
-        nm, pr = _NORMS[norm], _PAIRINGS[pairing]
-    except (KeyError, TypeError):
-        raise ValueError('libkda: norm is "l2" or "rms", pairing "halves" or "pairs"') from None
+    nm, pr = _NORMS.get(norm), _PAIRINGS.get(pairing)
+    if nm is None or pr is None:
+        raise ValueError('libkda: norm is "l2" or "rms", pairing "halves" or "pairs"')
     kp, Hk, ks = None, 0, 0
     if k is not None:
-        if _device_of(k, "k") != dev or k.dtype is not q.dtype or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != d:
+        nk, Hk, dk, ks = _head_rows(k, "k")
+        if nk != n or dk != d or k.dtype is not dt or k.get_device() != dev or k.dim() != q.dim():
             raise ValueError("libkda: q and k must agree in tokens, head size, dtype and device")
-        _, Hk, _, ks = _head_rows(k, "k")
         kp = k.data_ptr()
-    qw, kw = _may(q_weight, "q_weight", _F32, dev, (d,)), _may(k_weight, "k_weight", _F32, dev, (d,))
+    qw = None if q_weight is None else _need(q_weight, "q_weight", _F32, dev, (d,))
+    kw = None if k_weight is None else _need(k_weight, "k_weight", _F32, dev, (d,))
     rot, pos, freq = 0, None, None
     if inv_freq is not None and inv_freq.numel():
         rot = 2 * inv_freq.numel()
@@ -627,22 +638,30 @@ def kda_qk_norm(q, k=None, *, norm: str = "l2", q_weight=None, k_weight=None, ep
         if positions.numel() != n:
             raise ValueError("libkda: positions must have one entry per token")
     if out_dtype is None:
-        out_dtype = q.dtype if q_out is None else q_out.dtype
+        out_dtype = dt if q_out is None else q_out.dtype
+    out_code = _CODES.get(out_dtype)
+    if out_code is None:
+        raise TypeError(f"libkda: outputs must be bfloat16 or float32, got {out_dtype}")
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=out_dtype, device=q.device)
-    for x, o, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
-        if x is None:
-            if o is not None:
-                raise ValueError("libkda: k_out without k")
-        elif o.dtype is not out_dtype or o.get_device() != dev or o.shape != x.shape:
-            raise ValueError(f"libkda: {name} must be shaped like its input, in the output dtype, on its device")
-    qos = _head_rows(q_out, "q_out")[3]
-    kop, kos = (None, 0) if k is None else (k_out.data_ptr(), _head_rows(k_out, "k_out")[3])
+    qop, qos = _head_out(q_out, "q_out", q, dev, out_dtype, Hq * d)
+    kop, kos = None, 0
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=out_dtype, device=k.device)
+        kop, kos = _head_out(k_out, "k_out", k, dev, out_dtype, Hk * d)
+    elif k_out is not None:
+        raise ValueError("libkda: k_out without k")
     _run("kda_qk_norm", dev, stream, q.data_ptr(), qs, kp, ks, code, nm, qw, kw, eps, q_scale, pos, freq, rot, pr,
-         q_out.data_ptr(), qos, kop, kos, _io_code(q_out, "q_out"), n, Hq, Hk, d)
+         qop, qos, kop, kos, out_code, n, Hq, Hk, d)
     return q_out, k_out
+
+
+def _head_out(o, name, x, dev, dtype, row):
+    """(address, row stride) of an output of kda_qk_norm for the input x."""
+    if o.dtype is not dtype or o.get_device() != dev or o.shape != x.shape:
+        raise ValueError(f"libkda: {name} must be shaped like its input, in the output dtype, on its device")
+    return o.data_ptr(), row if o.is_contiguous() else _head_rows(o, name)[3]
 
 
 def _table(table, ref):

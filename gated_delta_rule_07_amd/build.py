@@ -2,7 +2,7 @@
 
 Usage: ``python -m gated_delta_rule_07_amd.build`` (or ``build()`` from Python).
 Each source compiles to an object in parallel, then one shared library is linked
-next to this file.  hipcc cross-compiles for gfx950 without a GPU present.
+next to this file, and beside it a small Python helper (_kda_args.so, host code).  hipcc cross-compiles for gfx950 without a GPU present.
 """
 from __future__ import annotations
 
@@ -62,6 +62,28 @@ def _link(objs, lib: Path, verbose: bool) -> None:
     os.replace(tmp, lib)
 
 
+def _args_helper(verbose: bool) -> None:
+    """The binding's argument helper: host code against the installed PyTorch's headers."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension as ext
+
+    out = PKG / "_kda_args.so"
+    tmp = out.with_suffix(".so.tmp%d" % os.getpid())
+    libs = ext.library_paths()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", str(CSRC / "kda_args.cpp"),
+           *[f"-I{p}" for p in ext.include_paths()], f"-I{sysconfig.get_paths()['include']}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-L{p}" for p in libs],
+           "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{libs[0]}", "-o", str(tmp)]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling kda_args.cpp failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+
+
 def build(verbose: bool = False, jobs: int | None = None) -> Path:
     """Compile every source and link libkda.so; always rebuilds.
 
@@ -73,7 +95,9 @@ def build(verbose: bool = False, jobs: int | None = None) -> Path:
     jobs = jobs or min(len(SOURCES) + 1, max(1, os.cpu_count() or 1))
     units = [(s, ()) for s in SOURCES] + [("kda_api.cpp", ("-DKDA_TEST_HOOKS",))]
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        helper = ex.submit(_args_helper, verbose)
         objs = list(ex.map(lambda u: _compile(u[0], verbose, u[1]), units))
+        helper.result()
     _link(objs[:len(SOURCES)], LIB, verbose)
     _link([objs[-1]] + objs[1:len(SOURCES)], TEST_LIB, verbose)
     return LIB

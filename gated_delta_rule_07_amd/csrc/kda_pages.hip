@@ -44,7 +44,7 @@ __device__ __forceinline__ int block_scan(int x, int* sums, int* total) {
 
 __global__ __launch_bounds__(kMetaThreads) void kda_cache_fork_kernel(ForkParams p) {
   __shared__ int sums[kMetaWaves];
-  __shared__ int child[kMaxForks];  // the row a fork may start, -1: refused
+  __shared__ __align__(16) int child[kMaxForks];  // the row a fork may start, -1: refused
   __shared__ int taken[kMaxForks];  // that row holds a page
   const int tid = threadIdx.x;
   int par = -2, ch = -1;
@@ -64,13 +64,21 @@ __global__ __launch_bounds__(kMetaThreads) void kda_cache_fork_kernel(ForkParams
   }
   __syncthreads();
   bool ok = ch >= 0 && !taken[tid];
+  __syncthreads();
+  if (!ok) child[tid] = -1;
+  __syncthreads();
   // the first fork that names a child has it; a parent that is itself started
   // here was an empty row before the call
   bool empty = false;
   if (ok) {
-    for (int j = 0; j < p.n; ++j) {
-      if (j < tid && child[j] == ch) ok = false;
-      if (child[j] >= 0 && child[j] == par && !taken[j]) empty = true;
+    for (int j = 0; j < p.n; j += 4) {  // (past the last fork: -1)
+      const int4 c = *reinterpret_cast<const int4*>(child + j);
+      const int cs[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        ok &= !(j + e < tid && cs[e] == ch);
+        empty |= cs[e] >= 0 && cs[e] == par;
+      }
     }
   }
   int need = 0;

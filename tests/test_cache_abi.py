@@ -183,6 +183,28 @@ def test_binding_refusals():
         kda.kda_tree_commit(q, q, q, i, i, q, i)
 
 
+def test_argument_helper_agrees_with_its_python_form():
+    """The compiled check refuses what the Python form refuses, with its words."""
+    import gated_delta_rule_07_amd as kda
+    helper = pytest.importorskip("gated_delta_rule_07_amd._kda_args")
+    assert kda._need is helper.need
+    seen = []
+    helper.set_refuse(lambda *a: seen.append(a) or 7)
+    try:
+        x = torch.zeros(2, 3)
+        cases = [(x, "x", torch.float32, 0, (2, 3)), (None, "x", torch.float32, 0, (2, 3)), (x, "x", "f32", 0, (2, 3)),
+                 (x.to_sparse(), "x", torch.float32, 0, (2, 3)), (torch.empty(2, 3, device="meta"), "x", torch.float32, 0, (2, 3)),
+                 (x, "x", torch.float32, 0, (2, "3")), (x, "x", torch.float32, 0, [2, 3])]
+        for a in cases:
+            assert helper.need(*a) == 7 and seen[-1] == a
+        with pytest.raises(TypeError):
+            helper.need(x, "x")
+    finally:
+        helper.set_refuse(kda._need_in_words)
+    with pytest.raises(ValueError, match="HIP device"):
+        kda._need(x, "x", torch.float32, 0, (2, 3))
+
+
 # ---- the models -----------------------------------------------------------------------------------
 
 
