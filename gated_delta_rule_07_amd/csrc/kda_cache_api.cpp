@@ -24,6 +24,9 @@ kda_status launched(hipError_t e) {
   return KDA_ERR_HIP;
 }
 
+// One workgroup of up to 512 threads for each of B H states, fewer than 2^32 threads in all.
+bool states_ok(int B, int H) { return (long long)B * H <= (1LL << 22); }
+
 template <size_t N>
 bool any_overlap(Span out, const Span (&ins)[N]) {
   for (const Span& s : ins)
@@ -203,7 +206,7 @@ kda_status kda_decode_step_paged(const void* q, const void* k, const void* v, kd
   if (!dtype_ok(raw_enum(qkv_dtype)) || !dtype_ok(raw_enum(o_dtype))) return KDA_ERR_DTYPE;
   if (B < 1 || B > KDA_MAX_PAGED_SEQS || H < 1 || n_pages < 1 || n_pages > KDA_MAX_PAGES) return KDA_ERR_SHAPE;
   if (!dim_ok(d_k) || !dim_ok(d_v)) return KDA_ERR_UNSUPPORTED;
-  if (!sizes_ok(B, 1, H, d_k, d_v) || !sizes_ok(n_pages, 1, H, d_k, d_v)) return KDA_ERR_SHAPE;
+  if (!states_ok(B, H) || !sizes_ok(n_pages, 1, H, d_k, d_v)) return KDA_ERR_SHAPE;
   if (alpha) z = nullptr, A = nullptr;
   if (!q || !k || !v || (!alpha && (!z || !A)) || !beta || !pool || !pages_in || !o) return KDA_ERR_NULL;
   const void* ptrs[] = {q, k, v, alpha, z, A, beta, pool, pages_in, pages_out, o};
@@ -229,7 +232,7 @@ kda_status kda_tree_verify(const void* q, const void* k, const void* v, kda_dtyp
   if (!dtype_ok(raw_enum(qkv_dtype)) || !dtype_ok(raw_enum(o_dtype))) return KDA_ERR_DTYPE;
   if (B < 1 || H < 1 || K < 1 || K > KDA_MAX_TREE || n_pages < 1 || n_pages > KDA_MAX_PAGES) return KDA_ERR_SHAPE;
   if (!dim_ok(d_k) || !dim_ok(d_v)) return KDA_ERR_UNSUPPORTED;
-  if (!sizes_ok(B, K, H, d_k, d_v) || !sizes_ok(n_pages, 1, H, d_k, d_v) || (!pages && n_pages < B)) return KDA_ERR_SHAPE;
+  if (!states_ok(B, H) || !sizes_ok(n_pages, 1, H, d_k, d_v) || (!pages && n_pages < B)) return KDA_ERR_SHAPE;
   if ((long long)K * H * std::max(d_k, d_v) >= (1LL << 30)) return KDA_ERR_SHAPE;  // (offsets within a sequence)
   if (!q || !k || !v || !alpha || !beta || !pool || !parents || !o || !u) return KDA_ERR_NULL;
   const void* ptrs[] = {q, k, v, alpha, beta, pool, pages, parents, n_nodes, o, u};
@@ -256,7 +259,7 @@ kda_status kda_tree_commit(const void* k, kda_dtype qkv_dtype, const float* alph
   if (B < 1 || B > KDA_MAX_PAGED_SEQS || H < 1 || K < 1 || K > KDA_MAX_TREE || n_pages < 1 || n_pages > KDA_MAX_PAGES)
     return KDA_ERR_SHAPE;
   if (!dim_ok(d_k) || !dim_ok(d_v)) return KDA_ERR_UNSUPPORTED;
-  if (!sizes_ok(B, K, H, d_k, d_v) || !sizes_ok(n_pages, 1, H, d_k, d_v) || (!pages_in && n_pages < B)) return KDA_ERR_SHAPE;
+  if (!states_ok(B, H) || !sizes_ok(n_pages, 1, H, d_k, d_v) || (!pages_in && n_pages < B)) return KDA_ERR_SHAPE;
   if (!k || !alpha || !u || !parents || !last || !pool) return KDA_ERR_NULL;
   const void* ptrs[] = {k, alpha, u, parents, n_nodes, last, pool, pages_in, pages_out};
   for (const void* ptr : ptrs)

@@ -130,10 +130,25 @@ hipError_t launch_one(const HeadsParams& p, hipStream_t s) {
   const int heads = p.Hq + p.Hk;
   int tokens = std::max(1, std::min(kMaxTokens, 4 * (kThreads / G) / heads));
   while (tokens > 1 && (long long)p.n < 1024LL * tokens) tokens /= 2;
-  const unsigned grid = (unsigned)(((long long)p.n + tokens - 1) / tokens);
   const size_t lds = (size_t)tokens * (p.rot / 2) * sizeof(float2);
-  hipLaunchKernelGGL((kda_heads_kernel<IO, OUT, G>), dim3(grid), dim3(kThreads), lds, s, p, tokens);
-  return hipGetLastError();
+  // (a launch has fewer than 2^32 threads: longer calls in slices)
+  const long long slice = (1LL << 23) * tokens;
+  for (long long t = 0; t < p.n; t += slice) {
+    HeadsParams c = p;
+    c.n = (int)std::min(slice, (long long)p.n - t);
+    c.q = static_cast<const IO*>(p.q) + t * p.q_stride;
+    c.q_out = static_cast<OUT*>(p.q_out) + t * p.q_out_stride;
+    if (p.Hk) {
+      c.k = static_cast<const IO*>(p.k) + t * p.k_stride;
+      c.k_out = static_cast<OUT*>(p.k_out) + t * p.k_out_stride;
+    }
+    if (p.rot) c.positions = p.positions + t;
+    hipLaunchKernelGGL((kda_heads_kernel<IO, OUT, G>), dim3((unsigned)((c.n + tokens - 1) / tokens)), dim3(kThreads), lds,
+                       s, c, tokens);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename IO, typename OUT>

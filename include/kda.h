@@ -508,7 +508,7 @@ kda_status kda_cache_copy(const void* src, void* dst, size_t page_bytes, int n_l
  *   pages_out: [B] int32, DEVICE memory (read), or NULL: each state is updated in
  *              place.  Another page keeps the state before the step as well (a
  *              fork without a copy of its own).
- *   B        : 1 .. KDA_MAX_PAGED_SEQS, n_pages: 1 .. KDA_MAX_PAGES
+ *   B        : 1 .. KDA_MAX_PAGED_SEQS, n_pages: 1 .. KDA_MAX_PAGES;  B H <= 2^22
  *
  * A sequence with a page outside [0, n_pages) is passed over -- its row of o and
  * the pool are left as they were -- which is how a captured batch is padded; and
@@ -543,7 +543,8 @@ kda_status kda_decode_step_paged(const void* q, const void* k, const void* v, kd
  *            NULL: K                                                    (read)
  *   o      : [B][K][H][d_v] o_dtype, o_t along the path to node t     (written)
  *   u      : [B][H][K][d_v] fp32, the write vectors kda_tree_commit needs (written)
- *   K      : 1 .. KDA_MAX_TREE;  n_pages: 1 .. KDA_MAX_PAGES;  K H max(d_k, d_v) < 2^30
+ *   K      : 1 .. KDA_MAX_TREE;  n_pages: 1 .. KDA_MAX_PAGES;  B H <= 2^22 and
+ *            K H max(d_k, d_v) < 2^30
  *
  * Rows of o and u behind a tree's last node, and every row of a sequence whose
  * page lies outside [0, n_pages), are left as they were.  o and u may overlap
@@ -564,7 +565,8 @@ kda_status kda_tree_verify(const void* q, const void* k, const void* v, kda_dtyp
  *   last     : [B] int32, DEVICE memory; a value outside [0, n_nodes[b]) accepts
  *              nothing (the state as it was)                             (read)
  *   pool, pages_in, pages_out, B: as kda_decode_step_paged, with its rules for pages
- *              out of range and shared pages; pages_in NULL: page b (n_pages >= B)
+ *              out of range and shared pages; pages_in NULL: page b (n_pages >= B).  K: 1 ..
+ *              KDA_MAX_TREE, B H <= 2^22
  */
 kda_status kda_tree_commit(const void* k, kda_dtype qkv_dtype, const float* alpha, const float* u, const int* parents,
                            const int* n_nodes, const int* last, float* pool, int n_pages, const int* pages_in,

@@ -117,7 +117,7 @@ def _decode(lib, **over):
 
 @pytest.mark.parametrize("over,code", [
     (dict(dt=2), 3), (dict(odt=9), 3), (dict(B=0), 2), (dict(B=4097), 2), (dict(H=0), 2), (dict(P=0), 2), (dict(P=65537), 2),
-    (dict(dk=48), 4), (dict(dv=256), 4), (dict(alpha=None), 1), (dict(alpha=None, z=_a(3)), 1), (dict(pi=None), 1), (dict(o=None), 1),
+    (dict(B=4096, H=1025), 2), (dict(dk=48), 4), (dict(dv=256), 4), (dict(alpha=None), 1), (dict(alpha=None, z=_a(3)), 1), (dict(pi=None), 1), (dict(o=None), 1),
     (dict(pool=None), 1), (dict(pi=_a(6, 4)), 5), (dict(o=_a(5, 1 << 16)), 6), (dict(o=_a(6)), 6), (dict(po=_a(5)), 6),
     (dict(q=_a(5, 16)), 6), (dict(alpha=None, z=_a(3), A=_a(8)), 6),
 ])
@@ -135,7 +135,8 @@ def _verify(lib, **over):
 
 @pytest.mark.parametrize("over,code", [
     (dict(dt=5), 3), (dict(odt=2), 3), (dict(B=0), 2), (dict(K=0), 2), (dict(K=65), 2), (dict(H=-1), 2), (dict(P=0), 2),
-    (dict(pages=None, P=3), 2), (dict(dk=24), 4), (dict(dv=8), 4), (dict(par=None), 1), (dict(u=None), 1), (dict(alpha=None), 1),
+    (dict(pages=None, P=3), 2), (dict(B=1 << 12, H=1025), 2),
+    (dict(K=64, H=1 << 17), 2), (dict(dk=24), 4), (dict(dv=8), 4), (dict(par=None), 1), (dict(u=None), 1), (dict(alpha=None), 1),
     (dict(u=_a(10, 4)), 5), (dict(u=_a(9)), 6), (dict(o=_a(5)), 6), (dict(u=_a(3)), 6), (dict(o=_a(7, 128)), 6),
 ])
 def test_verify_refusals(over, code):
@@ -151,7 +152,7 @@ def _commit(lib, **over):
 
 
 @pytest.mark.parametrize("over,code", [
-    (dict(dt=3), 3), (dict(B=4097), 2), (dict(K=65), 2), (dict(P=0), 2), (dict(pi=None, P=3), 2), (dict(dk=100), 4),
+    (dict(dt=3), 3), (dict(B=4097), 2), (dict(K=65), 2), (dict(P=0), 2), (dict(pi=None, P=3), 2), (dict(B=4096, H=1025), 2), (dict(dk=100), 4),
     (dict(last=None), 1), (dict(u=None), 1), (dict(last=_a(9, 8)), 5), (dict(u=_a(5)), 6), (dict(last=_a(5, 64)), 6),
     (dict(po=_a(5, 1024)), 6),
 ])
