@@ -15,7 +15,7 @@
 // is scalars.  G_ts is a running product along the path: no division, so a
 // channel that has decayed to nothing (or alpha = 0) needs no care.
 //
-// kda_tree_verify_kernel, one workgroup of four waves per (sequence, head):
+// kda_tree_verify_kernel, one workgroup of eight waves per (sequence, head):
 //   1. the keys, queries and decays of the tree's nodes, the state and the values
 //      are loaded, all in flight at once; the first three go to LDS;
 //   2. one group of d_k / 8 lanes per node walks up its path with the node's key
@@ -23,7 +23,7 @@
 //      take the place of the rows in LDS.  c and d fill two K x K matrices, C (beta_t c, strictly below the diagonal because a
 //      node follows its parent) and D (d, with k_t . q_t on it), zero elsewhere;
 //   3. the 2K x d_k by d_k x d_v product runs on the fp32 matrix cores.  Each wave
-//      owns d_v / 4 columns and holds the state as the B operand straight from
+//      owns 16 columns and holds the state as the B operand straight from
 //      its loads;
 //   4. U = (I + C)^-1 beta (V - X) and O = Y + D U, in blocks of 16 nodes, on the
 //      matrix cores too: the 16 x 16 inverses on the diagonal are one lane per
@@ -32,6 +32,20 @@
 //      LDS instead took 8 of 20 us on deep trees of 63 nodes.)
 //      Zero times a value that is not finite would spread one node's NaN to nodes
 //      that do not follow it, so such inputs take the sums along the paths.
+//
+// Measured, 64 sequences of 32 heads of 128, trees of 24 to 32 nodes 6 deep, bf16: 80 us,
+// for 252 MB (47 us at a copy's rate) and 256 + 48 fp32 matrix instructions a wave pair, 35 us
+// of the matrix cores at the 2.2 GHz that the launch runs at.  The loads alone take 40 us,
+// and the kernel without the first product 58 us: what is lost is overlap, two workgroups
+// of 47 KB of LDS and 64 KB of state in registers a compute unit.  Trees of 63 nodes, 12 deep, on
+// 120 fp32 states of 64 x 64: 13.5 us (33.7 us substituting node after node).  One tree of 8
+// nodes on 8 states: 7.4 us.  Tried and no faster on the first: four waves with two column tiles
+// each and three workgroups a compute unit (81 us, and 15.0 and 8.0 us on the others), a
+// persistent grid that loads the next state during the substitution (96 us), registers
+// cut to 80 for three workgroups of eight waves (105 us, spills).
+//
+// kda_tree_commit_kernel reads and writes a state as the decode step does: 45 us for the 2,048
+// states above (275 MB, 6.1 TB/s with what the verify left in the caches).
 #include "kda_device.h"
 #include "kda_launch.h"
 
@@ -43,7 +57,7 @@ constexpr int kInvRow = 20, kInvBytes = 16 * kInvRow * 4;  // a 16 x 16 inverse,
 
 template <typename IO, int DK, int DV>
 struct TCfg {
-  static constexpr int NTL = 1;        // 16-column tiles of a state wave
+  static constexpr int NTL = 1;                        // 16-column tiles of a state wave
   static constexpr int CW = 16 * NTL;                  // its columns
   static constexpr int NW = DV / CW;                   // state waves (of 8)
   // a node's row in LDS: key, query, decays, and 16 bytes by which 16 rows cover all banks
