@@ -560,13 +560,12 @@ def _need_in_words(t, name, dtype, index, shape):
     return t.data_ptr()
 
 
-try:  # the same in one compiled call; without it only the time of a call grows
+try:  # the same in one compiled call; without it (or with an older build of it) only the time of a call grows
     from . import _kda_args
-except ImportError:
-    _need = _need_in_words
-else:
+    _need, _rows = _kda_args.need, _kda_args.rows
     _kda_args.set_refuse(_need_in_words)
-    _need = _kda_args.need
+except (ImportError, AttributeError):
+    _need, _rows = _need_in_words, lambda t, dtype, index: None
 
 
 def _may(t, name, dtype, index, shape):
@@ -581,10 +580,13 @@ def _io_code(t, name):
     return code
 
 
-def _head_rows(t, name):
-    """(tokens, heads, d, row stride in elements) of [n,H,d] or [B,T,H,d] rows of dense heads."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"libkda: {name} must be a torch.Tensor")
+def _head_rows(t, name, dtype, index):
+    """(address, tokens, heads, d, row stride in elements) of [n,H,d] or [B,T,H,d] rows of dense heads."""
+    got = _rows(t, dtype, index)
+    if got is not None:
+        return got
+    if _device_of(t, name) != index or t.dtype != dtype:
+        raise ValueError(f"libkda: {name} must be {dtype} on device {index}, got {t.dtype} on {t.device}")
     shape, st = t.shape, t.stride()
     if len(shape) == 3:
         n, H, d = shape
@@ -598,7 +600,7 @@ def _head_rows(t, name):
         raise ValueError(f"libkda: {name} must be [n,H,d] or [B,T,H,d]")
     if n and ((st[-1] != 1 and d > 1) or (st[-2] != d and H > 1)):
         raise ValueError(f"libkda: the heads of a token of {name} must be dense")
-    return n, H, d, row
+    return t.data_ptr(), n, H, d, row
 
 
 def kda_qk_norm(q, k=None, *, norm: str = "l2", q_weight=None, k_weight=None, eps: float = 1e-6, q_scale: float = 1.0,
@@ -614,18 +616,17 @@ def kda_qk_norm(q, k=None, *, norm: str = "l2", q_weight=None, k_weight=None, ep
     at the end.  The outputs are dense in ``out_dtype`` (the inputs' by default) unless given; each may be its
     input."""
     dev = _device_of(q, "q")
-    n, Hq, d, qs = _head_rows(q, "q")
     dt = q.dtype
     code = _io_code(q, "q")
+    qp, n, Hq, d, qs = _head_rows(q, "q", dt, dev)
     nm, pr = _NORMS.get(norm), _PAIRINGS.get(pairing)
     if nm is None or pr is None:
         raise ValueError('libkda: norm is "l2" or "rms", pairing "halves" or "pairs"')
     kp, Hk, ks = None, 0, 0
     if k is not None:
-        nk, Hk, dk, ks = _head_rows(k, "k")
-        if nk != n or dk != d or k.dtype is not dt or k.get_device() != dev or k.dim() != q.dim():
-            raise ValueError("libkda: q and k must agree in tokens, head size, dtype and device")
-        kp = k.data_ptr()
+        kp, nk, Hk, dk, ks = _head_rows(k, "k", dt, dev)
+        if nk != n or dk != d or k.dim() != q.dim():
+            raise ValueError("libkda: q and k must agree in tokens and head size")
     qw = None if q_weight is None else _need(q_weight, "q_weight", _F32, dev, (d,))
     kw = None if k_weight is None else _need(k_weight, "k_weight", _F32, dev, (d,))
     rot, pos, freq = 0, None, None
@@ -644,24 +645,25 @@ def kda_qk_norm(q, k=None, *, norm: str = "l2", q_weight=None, k_weight=None, ep
         raise TypeError(f"libkda: outputs must be bfloat16 or float32, got {out_dtype}")
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
-    qop, qos = _head_out(q_out, "q_out", q, dev, out_dtype, Hq * d)
+    qop, qos = _head_out(q_out, "q_out", q, dev, out_dtype)
     kop, kos = None, 0
     if k is not None:
         if k_out is None:
             k_out = torch.empty(k.shape, dtype=out_dtype, device=k.device)
-        kop, kos = _head_out(k_out, "k_out", k, dev, out_dtype, Hk * d)
+        kop, kos = _head_out(k_out, "k_out", k, dev, out_dtype)
     elif k_out is not None:
         raise ValueError("libkda: k_out without k")
-    _run("kda_qk_norm", dev, stream, q.data_ptr(), qs, kp, ks, code, nm, qw, kw, eps, q_scale, pos, freq, rot, pr,
+    _run("kda_qk_norm", dev, stream, qp, qs, kp, ks, code, nm, qw, kw, eps, q_scale, pos, freq, rot, pr,
          qop, qos, kop, kos, out_code, n, Hq, Hk, d)
     return q_out, k_out
 
 
-def _head_out(o, name, x, dev, dtype, row):
+def _head_out(o, name, x, dev, dtype):
     """(address, row stride) of an output of kda_qk_norm for the input x."""
-    if o.dtype is not dtype or o.get_device() != dev or o.shape != x.shape:
-        raise ValueError(f"libkda: {name} must be shaped like its input, in the output dtype, on its device")
-    return o.data_ptr(), row if o.is_contiguous() else _head_rows(o, name)[3]
+    op, _, _, _, row = _head_rows(o, name, dtype, dev)
+    if o.shape != x.shape:
+        raise ValueError(f"libkda: {name} must be shaped like its input")
+    return op, row
 
 
 def _table(table, ref):

@@ -5,6 +5,10 @@
 //   need(tensor, name, dtype, device_index, shape) -> address
 // A tensor that is not a dense HIP tensor of this dtype, device and shape goes to the
 // callable given to set_refuse with the same arguments, which says what is wrong.
+//
+//   rows(tensor, dtype, device_index) -> (address, tokens, heads, d, row stride) or None
+// of a HIP tensor [n,H,d] or [B,T,H,d] of this dtype and device whose heads are dense and
+// whose token rows are evenly spaced; None for any other.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -48,7 +52,32 @@ PyObject* need(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return PyObject_Vectorcall(g_refuse, args, n, nullptr);
 }
 
+PyObject* rows(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 3) {
+    PyErr_SetString(PyExc_TypeError, "rows(tensor, dtype, device_index)");
+    return nullptr;
+  }
+  if (!THPVariable_Check(args[0]) || !THPDtype_Check(args[1]) || !PyLong_Check(args[2])) Py_RETURN_NONE;
+  try {
+    const at::Tensor& t = THPVariable_Unpack(args[0]);
+    const int64_t dim = t.defined() && t.layout() == at::kStrided ? t.dim() : 0;
+    if (!t.is_cuda() || t.scalar_type() != reinterpret_cast<THPDtype*>(args[1])->scalar_type ||
+        t.get_device() != PyLong_AsLongLong(args[2]) || (dim != 3 && dim != 4))
+      Py_RETURN_NONE;
+    const int64_t d = t.size(dim - 1), H = t.size(dim - 2), T = t.size(dim - 3), B = dim == 4 ? t.size(0) : 1;
+    const int64_t row = dim == 4 && T <= 1 ? t.stride(0) : t.stride(dim - 3);
+    if (B * T > 0 && ((d > 1 && t.stride(dim - 1) != 1) || (H > 1 && t.stride(dim - 2) != d))) Py_RETURN_NONE;
+    if (B > 1 && T > 1 && t.stride(0) != T * row) Py_RETURN_NONE;
+    return Py_BuildValue("(KLLLL)", (unsigned long long)(uintptr_t)t.data_ptr(), (long long)(B * T), (long long)H, (long long)d,
+                         (long long)row);
+  } catch (...) {
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
+}
+
 PyMethodDef methods[] = {
+    {"rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(rows)), METH_FASTCALL, nullptr},
     {"need", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(need)), METH_FASTCALL, nullptr},
     {"set_refuse", set_refuse, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};

@@ -124,3 +124,72 @@ def test_tree_step_and_decode_replayed(gpu):
         step(*other)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((pool, o, u, od), other))
+
+
+@pytest.mark.parametrize("helper", [True, False])
+def test_binding_refuses_what_does_not_fit(gpu, helper, monkeypatch):
+    """Shapes, types, strides and devices that do not fit raise before the library is called, with the compiled
+    argument helper and without it; calls that fit give the same results both ways."""
+    kda = _kda()
+    if helper:
+        assert kda._need is not kda._need_in_words, "the argument helper is not built"
+    else:
+        monkeypatch.setattr(kda, "_need", kda._need_in_words)
+        monkeypatch.setattr(kda, "_rows", lambda t, dtype, index: None)
+    f = lambda *s, dtype=torch.float32: torch.randn(*s, device=gpu).to(dtype)  # noqa: E731
+    q, bf = f(6, 4, 32), f(6, 4, 32, dtype=torch.bfloat16)
+    for bad in (dict(q=q[:, :, ::2]), dict(q=q[:, ::2]), dict(q=q[0]), dict(q=q.double()), dict(q=q, k=bf), dict(q=q, k=q[:5]),
+                dict(q=q, k=f(6, 4, 16)), dict(q=q, k=q.cpu()), dict(q=q, norm="l1"), dict(q=q, pairing=0),
+                dict(q=q, q_weight=f(31)), dict(q=q, inv_freq=f(8)), dict(q=q, inv_freq=f(8), positions=_i([1, 2], gpu)),
+                dict(q=q, q_out=f(6, 4, 16)), dict(q=q, q_out=bf, out_dtype=torch.float32), dict(q=q, out_dtype=torch.float16),
+                dict(q=f(3, 4, 2, 32)[:, ::2].transpose(0, 1), k=None), dict(q=q, k_out=q)):
+        with pytest.raises((ValueError, TypeError)):
+            kda.kda_qk_norm(**bad)
+    with pytest.raises(kda.KdaError, match="ALIAS"):
+        kda.kda_qk_norm(q, q.clone(), k_out=q)
+    with pytest.raises(kda.KdaError, match="UNSUPPORTED"):
+        kda.kda_qk_norm(f(2, 2, 20))
+    table, ref, one = _i([[0, 1], [-1, -1]], gpu), _i([1, 1, 0], gpu), _i([1], gpu)
+    for call in (lambda: kda.kda_cache_fork(table, ref, one, _i([0, 1], gpu)), lambda: kda.kda_cache_fork(table.t(), ref, one, one),
+                 lambda: kda.kda_cache_fork(table, ref.float(), one, one), lambda: kda.kda_cache_fork(table, ref, one, one, 2, moves=_i([[0, 0]], gpu)),
+                 lambda: kda.kda_cache_free(table, ref, one.long()), lambda: kda.kda_cache_free(table[0], ref, one),
+                 lambda: kda.kda_cache_compact(table, ref, table_out=table[:1]), lambda: kda.kda_cache_compact(table, ref, moves=one),
+                 lambda: kda.kda_cache_copy(q, _i([0, 1], gpu)), lambda: kda.kda_cache_copy(q, _i([[0, 1]], gpu), src=bf),
+                 lambda: kda.kda_cache_copy(q, _i([[0, 1]], gpu), n_layers=3), lambda: kda.kda_cache_copy(q, _i([[0, 1]], gpu), src=f(6, 4, 16))):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+    with pytest.raises(kda.KdaError, match="SHAPE"):
+        kda.kda_cache_fork(table, ref, one, one, 3)
+    assert table.tolist() == [[0, 1], [-1, -1]] and ref.tolist() == [1, 1, 0]
+    # calls that fit
+    y, _ = kda.kda_qk_norm(q.reshape(2, 3, 4, 32))
+    assert torch.allclose(y.reshape(6, 4, 32), q / q.norm(dim=-1, keepdim=True), atol=1e-5)
+    moves, n = kda.kda_cache_fork(table, ref, _i([0], gpu), one)
+    assert table.tolist() == [[0, 1], [2, 1]] and ref.tolist() == [1, 2, 1] and int(n) == 1
+    pool = f(3, 2, 16, 16)
+    kda.kda_cache_copy(pool, moves, n)
+    tok = {m: f(1, 2, 16) for m in ("q", "k", "v")}
+    o = kda.kda_decode_step_paged(tok["q"], tok["k"], tok["v"], torch.full((1, 2, 16), 0.5, device=gpu), f(1, 2), pool, _i([2], gpu))
+    assert torch.isfinite(o).all() and not torch.equal(pool[2], pool[0])
+    with pytest.raises((ValueError, TypeError)):
+        kda.kda_decode_step_paged(tok["q"], tok["k"], tok["v"], None, f(1, 2), pool, _i([2], gpu))
+    with pytest.raises((ValueError, TypeError)):
+        kda.kda_tree_verify(tok["q"], tok["k"], tok["v"], tok["q"], f(1, 2), pool, None, one)
+
+
+def test_head_norms_feed_the_recurrence(gpu):
+    """Keys as a fused projection leaves them, normalised in place and prefilled: the oracle on the same keys."""
+    import kda_inputs as ki
+    from kda_check import assert_close, gpu_o_heads, gpu_s_heads, oracle_prefill
+    kda = _kda()
+    B, T, H, d = 2, 130, 3, 64
+    x = ki.make_prefill(B, T, H, d, d, torch.bfloat16, 3.0, 0.1, seed=5, device=gpu)
+    rows = torch.randn(B, T, 3 * H, d, device=gpu).to(torch.bfloat16)
+    q, k = rows[:, :, :H], rows[:, :, H:2 * H]
+    x["q"], x["k"] = kda.kda_qk_norm(q, k, q_scale=d ** -0.5)
+    x["v"] = rows[:, :, 2 * H:].contiguous()
+    o, S = kda.kda_chunk_fwd(x["q"], x["k"], x["v"], x["alpha"], x["beta"], x["S0"])
+    torch.cuda.synchronize()
+    ro, rs = oracle_prefill(x)
+    assert_close(gpu_o_heads(o), ro, True, "o")
+    assert_close(gpu_s_heads(S), rs, True, "S_T")
