@@ -94,10 +94,12 @@ def test_a_turn_of_a_server(gpu):
             assert np.abs(pools[layer, page].cpu().numpy() - ref_states[layer, "row", b]).max() < 2e-4
 
 
-def test_tree_step_and_decode_replayed(gpu):
-    """One graph with the norms, a tree step and a decode; every replay equals the eager calls on the same lists."""
+@pytest.mark.parametrize("K", [24, 64])
+def test_tree_step_and_decode_replayed(gpu, K):
+    """One graph with a tree step (the largest takes more LDS than a launch has by default) and a decode; every
+    replay equals the eager calls on the same lists."""
     kda = _kda()
-    B, K, H, dk, dv, P = 4, 24, 4, 128, 128, 9
+    B, H, dk, dv, P = 4, 4, 128, 128, 9
     rng = np.random.default_rng(2)
     g = torch.Generator(device=gpu).manual_seed(3)
     x, y = _tokens(kda, gpu, g, (B, K), H, dk, dv), _tokens(kda, gpu, g, (B, 1), H, dk, dv)

@@ -247,3 +247,32 @@ def test_a_state_that_is_not_finite(gpu):
     r = sm.tree_run(_host(pool)[0, 0], *(x[n][0, :, 0] for n in ("q", "k", "v", "alpha", "beta")), par[0])
     sm.within(_host(o)[0, :, 0][:, _host(keep).astype(bool)], r["o"][:, _host(keep).astype(bool)], r["eo"][:, _host(keep).astype(bool)], sm.U)
     sm.within(_host(clean)[0, :, 0][:, _host(keep).astype(bool)], r["o"][:, _host(keep).astype(bool)], r["eo"][:, _host(keep).astype(bool)], sm.U)
+
+
+@pytest.mark.parametrize("K", [1, 9, 32, 64])
+def test_captured_before_its_first_eager_call(gpu, K):
+    """A shape whose first call is inside a capture, from another thread's stream, replayed on new trees."""
+    import threading
+    kda = _kda()
+    rng = np.random.default_rng(K)
+    B, H = 2, 3
+    d, pool = _drafts(gpu, B, K, H, 32, 64, torch.float32, 3, K)
+    par = _i([sm.random_tree(rng, K, 5) for _ in range(B)], gpu)
+    o, u = torch.zeros(B, K, H, 64, device=gpu), torch.zeros(B, H, K, 64, device=gpu)
+    graph = torch.cuda.CUDAGraph()
+
+    def capture():
+        with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+            kda.kda_tree_verify(d["q"], d["k"], d["v"], d["alpha"], d["beta"], pool, None, par, o=o, u=u)
+
+    torch.cuda.synchronize()
+    t = threading.Thread(target=capture)
+    t.start()
+    t.join()
+    for _ in range(3):
+        par.copy_(_i([sm.random_tree(rng, K, 5) for _ in range(B)], gpu))
+        d["q"].mul_(1.25)
+        graph.replay()
+        wo, wu = kda.kda_tree_verify(d["q"], d["k"], d["v"], d["alpha"], d["beta"], pool, None, par)
+        torch.cuda.synchronize()
+        assert torch.equal(o, wo) and torch.equal(u, wu)
