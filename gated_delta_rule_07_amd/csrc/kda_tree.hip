@@ -31,7 +31,8 @@
 //      product's B operand.  (Substituting level after level of the tree through
 //      LDS instead took 8 of 20 us on deep trees of 63 nodes.)
 //      Zero times a value that is not finite would spread one node's NaN to nodes
-//      that do not follow it, so such inputs take the sums along the paths.
+//      that do not follow it, so from a block on whose right-hand sides or u pass 1e18 (as any
+//      do where C, D, an inverse or an input has left fp32) a wave takes the sums along the paths.
 //
 // Measured, 64 sequences of 32 heads of 128, trees of 24 to 32 nodes 6 deep, bf16: 80 us,
 // for 252 MB (47 us at a copy's rate) and 256 + 48 fp32 matrix instructions a wave pair, 35 us
@@ -117,7 +118,8 @@ __device__ __forceinline__ void wave_lds_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// Values up to here take the products with C, D and the inverses.
+// Entries of C and D, right-hand sides and write vectors up to here take the products with C, D and the
+// inverses: sums of 64 products of two of them stay inside fp32.
 constexpr float kPlain = 1e18f;
 
 template <typename IO, int DK, int DV, int MAXK>
@@ -354,42 +356,53 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 4 : 2) void kda_tree_ver
       }
     }
   }
-  if (__all(fine)) {
-    // block after block of nodes: xa turns into u, ya into o
+  // block after block of nodes: xa turns into u, ya into o, as long as u stays below kPlain too (it grows by up to
+  // |c| a level, and the inverses with it: an entry that has left fp32 makes its row of um infinite or NaN)
+  bool plain = __all(fine);
+  int done = 0;  // blocks whose u and o stand
 #pragma unroll
-    for (int m = 0; m < NT; ++m) {
-      if (16 * m >= n) continue;
-      const float* crow = cm + (16 * m + ln) * MROW + 4 * lg;
-      const float* drow = dm + (16 * m + ln) * MROW + 4 * lg;
+  for (int m = 0; m < NT; ++m) {
+    if (16 * m >= n || !plain) continue;
+    const float* crow = cm + (16 * m + ln) * MROW + 4 * lg;
+    const float* drow = dm + (16 * m + ln) * MROW + 4 * lg;
 #pragma unroll
-      for (int mm = 0; mm < m; ++mm) {
-        const f32x4 c4 = *reinterpret_cast<const f32x4*>(crow + 16 * mm), d4 = *reinterpret_cast<const f32x4*>(drow + 16 * mm);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int j = 0; j < C::NTL; ++j) {
-            xa[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(-c4[r], xa[mm][j][r], xa[m][j], 0, 0, 0);
-            ya[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(d4[r], xa[mm][j][r], ya[m][j], 0, 0, 0);
-          }
-      }
-      const f32x4 i4 = *reinterpret_cast<const f32x4*>(sm + L.inv + m * kInvBytes + 4 * (ln * kInvRow + 4 * lg));
-      const f32x4 d4 = *reinterpret_cast<const f32x4*>(drow + 16 * m);
-      f32x4 um[C::NTL];
-#pragma unroll
-      for (int j = 0; j < C::NTL; ++j) um[j] = (f32x4)0.0f;
+    for (int mm = 0; mm < m; ++mm) {
+      const f32x4 c4 = *reinterpret_cast<const f32x4*>(crow + 16 * mm), d4 = *reinterpret_cast<const f32x4*>(drow + 16 * mm);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int j = 0; j < C::NTL; ++j) um[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(i4[r], xa[m][j][r], um[j], 0, 0, 0);
-#pragma unroll
-      for (int j = 0; j < C::NTL; ++j) {
-        xa[m][j] = um[j];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) ya[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(d4[r], um[j][r], ya[m][j], 0, 0, 0);
-      }
+        for (int j = 0; j < C::NTL; ++j) {
+          xa[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(-c4[r], xa[mm][j][r], xa[m][j], 0, 0, 0);
+          ya[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(d4[r], xa[mm][j][r], ya[m][j], 0, 0, 0);
+        }
     }
-  } else {
-    // node after node, along its path: [K][CW] of this wave in LDS
+    const f32x4 i4 = *reinterpret_cast<const f32x4*>(sm + L.inv + m * kInvBytes + 4 * (ln * kInvRow + 4 * lg));
+    const f32x4 d4 = *reinterpret_cast<const f32x4*>(drow + 16 * m);
+    f32x4 um[C::NTL];
+#pragma unroll
+    for (int j = 0; j < C::NTL; ++j) um[j] = (f32x4)0.0f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int j = 0; j < C::NTL; ++j) um[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(i4[r], xa[m][j][r], um[j], 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < C::NTL; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) fine &= fabsf(um[j][r]) <= kPlain;
+    plain = __all(fine);
+    if (!plain) continue;
+    done = m + 1;
+#pragma unroll
+    for (int j = 0; j < C::NTL; ++j) {
+      xa[m][j] = um[j];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) ya[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(d4[r], um[j][r], ya[m][j], 0, 0, 0);
+    }
+  }
+  if (!plain) {
+    // from the block that was not plain on node after node, along its path: [K][CW] of this wave in LDS.  That block's xa
+    // and ya hold the products with the blocks before it already, the later blocks' none.
+    const int t0 = 16 * done;
     float* us = reinterpret_cast<float*>(sm + L.u) + (size_t)K * C::CW * wave;
 #pragma unroll
     for (int m = 0; m < NT; ++m)
@@ -399,21 +412,23 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 4 : 2) void kda_tree_ver
         for (int j = 0; j < C::NTL; ++j)
           if (16 * m + 4 * lg + r < n) us[(16 * m + 4 * lg + r) * C::CW + C::NTL * ln + j] = xa[m][j][r];
     wave_lds_order();
-    for (int t = 0; t < n; ++t) {
+    for (int t = t0; t < n; ++t) {
+      const int from = t < t0 + 16 ? t0 : 0;
       if (lane < C::CW) {
         float x = us[t * C::CW + lane];
-        for (int a = par[t]; a < K; a = par[a]) x -= cm[t * MROW + a] * us[a * C::CW + lane];
+        for (int a = par[t]; a < K && a >= from; a = par[a]) x -= cm[t * MROW + a] * us[a * C::CW + lane];
         us[t * C::CW + lane] = x;
       }
       wave_lds_order();
     }
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
+      const int from = m == done ? t0 : 0;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int t = 16 * m + 4 * lg + r;
-        if (t >= n) continue;
-        for (int a = t; a < K; a = par[a]) {
+        if (m < done || t >= n) continue;
+        for (int a = t; a < K && a >= from; a = par[a]) {
           const float w = dm[t * MROW + a];
 #pragma unroll
           for (int j = 0; j < C::NTL; ++j) ya[m][j][r] += w * us[a * C::CW + C::NTL * ln + j];
