@@ -560,12 +560,20 @@ def _need_in_words(t, name, dtype, index, shape):
     return t.data_ptr()
 
 
-try:  # the same in one compiled call; without it (or with an older build of it) only the time of a call grows
-    from . import _kda_args
-    _need, _rows = _kda_args.need, _kda_args.rows
-    _kda_args.set_refuse(_need_in_words)
-except (ImportError, AttributeError):
-    _need, _rows = _need_in_words, lambda t, dtype, index: None
+def _argument_forms():
+    """(_need, _rows): one compiled call each, or Python forms of the same where the helper is missing, or was built
+    against another PyTorch than this one (it reads the layout of its objects): only the time of a call grows."""
+    try:
+        from . import _kda_args
+        if _kda_args.torch_version == torch.__version__:
+            _kda_args.set_refuse(_need_in_words)
+            return _kda_args.need, _kda_args.rows
+    except (ImportError, AttributeError):
+        pass
+    return _need_in_words, lambda t, dtype, index: None
+
+
+_need, _rows = _argument_forms()
 
 
 def _may(t, name, dtype, index, shape):

@@ -9,8 +9,13 @@
 //   rows(tensor, dtype, device_index) -> (address, tokens, heads, d, row stride) or None
 // of a HIP tensor [n,H,d] or [B,T,H,d] of this dtype and device whose heads are dense and
 // whose token rows are evenly spaced; None for any other.
+//
+//   torch_version: the PyTorch whose headers this was compiled against.  Its objects' layouts
+// are read here, so the binding uses this module with that version only; a Python of
+// another minor version is refused at import.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <stdio.h>
 
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -85,4 +90,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_args", nullptr, -1, methods, 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__kda_args() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__kda_args() {
+  int major = 0, minor = 0;
+  if (sscanf(Py_GetVersion(), "%d.%d", &major, &minor) != 2 || major != PY_MAJOR_VERSION || minor != PY_MINOR_VERSION) {
+    PyErr_SetString(PyExc_ImportError, "_kda_args was built for another Python");
+    return nullptr;
+  }
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", KDA_TORCH_VERSION) != 0) Py_CLEAR(m);
+  return m;
+}
