@@ -580,6 +580,15 @@ def _may(t, name, dtype, index, shape):
     return None if t is None else _need(t, name, dtype, index, shape)
 
 
+def _filled(shape, dtype, device, value, stream):
+    """A new tensor for a call that may pass over some of its rows: `value` throughout, filled on the call's stream."""
+    if stream is None:
+        return torch.full(shape, value, dtype=dtype, device=device)
+    t = torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return t.fill_(value)
+
+
 def _io_code(t, name):
     """kda_dtype of a bf16 or fp32 tensor."""
     code = _CODES.get(t.dtype)
@@ -684,11 +693,11 @@ def _table(table, ref):
     return dev, R, W, P, _need(table, "table", _I32, dev, (R, W)), _need(ref, "ref", _I32, dev, (P,))
 
 
-def _move_list(moves, n_moves, room, t):
-    """moves and n_moves, made on t's device where they are not given, and their addresses."""
+def _move_list(moves, n_moves, room, t, stream):
+    """moves (pairs of -1) and n_moves, made on t's device where they are not given, and their addresses."""
     dev = t.get_device()
     if moves is None:
-        moves = torch.empty(max(room, 1), 2, dtype=_I32, device=t.device)
+        moves = _filled((max(room, 1), 2), _I32, t.device, -1, stream)
     if n_moves is None:
         n_moves = torch.empty(1, dtype=_I32, device=t.device)
     mp, np_ = _need(moves, "moves", _I32, dev, (max(moves.shape[0], room), 2)), _need(n_moves, "n_moves", _I32, dev, (1,))
@@ -698,13 +707,14 @@ def _move_list(moves, n_moves, room, t):
 def kda_cache_fork(table, ref, parents, children, n_private: int = 1, *, moves=None, n_moves=None, stream=None):
     """Rows ``children`` of the page table become copies of rows ``parents`` (-1: empty rows), in place: the
     first ``n_private`` entries on free pages of their own, the others shared.  Returns ``(moves, n_moves)``, the
-    page copies that ``kda_cache_copy`` has to carry out on each pool.  table: [n_rows,width] int32; ref:
+    page copies that ``kda_cache_copy`` has to carry out on each pool (a list that the call makes itself holds pairs of -1,
+    which are passed over, behind them).  table: [n_rows,width] int32; ref:
     [n_pages] int32; parents, children: [n] int32 on the device.  A fork that cannot be served (no free pages
     left, the child's row in use) leaves the child's row as it was."""
     dev, R, W, P, tp, rp = _table(table, ref)
     n = children.numel() if isinstance(children, torch.Tensor) else -1
     cp, pp = _need(children, "children", _I32, dev, (n,)), _need(parents, "parents", _I32, dev, (n,))
-    moves, n_moves, mp, np_ = _move_list(moves, n_moves, n * max(n_private, 0), table)
+    moves, n_moves, mp, np_ = _move_list(moves, n_moves, n * max(n_private, 0), table, stream)
     _run("kda_cache_fork", dev, stream, tp, rp, pp, cp, mp, np_, n, n_private, R, W, P)
     return moves, n_moves
 
@@ -725,7 +735,7 @@ def kda_cache_compact(table, ref, *, table_out=None, ref_out=None, moves=None, n
     ref_out = torch.empty_like(ref) if ref_out is None else ref_out
     n_live = torch.empty(1, dtype=_I32, device=table.device) if n_live is None else n_live
     to, ro = _need(table_out, "table_out", _I32, dev, (R, W)), _need(ref_out, "ref_out", _I32, dev, (P,))
-    moves, n_moves, mp, np_ = _move_list(moves, n_moves, max(P // 2, 1), table)
+    moves, n_moves, mp, np_ = _move_list(moves, n_moves, max(P // 2, 1), table, stream)
     _run("kda_cache_compact", dev, stream, tp, rp, to, ro, mp, np_, _need(n_live, "n_live", _I32, dev, (1,)), R, W, P)
     return table_out, ref_out, moves, n_moves, n_live
 
@@ -762,7 +772,8 @@ def kda_decode_step_paged(q, k, v, alpha, beta, pool, pages_in, pages_out=None, 
     ``pool`` ([n_pages,H,d_k,d_v] fp32) goes to page ``pages_out[b]`` (default: the same page).  ``alpha`` None: the
     gate inputs z and A of ``kda_decode_step_gated``.  A sequence whose page is out of range (padding: -1), or is
     written by another sequence of the call, is passed over: its row of ``o`` and the pool are left as they were.
-    Returns ``o``."""
+    Returns ``o``; where it is not given it is made here, with zeros in the rows passed over (a fill that a step with
+    its own ``o`` does without)."""
     dev = _device_of(q, "q")
     if q.dim() != 3 or not isinstance(v, torch.Tensor) or v.dim() != 3:
         raise ValueError("libkda: decode q/k/v must be [B,H,d]")
@@ -781,7 +792,7 @@ def kda_decode_step_paged(q, k, v, alpha, beta, pool, pages_in, pages_out=None, 
     P, poolp = _state_pool(pool, H, dk, dv, dev)
     ip, op = _need(pages_in, "pages_in", _I32, dev, (B,)), _may(pages_out, "pages_out", _I32, dev, (B,))
     if o is None:
-        o = torch.empty(B, H, dv, device=q.device, dtype=o_dtype)
+        o = _filled((B, H, dv), o_dtype, q.device, 0.0, stream)
     _run("kda_decode_step_paged", dev, stream, qp, kp, vp, code, ap, zp, Ap, bp, poolp, P, ip, op,
          _need(o, "o", o.dtype, dev, (B, H, dv)), _io_code(o, "o"), B, H, dk, dv)
     return o
@@ -795,7 +806,8 @@ def kda_tree_verify(q, k, v, alpha, beta, pool, pages, parents, n_nodes=None, *,
     [B] int32 the page of each sequence (None: page b).  ``parents`` [B,K] int32: the node that node t follows (its
     index is smaller), -1 for the state itself; ``n_nodes`` [B] int32: how many nodes each tree has (None: K).  o:
     [B,K,H,d_v], the output after the path to each node; u: [B,H,K,d_v] fp32, what ``kda_tree_commit`` needs.  Rows
-    behind a tree's last node, and those of a sequence whose page is out of range, are left as they were."""
+    behind a tree's last node, and those of a sequence whose page is out of range, are left as they were; in an ``o`` or
+    ``u`` that is not given, and made here, they are zeros."""
     dev = _device_of(q, "q")
     if q.dim() != 4 or not isinstance(v, torch.Tensor) or v.dim() != 4:
         raise ValueError("libkda: draft q/k/v must be [B,K,H,d]")
@@ -807,10 +819,13 @@ def kda_tree_verify(q, k, v, alpha, beta, pool, pages, parents, n_nodes=None, *,
     ap, bp = _need(alpha, "alpha", _F32, dev, shape), _need(beta, "beta", _F32, dev, (B, K, H))
     P, poolp = _state_pool(pool, H, dk, dv, dev)
     pg, pa, nn = _may(pages, "pages", _I32, dev, (B,)), _need(parents, "parents", _I32, dev, (B, K)), _may(n_nodes, "n_nodes", _I32, dev, (B,))
+    whole = pages is None and n_nodes is None  # (every row is written)
     if o is None:
-        o = torch.empty(B, K, H, dv, device=q.device, dtype=o_dtype)
+        shape = (B, K, H, dv)
+        o = torch.empty(shape, device=q.device, dtype=o_dtype) if whole else _filled(shape, o_dtype, q.device, 0.0, stream)
     if u is None:
-        u = torch.empty(B, H, K, dv, device=q.device, dtype=_F32)
+        shape = (B, H, K, dv)
+        u = torch.empty(shape, device=q.device, dtype=_F32) if whole else _filled(shape, _F32, q.device, 0.0, stream)
     _run("kda_tree_verify", dev, stream, qp, kp, vp, code, ap, bp, poolp, P, pg, pa, nn, _need(o, "o", o.dtype, dev, (B, K, H, dv)),
          _io_code(o, "o"), _need(u, "u", _F32, dev, (B, H, K, dv)), B, K, H, dk, dv)
     return o, u
