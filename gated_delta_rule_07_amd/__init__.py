@@ -543,10 +543,16 @@ def _run(name, index, stream, *args):
         raise KdaError(st, name)
 
 
-def _device_of(t, name):
-    """The index of t's device; t has to be a tensor on a HIP device."""
+def _tensor(t, name):
+    """t, which has to be a tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"libkda: {name} must be a torch.Tensor")
+    return t
+
+
+def _device_of(t, name):
+    """The index of t's device; t has to be a tensor on a HIP device."""
+    _tensor(t, name)
     if not t.is_cuda:
         raise ValueError(f"libkda: {name} must be on a HIP device, got {t.device}")
     return t.get_device()
@@ -642,21 +648,21 @@ def kda_qk_norm(q, k=None, *, norm: str = "l2", q_weight=None, k_weight=None, ep
     kp, Hk, ks = None, 0, 0
     if k is not None:
         kp, nk, Hk, dk, ks = _head_rows(k, "k", dt, dev)
-        if nk != n or dk != d or k.dim() != q.dim():
+        if nk != n or dk != d or k.dim() != q.dim() or (q.dim() == 4 and k.shape[:2] != q.shape[:2]):
             raise ValueError("libkda: q and k must agree in tokens and head size")
     qw = None if q_weight is None else _need(q_weight, "q_weight", _F32, dev, (d,))
     kw = None if k_weight is None else _need(k_weight, "k_weight", _F32, dev, (d,))
     rot, pos, freq = 0, None, None
-    if inv_freq is not None and inv_freq.numel():
+    if inv_freq is not None and _tensor(inv_freq, "inv_freq").numel():
         rot = 2 * inv_freq.numel()
         freq = _need(inv_freq, "inv_freq", _F32, dev, (rot // 2,))
         if positions is None:
             raise ValueError("libkda: a rotation needs positions")
-        pos = _need(positions, "positions", _I32, dev, positions.shape)
-        if positions.numel() != n:
+        pos = _need(positions, "positions", _I32, dev, _tensor(positions, "positions").shape)
+        if positions.numel() != n or (q.dim() == 4 and positions.dim() > 1 and positions.shape != q.shape[:2]):
             raise ValueError("libkda: positions must have one entry per token")
     if out_dtype is None:
-        out_dtype = dt if q_out is None else q_out.dtype
+        out_dtype = dt if q_out is None else _tensor(q_out, "q_out").dtype
     out_code = _CODES.get(out_dtype)
     if out_code is None:
         raise TypeError(f"libkda: outputs must be bfloat16 or float32, got {out_dtype}")
@@ -700,7 +706,8 @@ def _move_list(moves, n_moves, room, t, stream):
         moves = _filled((max(room, 1), 2), _I32, t.device, -1, stream)
     if n_moves is None:
         n_moves = torch.empty(1, dtype=_I32, device=t.device)
-    mp, np_ = _need(moves, "moves", _I32, dev, (max(moves.shape[0], room), 2)), _need(n_moves, "n_moves", _I32, dev, (1,))
+    rows = moves.shape[0] if _tensor(moves, "moves").dim() == 2 else 0
+    mp, np_ = _need(moves, "moves", _I32, dev, (max(rows, room), 2)), _need(n_moves, "n_moves", _I32, dev, (1,))
     return moves, n_moves, mp, np_
 
 
@@ -793,8 +800,9 @@ def kda_decode_step_paged(q, k, v, alpha, beta, pool, pages_in, pages_out=None, 
     ip, op = _need(pages_in, "pages_in", _I32, dev, (B,)), _may(pages_out, "pages_out", _I32, dev, (B,))
     if o is None:
         o = _filled((B, H, dv), o_dtype, q.device, 0.0, stream)
+    odt = _tensor(o, "o").dtype
     _run("kda_decode_step_paged", dev, stream, qp, kp, vp, code, ap, zp, Ap, bp, poolp, P, ip, op,
-         _need(o, "o", o.dtype, dev, (B, H, dv)), _io_code(o, "o"), B, H, dk, dv)
+         _need(o, "o", odt, dev, (B, H, dv)), _io_code(o, "o"), B, H, dk, dv)
     return o
 
 
@@ -826,7 +834,8 @@ def kda_tree_verify(q, k, v, alpha, beta, pool, pages, parents, n_nodes=None, *,
     if u is None:
         shape = (B, H, K, dv)
         u = torch.empty(shape, device=q.device, dtype=_F32) if whole else _filled(shape, _F32, q.device, 0.0, stream)
-    _run("kda_tree_verify", dev, stream, qp, kp, vp, code, ap, bp, poolp, P, pg, pa, nn, _need(o, "o", o.dtype, dev, (B, K, H, dv)),
+    odt = _tensor(o, "o").dtype
+    _run("kda_tree_verify", dev, stream, qp, kp, vp, code, ap, bp, poolp, P, pg, pa, nn, _need(o, "o", odt, dev, (B, K, H, dv)),
          _io_code(o, "o"), _need(u, "u", _F32, dev, (B, H, K, dv)), B, K, H, dk, dv)
     return o, u
 
