@@ -126,6 +126,8 @@ kda_status kda_cache_fork(int* table, int* ref, const int* parents, const int* c
                           int n, int n_private, int n_rows, int width, int n_pages, hipStream_t stream) {
   if (!table_ok(n_rows, width, n_pages) || n < 0 || n > KDA_MAX_FORKS || n_private < 0 || n_private > width)
     return KDA_ERR_SHAPE;
+  // one workgroup looks through n rows, and one thread through a row's private entries
+  if ((long long)n * width > (1LL << 26) || n_private > KDA_MAX_PAGES) return KDA_ERR_SHAPE;
   if (!table || !ref || !n_moves || (n > 0 && (!parents || !children || (n_private > 0 && !moves)))) return KDA_ERR_NULL;
   const void* ptrs[] = {table, ref, parents, children, moves, n_moves};
   for (const void* ptr : ptrs)

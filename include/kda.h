@@ -440,7 +440,8 @@ kda_status kda_qk_norm(const void* q, long long q_stride, const void* k, long lo
  *
  *   table, ref       : as above                                   (updated in place)
  *   parents, children: [n] int32, 0 <= n <= KDA_MAX_FORKS         (read)
- *   n_private        : 0 .. width
+ *                      and n * width <= 2^26 (any n up to n_rows is)
+ *   n_private        : 0 .. width, at most KDA_MAX_PAGES
  *   moves            : room for n * n_private pairs, n_moves: [1]  (written; what
  *                      moves holds past *n_moves is unspecified)
  *
