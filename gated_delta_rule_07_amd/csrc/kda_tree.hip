@@ -58,8 +58,7 @@ constexpr int kInvRow = 20, kInvBytes = 16 * kInvRow * 4;  // a 16 x 16 inverse,
 
 template <typename IO, int DK, int DV>
 struct TCfg {
-  static constexpr int NTL = 1;                        // 16-column tiles of a state wave
-  static constexpr int CW = 16 * NTL;                  // its columns
+  static constexpr int CW = 16;                        // columns of a state wave
   static constexpr int NW = DV / CW;                   // state waves (of 8)
   // a node's row in LDS: key, query, decays, and 16 bytes by which 16 rows cover all banks
   static constexpr int QAT = DK * (int)sizeof(IO), AAT = 2 * QAT, ROW = AAT + DK * 4 + 16;
@@ -166,18 +165,16 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 4 : 2) void kda_tree_ver
   __builtin_amdgcn_sched_barrier(0);  // (loads are counted in order: the small ones come first)
 
   // the state, as the matrix cores' B operand: slot (lg, e) of step kk is row 16 kk + 4 lg + e
-  typedef float colf __attribute__((ext_vector_type(C::NTL)));
-  typedef IO colio __attribute__((ext_vector_type(C::NTL)));
   const int ln = lane % 16, lg = lane / 16;
   const bool stw = C::NW == kTreeThreads / 64 || wave < C::NW;  // a state wave (the others load what the last one does)
-  const int col = C::CW * min(wave, C::NW - 1) + C::NTL * ln;  // its lane's first column
-  colf s[DK / 16][4];
-  colio rv[NT][4];
+  const int col = C::CW * min(wave, C::NW - 1) + ln;  // its lane's column
+  float s[DK / 16][4];
+  IO rv[NT][4];
   const float* S = p.pool + ((size_t)page * p.H + h) * DK * DV + col;
 #pragma unroll
   for (int kk = 0; kk < DK / 16; ++kk)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[kk][e] = *reinterpret_cast<const colf*>(S + (size_t)(16 * kk + 4 * lg + e) * DV);
+    for (int e = 0; e < 4; ++e) s[kk][e] = S[(size_t)(16 * kk + 4 * lg + e) * DV];
   __builtin_amdgcn_sched_barrier(0);
 
   int* par = reinterpret_cast<int*>(sm + L.par);
@@ -287,7 +284,7 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 4 : 2) void kda_tree_ver
   for (int m = 0; m < NT; ++m) {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      rv[m][r] = *reinterpret_cast<const colio*>(
+      rv[m][r] = *reinterpret_cast<const IO*>(
           vb + ((unsigned)min(16 * m + 4 * lg + r, n - 1) * H * (unsigned)(DV * sizeof(IO)) + (unsigned)(col * sizeof(IO))));
   }
   // wave m inverts I + C of block m: column ln of the inverse, row after row
@@ -314,11 +311,9 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 4 : 2) void kda_tree_ver
   }
 
   // products with the state: x (of the keys) and y (of the queries), of node 16 m + 4 lg + r
-  f32x4 xa[NT][C::NTL], ya[NT][C::NTL];
+  f32x4 xa[NT], ya[NT];
 #pragma unroll
-  for (int m = 0; m < NT; ++m)
-#pragma unroll
-    for (int j = 0; j < C::NTL; ++j) xa[m][j] = ya[m][j] = (f32x4)0.0f;
+  for (int m = 0; m < NT; ++m) xa[m] = ya[m] = (f32x4)0.0f;
   if (stw) {
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
@@ -329,12 +324,10 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 4 : 2) void kda_tree_ver
         const int i = 16 * kk + 4 * lg;
         const f32x4 ak = lds4(prow(t) + i), aq = lds4(prow(t) + DK + i);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int j = 0; j < C::NTL; ++j) {
-            xa[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(ak[e], s[kk][e][j], xa[m][j], 0, 0, 0);
-            ya[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(aq[e], s[kk][e][j], ya[m][j], 0, 0, 0);
-          }
+        for (int e = 0; e < 4; ++e) {
+          xa[m] = __builtin_amdgcn_mfma_f32_16x16x4f32(ak[e], s[kk][e], xa[m], 0, 0, 0);
+          ya[m] = __builtin_amdgcn_mfma_f32_16x16x4f32(aq[e], s[kk][e], ya[m], 0, 0, 0);
+        }
       }
     }
   }
@@ -348,12 +341,9 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 4 : 2) void kda_tree_ver
     for (int r = 0; r < 4; ++r) {
       const int t = 16 * m + 4 * lg + r;
       const float be = beta[min(t, n - 1)];
-#pragma unroll
-      for (int j = 0; j < C::NTL; ++j) {
-        const float x = be * (to_f32(rv[m][r][j]) - xa[m][j][r]);
-        xa[m][j][r] = t < n ? x : 0.0f;
-        fine &= fabsf(xa[m][j][r]) <= kPlain;
-      }
+      const float x = be * (to_f32(rv[m][r]) - xa[m][r]);
+      xa[m][r] = t < n ? x : 0.0f;
+      fine &= fabsf(xa[m][r]) <= kPlain;
     }
   }
   // block after block of nodes: xa turns into u, ya into o, as long as u stays below kPlain too (it grows by up to
@@ -369,35 +359,24 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 4 : 2) void kda_tree_ver
     for (int mm = 0; mm < m; ++mm) {
       const f32x4 c4 = *reinterpret_cast<const f32x4*>(crow + 16 * mm), d4 = *reinterpret_cast<const f32x4*>(drow + 16 * mm);
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int j = 0; j < C::NTL; ++j) {
-          xa[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(-c4[r], xa[mm][j][r], xa[m][j], 0, 0, 0);
-          ya[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(d4[r], xa[mm][j][r], ya[m][j], 0, 0, 0);
-        }
+      for (int r = 0; r < 4; ++r) {
+        xa[m] = __builtin_amdgcn_mfma_f32_16x16x4f32(-c4[r], xa[mm][r], xa[m], 0, 0, 0);
+        ya[m] = __builtin_amdgcn_mfma_f32_16x16x4f32(d4[r], xa[mm][r], ya[m], 0, 0, 0);
+      }
     }
     const f32x4 i4 = *reinterpret_cast<const f32x4*>(sm + L.inv + m * kInvBytes + 4 * (ln * kInvRow + 4 * lg));
     const f32x4 d4 = *reinterpret_cast<const f32x4*>(drow + 16 * m);
-    f32x4 um[C::NTL];
+    f32x4 um = (f32x4)0.0f;
 #pragma unroll
-    for (int j = 0; j < C::NTL; ++j) um[j] = (f32x4)0.0f;
+    for (int r = 0; r < 4; ++r) um = __builtin_amdgcn_mfma_f32_16x16x4f32(i4[r], xa[m][r], um, 0, 0, 0);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int j = 0; j < C::NTL; ++j) um[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(i4[r], xa[m][j][r], um[j], 0, 0, 0);
-#pragma unroll
-    for (int j = 0; j < C::NTL; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) fine &= fabsf(um[j][r]) <= kPlain;
+    for (int r = 0; r < 4; ++r) fine &= fabsf(um[r]) <= kPlain;
     plain = __all(fine);
     if (!plain) continue;
     done = m + 1;
+    xa[m] = um;
 #pragma unroll
-    for (int j = 0; j < C::NTL; ++j) {
-      xa[m][j] = um[j];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) ya[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(d4[r], um[j][r], ya[m][j], 0, 0, 0);
-    }
+    for (int r = 0; r < 4; ++r) ya[m] = __builtin_amdgcn_mfma_f32_16x16x4f32(d4[r], um[r], ya[m], 0, 0, 0);
   }
   if (!plain) {
     // from the block that was not plain on node after node, along its path: [K][CW] of this wave in LDS.  That block's xa
@@ -408,9 +387,7 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 4 : 2) void kda_tree_ver
     for (int m = 0; m < NT; ++m)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int j = 0; j < C::NTL; ++j)
-          if (16 * m + 4 * lg + r < n) us[(16 * m + 4 * lg + r) * C::CW + C::NTL * ln + j] = xa[m][j][r];
+        if (16 * m + 4 * lg + r < n) us[(16 * m + 4 * lg + r) * C::CW + ln] = xa[m][r];
     wave_lds_order();
     for (int t = t0; t < n; ++t) {
       const int from = t < t0 + 16 ? t0 : 0;
@@ -428,13 +405,8 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 4 : 2) void kda_tree_ver
       for (int r = 0; r < 4; ++r) {
         const int t = 16 * m + 4 * lg + r;
         if (m < done || t >= n) continue;
-        for (int a = t; a < K && a >= from; a = par[a]) {
-          const float w = dm[t * MROW + a];
-#pragma unroll
-          for (int j = 0; j < C::NTL; ++j) ya[m][j][r] += w * us[a * C::CW + C::NTL * ln + j];
-        }
-#pragma unroll
-        for (int j = 0; j < C::NTL; ++j) xa[m][j][r] = us[t * C::CW + C::NTL * ln + j];
+        for (int a = t; a < K && a >= from; a = par[a]) ya[m][r] += dm[t * MROW + a] * us[a * C::CW + ln];
+        xa[m][r] = us[t * C::CW + ln];
       }
     }
   }
@@ -445,23 +417,10 @@ __global__ __launch_bounds__(kTreeThreads, MAXK <= 32 ? 4 : 2) void kda_tree_ver
     for (int r = 0; r < 4; ++r) {
       const int t = 16 * m + 4 * lg + r;
       if (t >= n) continue;
-      colf ut, ot;
-#pragma unroll
-      for (int j = 0; j < C::NTL; ++j) {
-        ut[j] = xa[m][j][r];
-        ot[j] = ya[m][j][r];
-      }
       const unsigned at = (unsigned)t * H * DV + col;
-      *reinterpret_cast<colf*>(ub + (t * DV + col)) = ut;
-      if (p.o_f32) {
-        *reinterpret_cast<colf*>(static_cast<float*>(p.o) + row0 * DV + at) = ot;
-      } else {
-        typedef __bf16 colb __attribute__((ext_vector_type(C::NTL)));
-        colb ob;
-#pragma unroll
-        for (int j = 0; j < C::NTL; ++j) ob[j] = (__bf16)ot[j];
-        *reinterpret_cast<colb*>(static_cast<__bf16*>(p.o) + row0 * DV + at) = ob;
-      }
+      ub[t * DV + col] = xa[m][r];
+      if (p.o_f32) (static_cast<float*>(p.o) + row0 * DV)[at] = ya[m][r];
+      else (static_cast<__bf16*>(p.o) + row0 * DV)[at] = (__bf16)ya[m][r];
     }
   }
 }
