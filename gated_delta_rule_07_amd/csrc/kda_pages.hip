@@ -184,9 +184,11 @@ __device__ __forceinline__ void rename_entries(const CompactParams& p, int n, in
   }
 }
 
-// Tables of up to so many entries are renamed by the one workgroup that packs the pages
-// (a launch less: 3 us of 12 on a table of 96 entries); larger ones by a launch of their own.
-constexpr long long kSmallTable = 8192;
+// Tables of at most two entries a thread are renamed by the one workgroup that packs the pages, larger ones by a launch of
+// their own.  Measured in a graph, one launch against two: with 97 pages 5.5 against 6.1 us for 96 entries, 6.9 against 7.4
+// for 1,026, 7.3 against 7.3 for 2,048, 18.7 against 7.4 for 8,192; with 1,024 pages 6.4 against 7.3, 8.0 against 8.6, 9.8
+// against 8.8 and 26.6 against 9.1.
+constexpr long long kSmallTable = 2 * kMetaThreads;
 
 __global__ __launch_bounds__(kMetaThreads) void kda_cache_compact_kernel(CompactParams p) {
   __shared__ int sums[kMetaWaves];
