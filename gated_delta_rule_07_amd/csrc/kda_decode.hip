@@ -19,10 +19,13 @@
 // Paged: the same step with each sequence's state read from one page of a pool
 // and written to another (or the same).  A sequence without a valid page, or
 // whose pages another sequence writes, leaves the pool and its row of o alone.
-// The look over the other sequences' pages is a read of 2 B ints for a workgroup, done
-// while its state is in flight.  Measured over three pools in turn (nothing left in the
-// caches): 250 sequences of 32 heads 207 us, 5.1 TB/s, where a copy of 4 GiB reaches 5.0 to
-// 5.4; the dense step on three states in turn takes 220 us for 256 (160 us on one state).
+// The look over the other sequences' pages is a read of 2 B ints for each workgroup, begun
+// while its state is in flight; it is hidden where a state is large and the sequences few.
+// Measured over three pools in turn (nothing left in the caches): 250 sequences of 32 heads of
+// 128 206 us, 5.1 TB/s, where a copy of 4 GiB reaches 5.0 to 5.4; the dense step on three states
+// in turn takes 220 us for 256.  On one pool, again and again, paged against dense: 256 x 32 heads
+// of 128 179 against 159 us, 4,096 x 8 heads of 32 116 against 54, 4,096 x 8 heads of 16 (1 KB a
+// state, 16 KB of pages looked over by 64 threads) 90 against 20.
 #include "kda_device.h"
 #include "kda_launch.h"
 

@@ -10,11 +10,14 @@
 // the other half of the rotated part sits in a lane a fixed distance away, one
 // shuffle per value.  A workgroup takes all heads of a few tokens, so that the
 // cosines and sines, which the heads of a token share, are formed once: in LDS,
-// from an angle reduced in fp64 to a fraction of a turn.
+// from an angle reduced in fp64 to a fraction of a turn.  That fraction is rounded to fp32
+// before its sine, and the norm's reciprocal before it multiplies the head: at most 2 pi 2^-25
+// of |a| + |b| and half a step of fp32, below the rounding of any bf16 output; fp32 outputs end
+// 7.0e-8 from the formula where dividing and 64-bit sines end 5.9e-8 from it.
 //
 // Measured: 65,536 tokens of 32 + 32 heads of 128 in bf16 (2.15 GB) 370 us, 5.8 TB/s;
 // 4,099 tokens of 32 + 4 heads of 64 in fp32 with half of each head rotated (76 MB)
-// 16.8 us, 4.5 TB/s; one token of 8 + 8 heads 2.0 us.  Twice as many heads for each group
+// 17.0 us, 4.5 TB/s; one token of 8 + 8 heads 2.0 us.  Twice as many heads for each group
 // took 385 us on the first, four heads loaded ahead of their sums 403 us (80 registers,
 // half the waves), non-temporal loads and stores 353 us: not used, since what reads the
 // outputs next finds those of all but the longest calls in the caches.

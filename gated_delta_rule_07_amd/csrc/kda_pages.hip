@@ -8,8 +8,8 @@
 // forks, never from the order of atomics, so the same inputs give the same pages.
 // Copying the pages is bound by HBM: each page is read once and written once.
 //
-// Measured: 1 and 64 forks over 64 and 160 pages 5 and 8 us, packing 97 pages under a
-// table of 96 entries 6 us, freeing 64 rows 3 us.
+// Measured: 1 and 64 forks over 64 and 160 pages 5.2 and 8 to 9.5 us, packing 97 pages under a
+// table of 96 entries 5.2 us, freeing 64 rows 3.4 to 5.2 us.
 #include <algorithm>
 
 #include "kda_device.h"
@@ -236,7 +236,11 @@ __global__ __launch_bounds__(256) void kda_cache_rename_kernel(CompactParams p) 
 // together (40 pages of 2 MiB on 8 layers: 247 us, 5.4 TB/s, against 267 us with a run
 // of tiles for each workgroup).  Which moves race is settled by every workgroup
 // for itself, with one pass over the list: a bit for each page that is a
-// destination, and one for each that is so more than once.
+// destination, and one for each that is so more than once.  Long lists of small pages pay
+// for that pass: 4,096 moves of 64 KiB between two pools 91 us (5.9 TB/s), 16,384 of 16 KiB 110 us
+// (4.9), 65,536 of 4 KiB 201 us (2.7) and of 256 bytes 157 us.  A source that several moves name is
+// read for each of them, from the caches where they still hold it: 64 copies of 16 pages of 2 MiB
+// on 8 layers fetch 0.86 GB, 3.2 times the pages' 0.27, in 282 to 292 us.
 constexpr int kTile = 16384;
 constexpr int kCopyThreads = 256;
 constexpr int kPageWords = kMaxPages / 32;

@@ -34,19 +34,20 @@
 //      that do not follow it, so from a block on whose right-hand sides or u pass 1e18 (as any
 //      do where C, D, an inverse or an input has left fp32) a wave takes the sums along the paths.
 //
-// Measured, 64 sequences of 32 heads of 128, trees of 24 to 32 nodes 6 deep, bf16: 80 us,
+// Measured, 64 sequences of 32 heads of 128, trees of 24 to 32 nodes 6 deep, bf16: 84 us (78 at best),
 // for 252 MB (47 us at a copy's rate) and 256 + 48 fp32 matrix instructions a wave pair, 35 us
 // of the matrix cores at the 2.2 GHz that the launch runs at.  The loads alone take 40 us,
 // and the kernel without the first product 58 us: what is lost is overlap, two workgroups
 // of 47 KB of LDS and 64 KB of state in registers a compute unit.  Trees of 63 nodes, 12 deep, on
-// 120 fp32 states of 64 x 64: 13.5 us (33.7 us substituting node after node).  One tree of 8
-// nodes on 8 states: 7.4 us.  Tried and no faster on the first: four waves with two column tiles
-// each and three workgroups a compute unit (81 us, and 15.0 and 8.0 us on the others), a
+// 120 fp32 states of 64 x 64: 13.7 us (33.7 us substituting node after node).  One tree of 8
+// nodes on 8 states: 7.4 us.  Tried and no faster on the first, where this form took
+// 80 us then: four waves with two column tiles each and three workgroups a compute unit (81 us, and 15.0 and 8.0 us on the others), a
 // persistent grid that loads the next state during the substitution (96 us), registers
 // cut to 80 for three workgroups of eight waves (105 us, spills).
 //
 // kda_tree_commit_kernel reads and writes a state as the decode step does: 45 us for the 2,048
-// states above (275 MB, 6.1 TB/s with what the verify left in the caches).
+// states above (275 MB, 6.1 TB/s with what the verify left in the caches).  It looks over the other
+// sequences' pages as that step does: 4,096 x 8 states of 16 x 16 take 109 us.
 #include "kda_device.h"
 #include "kda_launch.h"
 
