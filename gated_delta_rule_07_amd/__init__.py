@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 from pathlib import Path
+from typing import NamedTuple
 
 import torch
 
@@ -21,12 +22,13 @@ __all__ = ["kda_chunk_fwd", "kda_chunk_fwd_snapshots", "kda_chunk_fwd_varlen", "
            "kda_decode_commit",
            "kda_qk_norm", "kda_cache_fork", "kda_cache_free", "kda_cache_compact", "kda_cache_copy",
            "kda_decode_step_paged", "kda_tree_verify", "kda_tree_commit",
+           "kda_attn_fwd", "kda_kv_append", "kda_kv_read", "kda_attn_decode", "kda_attn_decode_plan", "KVLayout",
            "kda_status_string", "kda_version",
            "kda_last_hip_error", "library_path", "load_library", "bind", "KdaError",
-           "KDA_F32", "KDA_BF16", "KDA_MAX_SNAPSHOTS", "KDA_MAX_DRAFT", "KDA_MAX_PAGES", "KDA_MAX_FORKS",
-           "KDA_MAX_PAGED_SEQS", "KDA_MAX_TREE"]
+           "KDA_F32", "KDA_BF16", "KDA_E4M3", "KDA_MAX_SNAPSHOTS", "KDA_MAX_DRAFT", "KDA_MAX_PAGES", "KDA_MAX_FORKS",
+           "KDA_MAX_PAGED_SEQS", "KDA_MAX_TREE", "KDA_MAX_HEADS", "KDA_MAX_CALL_TOKENS", "KDA_MAX_ATTN_TOKENS"]
 
-KDA_F32, KDA_BF16 = 0, 1
+KDA_F32, KDA_BF16, KDA_E4M3 = 0, 1, 2
 KDA_MAX_SNAPSHOTS = 128
 KDA_MAX_DRAFT = 16
 KDA_SPLIT_SCRATCH_BYTES = 64 << 20
@@ -34,6 +36,9 @@ KDA_MAX_PAGES = 65536
 KDA_MAX_FORKS = 1024
 KDA_MAX_PAGED_SEQS = 4096
 KDA_MAX_TREE = 64
+KDA_MAX_HEADS = 4096
+KDA_MAX_CALL_TOKENS = 1 << 22
+KDA_MAX_ATTN_TOKENS = 16
 _PKG = Path(__file__).resolve().parent
 _LIB_PATH = _PKG / "libkda.so"
 _lib = None
@@ -117,6 +122,21 @@ def bind(path) -> ctypes.CDLL:
                                     i32, i32, i32, i32, i32, vp]
     lib.kda_tree_commit.restype = i32
     lib.kda_tree_commit.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp]
+    lib.kda_attn_fwd.restype = i32
+    lib.kda_attn_fwd.argtypes = [vp, i64, vp, i64, vp, i64, i32, f32, vp, vp, i32, i32, i32, vp, i64, i32,
+                                 i32, i32, i32, i32, vp]
+    lib.kda_kv_page_bytes.restype = i32
+    lib.kda_kv_page_bytes.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
+    lib.kda_kv_append.restype = i32
+    lib.kda_kv_append.argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, vp, i32, i32, vp, i64, vp, i64, vp, i32, i32, i32,
+                                  vp, i32, i32, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp]
+    lib.kda_kv_read.restype = i32
+    lib.kda_kv_read.argtypes = [vp, i32, i32, i32, vp, i32, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp]
+    lib.kda_attn_decode_plan.restype = i32
+    lib.kda_attn_decode_plan.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
+    lib.kda_attn_decode.restype = i32
+    lib.kda_attn_decode.argtypes = [vp, i32, f32, vp, i32, i32, i32, vp, i32, i32, vp, vp, vp, i32, vp, sz,
+                                    i32, i32, i32, i32, i32, i32, vp]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_status_string.argtypes = [i32]
     lib.kda_last_hip_error.restype = i32
@@ -859,3 +879,206 @@ def kda_tree_commit(k, alpha, u, parents, last, pool, pages_in, pages_out=None, 
     nn, ip, op = (_may(t, name, _I32, dev, (B,)) for t, name in ((n_nodes, "n_nodes"), (pages_in, "pages_in"), (pages_out, "pages_out")))
     _run("kda_tree_commit", dev, stream, kp, code, ap, up, pa, nn, lp, poolp, P, ip, op, B, K, H, dk, dv)
     return pool
+
+
+_KV_CODES = {torch.bfloat16: KDA_BF16, torch.float8_e4m3fn: KDA_E4M3}
+
+
+class KVLayout(NamedTuple):
+    """What a page of keys and values holds: ``page_tokens`` tokens of ``H`` heads, keys of ``d_k`` and values of
+    ``d_v``, as ``dtype`` (torch.bfloat16, or torch.float8_e4m3fn with a scale for each head's keys and values on the
+    page).  A pool is a uint8 tensor [n_pages, page_bytes] (one layer; ``kda_cache_copy`` takes
+    [n_layers, n_pages, page_bytes])."""
+    dtype: torch.dtype
+    page_tokens: int
+    H: int
+    d_k: int
+    d_v: int
+
+    @property
+    def page_bytes(self) -> int:
+        n = ctypes.c_size_t(0)
+        st = (_lib or load_library()).kda_kv_page_bytes(_KV_CODES.get(self.dtype, -1), self.page_tokens, self.H, self.d_k, self.d_v,
+                                                        ctypes.byref(n))
+        if st != 0:
+            raise KdaError(st, "kda_kv_page_bytes")
+        return n.value
+
+    def pool(self, n_pages: int, device, n_layers: int | None = None) -> torch.Tensor:
+        """A pool of zeros."""
+        shape = (n_pages, self.page_bytes) if n_layers is None else (n_layers, n_pages, self.page_bytes)
+        return torch.zeros(shape, dtype=torch.uint8, device=device)
+
+    def views(self, pool):
+        """``(k, v, scales)`` of one layer's pool, without a copy: keys [n_pages,H,page_tokens,d_k], values
+        [n_pages,H,page_tokens,d_v], and scales [n_pages,2,H] fp32 (None for bf16 pages)."""
+        e = 1 if _KV_CODES[self.dtype] == KDA_E4M3 else 2
+        a = self.H * self.page_tokens * self.d_k * e
+        b = a + self.H * self.page_tokens * self.d_v * e
+        k = pool[:, :a].view(self.dtype).unflatten(1, (self.H, self.page_tokens, self.d_k))
+        v = pool[:, a:b].view(self.dtype).unflatten(1, (self.H, self.page_tokens, self.d_v))
+        return k, v, pool[:, b:b + 8 * self.H].view(torch.float32).unflatten(1, (2, self.H)) if e == 1 else None
+
+
+def _kv_cache(pool, layout, table, rows, n, dev):
+    """(pool, kv code, n_pages, page_tokens, table, n_rows, width, rows) of the calls on pages of keys and values."""
+    code = _KV_CODES.get(layout.dtype)
+    if code is None:
+        raise TypeError(f"libkda: pages hold bfloat16 or float8_e4m3fn, got {layout.dtype}")
+    P = _tensor(pool, "pool").shape[0] if _tensor(pool, "pool").dim() == 2 else -1
+    R, W = _tensor(table, "table").shape if table.dim() == 2 else (-1, -1)
+    return (_need(pool, "pool", torch.uint8, dev, (P, layout.page_bytes)), code, P, layout.page_tokens,
+            _need(table, "table", _I32, dev, (R, W)), R, W, _may(rows, "rows", _I32, dev, (n,)))
+
+
+def kda_attn_fwd(q, k, v, *, scale=None, cu_seqlens=None, cu_seqlens_k=None, o=None, o_dtype=None, stream=None):
+    """Causal attention over whole prompts: ``o``.
+
+    q: [n,H_q,d_k] or [B,T,H_q,d_k]; k: [m,H_kv,d_k] or [B,T_k,H_kv,d_k]; v: the same with d_v (bf16 or fp32; token rows
+    may be slices of wider rows; H_q a multiple of H_kv: grouped heads).  Packed sequences: ``cu_seqlens`` [N+1] int32 on
+    the device, with [n,...] tensors; ``cu_seqlens_k`` the same for keys and values where a sequence has more of them than
+    queries (a cached prefix: query i sees the keys j <= i + n_k - n_q).  Without: one sequence, or B of them.
+    ``scale``: d_k ** -0.5 by default.  ``o`` is made where it is not given (zeros in the rows that no sequence covers)."""
+    dev = _device_of(q, "q")
+    dt = q.dtype
+    code = _io_code(q, "q")
+    qp, n, Hq, dk, qs = _head_rows(q, "q", dt, dev)
+    kp, m, Hk, dk2, ks = _head_rows(_tensor(k, "k"), "k", dt, dev)
+    vp, m2, Hk2, dv, vs = _head_rows(_tensor(v, "v"), "v", dt, dev)
+    if dk2 != dk or m2 != m or Hk2 != Hk or k.dim() != q.dim() or v.shape[:-1] != k.shape[:-1]:
+        raise ValueError("libkda: k must have q's head size, and v as many tokens and heads as k")
+    N = 1
+    if q.dim() == 4:
+        N = q.shape[0]
+        if k.shape[0] != N:
+            raise ValueError("libkda: q and k must have as many sequences")
+    if cu_seqlens is not None:
+        if q.dim() != 3:
+            raise ValueError("libkda: packed sequences are [n,H,d]")
+        N = _tensor(cu_seqlens, "cu_seqlens").numel() - 1
+    cp, ckp = _may(cu_seqlens, "cu_seqlens", _I32, dev, (N + 1,)), _may(cu_seqlens_k, "cu_seqlens_k", _I32, dev, (N + 1,))
+    if o is None:
+        shape, odt = (*q.shape[:-1], dv), dt if o_dtype is None else o_dtype
+        o = torch.empty(shape, dtype=odt, device=q.device) if cp is None else _filled(shape, odt, q.device, 0.0, stream)
+    op, _, _, _, os = _head_rows(_tensor(o, "o"), "o", o.dtype, dev)
+    if o.shape != (*q.shape[:-1], dv):
+        raise ValueError("libkda: o must be shaped like q, with v's head size")
+    _run("kda_attn_fwd", dev, stream, qp, qs, kp, ks, vp, vs, code, dk ** -0.5 if scale is None else scale, cp, ckp, N, n, m,
+         op, os, _io_code(o, "o"), Hq, Hk, dk, dv)
+    return o
+
+
+def kda_kv_append(k, v, pool, layout, table, lens, *, rows=None, cu_seqlens=None, q=None, inv_freq=None, positions=None,
+                  pairing: str = "halves", q_out=None, k_out=None, stream=None):
+    """New tokens' keys and values onto the pages of their sequences, turned by position on the way: ``(q_out, k_out)``.
+
+    k: [n,H,d_k], v: [n,H,d_v] (bf16 or fp32; rows may be slices of wider rows); ``pool`` uint8 [n_pages,page_bytes] of
+    ``layout``; ``table`` [n_rows,width] int32, row ``rows[b]`` ([N] int32; None: b; -1: padding) lists sequence b's pages;
+    ``lens`` [N] int32: the tokens it has there.  ``cu_seqlens`` [N+1] int32: the sequences' tokens (None: one each).  With
+    ``inv_freq`` ([rot/2] fp32) the first rot values of each key, and of each query in ``q`` [n,H_q,d_k], turn by the
+    token's place in its sequence, or by ``positions`` [n] int32.  ``q_out`` (made where q is given) and ``k_out`` (only
+    where given; may be ``k``) receive the turned rows.  ``lens`` is not changed.  Tokens without a page, and tokens of
+    sequences that would write one page, are not stored."""
+    dev = _device_of(k, "k")
+    dt = k.dtype
+    code = _io_code(k, "k")
+    kp, n, H, dk, ks = _head_rows(k, "k", dt, dev)
+    vp, n2, H2, dv, vs = _head_rows(_tensor(v, "v"), "v", dt, dev)
+    if k.dim() != 3 or n2 != n or (H, dk, H2, dv) != (layout.H, layout.d_k, layout.H, layout.d_v):
+        raise ValueError("libkda: k and v must be [n,H,d] of the pages' heads and sizes")
+    N = n if cu_seqlens is None else _tensor(cu_seqlens, "cu_seqlens").numel() - 1
+    cache = _kv_cache(pool, layout, table, rows, N, dev)
+    pr = _PAIRINGS.get(pairing)
+    if pr is None:
+        raise ValueError('libkda: pairing is "halves" or "pairs"')
+    rot, fp, pp = 0, None, None
+    if inv_freq is not None and _tensor(inv_freq, "inv_freq").numel():
+        rot = 2 * inv_freq.numel()
+        fp, pp = _need(inv_freq, "inv_freq", _F32, dev, (rot // 2,)), _may(positions, "positions", _I32, dev, (n,))
+    qp, Hq, qs, qop, qos, kop, kos = None, H, 0, None, 0, None, 0
+    if q is not None:
+        qp, nq, Hq, dq, qs = _head_rows(_tensor(q, "q"), "q", dt, dev)
+        if nq != n or dq != dk or q.dim() != 3:
+            raise ValueError("libkda: q must be [n,H_q,d_k] of k's tokens")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dt, device=q.device) if cu_seqlens is None else _filled(q.shape, dt, q.device, 0.0, stream)
+        qop, qos = _head_out(_tensor(q_out, "q_out"), "q_out", q, dev, dt)
+    elif q_out is not None:
+        raise ValueError("libkda: q_out without q")
+    if k_out is not None:
+        kop, kos = _head_out(_tensor(k_out, "k_out"), "k_out", k, dev, dt)
+    _run("kda_kv_append", dev, stream, kp, ks, vp, vs, qp, qs, code, pp, fp, rot, pr, qop, qos, kop, kos, *cache,
+         _need(lens, "lens", _I32, dev, (N,)), _may(cu_seqlens, "cu_seqlens", _I32, dev, (N + 1,)), N, n, Hq, H, dk, dv)
+    return q_out, k_out
+
+
+def kda_kv_read(pool, layout, table, cu_seqlens, total: int, *, rows=None, starts=None, k_out=None, v_out=None,
+                out_dtype=torch.bfloat16, stream=None):
+    """Cached keys and values back as dense rows: ``(k_out, v_out)``, [total,H,d_k] and [total,H,d_v].  Rows
+    cu_seqlens[b] .. cu_seqlens[b+1] are sequence b's tokens from place ``starts[b]`` ([N] int32; None: 0) on; the other
+    arguments as ``kda_kv_append``.  Tokens without a page leave their rows as they were (zeros where the outputs are made
+    here)."""
+    dev = _device_of(pool, "pool")
+    N = _tensor(cu_seqlens, "cu_seqlens").numel() - 1
+    cache = _kv_cache(pool, layout, table, rows, N, dev)
+    cp, sp = _need(cu_seqlens, "cu_seqlens", _I32, dev, (N + 1,)), _may(starts, "starts", _I32, dev, (N,))
+    if out_dtype not in _CODES:
+        raise TypeError(f"libkda: outputs must be bfloat16 or float32, got {out_dtype}")
+    if k_out is None:
+        k_out = _filled((total, layout.H, layout.d_k), out_dtype if v_out is None else _tensor(v_out, "v_out").dtype, pool.device, 0.0, stream)
+    odt = _tensor(k_out, "k_out").dtype
+    if v_out is None:
+        v_out = _filled((total, layout.H, layout.d_v), odt, pool.device, 0.0, stream)
+    _run("kda_kv_read", dev, stream, *cache, sp, cp, _need(k_out, "k_out", odt, dev, (total, layout.H, layout.d_k)),
+         _need(v_out, "v_out", odt, dev, (total, layout.H, layout.d_v)), _io_code(k_out, "k_out"), N, total, layout.H, layout.d_k, layout.d_v)
+    return k_out, v_out
+
+
+def kda_attn_decode_plan(layout, B: int, K: int, H_q: int, width: int) -> int:
+    """Bytes of workspace that a ``kda_attn_decode`` call with these sizes needs (``width``: the page table's)."""
+    n = ctypes.c_size_t(0)
+    st = (_lib or load_library()).kda_attn_decode_plan(_KV_CODES.get(layout.dtype, -1), layout.page_tokens, width, B, K, H_q, layout.H,
+                                                       layout.d_k, layout.d_v, ctypes.byref(n))
+    if st != 0:
+        raise KdaError(st, "kda_attn_decode_plan")
+    return n.value
+
+
+def kda_attn_decode(q, pool, layout, table, lens, *, rows=None, scale=None, o=None, o_dtype=None, workspace=None, stream=None):
+    """Attention of each sequence's last tokens over its pages: ``o``.
+
+    q: [B,H_q,d_k] (one token), or [B,K,H_q,d_k] (a chain of K drafted tokens), bf16 or fp32, of tokens that are on the pages
+    already; ``lens`` [B] int32: the tokens on each sequence's pages, these included; token t of K sees the first
+    lens - K + 1 + t.  ``pool``, ``layout``, ``table``, ``rows``: as ``kda_kv_append``.  o: [B,H_q,d_v] or [B,K,H_q,d_v];
+    rows of padding are left as they were (zeros where ``o`` is made here).  ``workspace``: uint8 of
+    ``kda_attn_decode_plan`` bytes, made where it is not given; calls that may run at the same time need one each."""
+    dev = _device_of(q, "q")
+    if q.dim() not in (3, 4):
+        raise ValueError("libkda: q must be [B,H_q,d_k] or [B,K,H_q,d_k]")
+    shape, dt = q.shape, q.dtype
+    B, Hq, dk = shape[0], shape[-2], shape[-1]
+    K = 1 if len(shape) == 3 else shape[1]
+    if dk != layout.d_k:
+        raise ValueError("libkda: q must have the pages' key size")
+    cache = _kv_cache(pool, layout, table, rows, B, dev)
+    out = (*shape[:-1], layout.d_v)
+    if o is None:
+        odt = dt if o_dtype is None else o_dtype
+        o = torch.empty(out, dtype=odt, device=q.device) if rows is None else _filled(out, odt, q.device, 0.0, stream)
+    need = kda_attn_decode_plan(layout, B, K, Hq, cache[6])
+    wp, wn = None, 0
+    if workspace is not None:
+        wn = _tensor(workspace, "workspace").numel()
+        wp = _need(workspace, "workspace", torch.uint8, dev, (wn,))
+    elif need:
+        # (memory of the call's stream: a block that the allocator hands out on another one could still be in use there)
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        wp, wn = workspace.data_ptr(), need
+    _run("kda_attn_decode", dev, stream, _need(q, "q", dt, dev, shape), _io_code(q, "q"), dk ** -0.5 if scale is None else scale,
+         *cache, _need(lens, "lens", _I32, dev, (B,)), _need(o, "o", _tensor(o, "o").dtype, dev, out), _io_code(o, "o"), wp, wn,
+         B, K, Hq, layout.H, dk, layout.d_v)
+    return o

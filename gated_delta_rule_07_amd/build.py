@@ -24,7 +24,8 @@ ARGS_HELPER = PKG / "_kda_args.so"
 OBJDIR = PKG / "_build"
 
 SOURCES = ["kda_api.cpp", "kda_decode.hip", "kda_prefill.hip", "kda_prefill_pipe.hip", "kda_prep.hip",
-           "kda_spec.hip", "kda_split.hip", "kda_cache_api.cpp", "kda_heads.hip", "kda_pages.hip", "kda_tree.hip"]
+           "kda_spec.hip", "kda_split.hip", "kda_cache_api.cpp", "kda_heads.hip", "kda_pages.hip", "kda_tree.hip",
+           "kda_attn_api.cpp", "kda_attn.hip", "kda_attn_decode.hip", "kda_kv.hip"]
 
 ARCH = "gfx950"
 # Packed-fp32 VALU forms are disabled: plain fp32 code only.  Matrix-core

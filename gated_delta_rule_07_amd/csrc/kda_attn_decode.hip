@@ -1,0 +1,477 @@
+// Attention of one or a few tokens of each sequence over its cached keys and values, for gfx950.
+//
+//   o = sum_j p_j v_j,  p = softmax_j(scale q . k_j),  k_j, v_j = scale of their page x code
+//
+// Every cached byte is read once and multiplied with the K G queries (K tokens, G heads of a group)
+// that share it, so the call is bound by those bytes.  The work is cut into granules of 128 keys of
+// one (sequence, head, 16 query rows) and every workgroup takes an equal run of them, whatever the
+// sequences' lengths: a run that holds a unit whole writes its output, others leave (o, m, l) in the
+// workspace for a second kernel.  Within a workgroup each wave streams its own 32-key tiles from
+// memory into registers -- no LDS and no barrier until a unit ends:
+//   S^T = K Q^T with a lane holding 16 bytes of a key's row; P^T as it comes out is the operand of
+//   O^T = V^T P^T, whose other operand wants 8 keys' values of one channel in a lane: a lane loads
+//   8 channels of 8 keys and transposes them in registers (byte permutes, then the conversion to bf16).
+// Codes convert to bf16 exactly; the page's scales multiply scores and probabilities instead.
+// fp32 queries are split into three bf16 terms, and so are their probabilities: 24 bits on bf16 matrix cores.
+#include <algorithm>
+
+#include "kda_kv_device.h"
+
+namespace kda {
+namespace {
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kTile = 32, kGranule = kTile * kWaves;
+constexpr int kWorkers = 512;     // workgroups that share the granules
+constexpr int kLeastRun = 2;      // granules a workgroup takes at least
+constexpr int kWholeUnits = 2048; // up to this many tokens a sequence, a workgroup takes a unit whole
+constexpr float kLog2e = 1.4426950408889634f;
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+__host__ __device__ inline int columns(int K, int G) { return (K * G + kAttnColumns - 1) / kAttnColumns; }
+
+// The workspace: for each worker two partial results, then the units that have to be joined.
+struct Join {
+  int unit, last, slot, unused;  // unit = (b column tiles + column tile) H + head, or -1; the worker that ends it; which part it is here
+};
+__host__ __device__ inline size_t part_floats(int dv) { return (size_t)kAttnColumns * (dv + 2); }
+
+struct DecodePlan {
+  AttnDecodeParams p;
+  int G, CT, workers;
+  float* parts;  // [workers][2][16 dv + 16 m + 16 l]
+  Join* joins;   // [workers]
+};
+
+__device__ __forceinline__ uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel) { return __builtin_amdgcn_perm(hi, lo, sel); }
+__device__ __forceinline__ uint32_t bf16_of_e4m3(uint32_t w, bool hi) {
+  return __builtin_bit_cast(uint32_t, hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true)
+                                         : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+}
+
+// Tokens that rows of sequence b attend to, and its granules (0: no row of the table, nothing is written).
+__device__ __forceinline__ int tokens_of(const AttnDecodeParams& p, int b) {
+  return min(max(p.lens[b], 0), p.c.width * p.c.page_tokens);
+}
+__device__ __forceinline__ int granules_of(const AttnDecodeParams& p, int b) {
+  const int row = p.c.rows ? p.c.rows[b] : b;
+  if (row < 0 || row >= p.c.n_rows) return 0;
+  return max(1, (tokens_of(p, b) + kGranule - 1) / kGranule);
+}
+
+template <bool E4, int DK, int DV>
+struct Tile {
+  static constexpr int NK = DK * (E4 ? 1 : 2) / 64;  // 16-byte loads of a lane for 16 keys
+  static constexpr int NV = DV / 16;                 // channels of a lane
+  static constexpr int VW = NV * (E4 ? 1 : 2) / 4;   // dwords of a lane and key
+  u32x4 k[2][NK];
+  uint32_t v[8][VW];
+  float ks[2], vs[2];
+  int page[2];
+};
+
+template <int NT, bool E4, int DK, int DV>
+__global__ __launch_bounds__(kThreads) void kda_attn_decode_kernel(DecodePlan a) {
+  using T = Tile<E4, DK, DV>;
+  constexpr int NM = DV / 16, NS = DK / 32;
+  constexpr int ES = E4 ? 1 : 2;
+  __shared__ __attribute__((aligned(16))) float so[kWaves][kAttnColumns][DV + 4];
+  __shared__ float sm[kWaves][kAttnColumns], sl[kWaves][kAttnColumns];
+  __shared__ int swave[kWaves];
+  extern __shared__ int prefix[];  // [B + 1]: granules of the sequences before
+  const AttnDecodeParams& p = a.p;
+  const KvCache& cache = p.c;
+  const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), col = lane % 16, g = lane / 16;
+  const int H = cache.H, units = a.CT * H, pt = cache.page_tokens;
+
+  long long at, end, mine;  // this workgroup's granules; where its run begins
+  const bool whole = a.workers == 0;
+  int b = 0;
+  if (whole) {
+    b = blockIdx.x / units;
+    at = mine = 0;
+    end = granules_of(p, b);
+  } else {
+    const int each = (p.B + kThreads - 1) / kThreads, i0 = min(tid * each, p.B), i1 = min(i0 + each, p.B);
+    int sum = 0;
+    for (int i = i0; i < i1; ++i) sum += granules_of(p, i);
+    int run = sum;
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) {
+      const int up = __shfl_up(run, m);
+      if (lane >= m) run += up;
+    }
+    if (lane == 63) swave[wave] = run;
+    __syncthreads();
+    int before = run - sum;
+    for (int w = 0; w < wave; ++w) before += swave[w];
+    for (int i = i0; i < i1; ++i) {
+      prefix[i] = before;
+      before += granules_of(p, i);
+    }
+    if (tid == kThreads - 1) prefix[p.B] = before;
+    __syncthreads();
+    const long long total = (long long)prefix[p.B] * units;
+    const long long per = max((total + a.workers - 1) / a.workers, (long long)kLeastRun);
+    at = mine = min(per * blockIdx.x, total);
+    end = min(at + per, total);
+    if (tid == 0) a.joins[blockIdx.x] = Join{-1, 0, 0, 0};
+    if (at < end) b = last_at_most(p.B, at, [&](int i) { return (long long)prefix[i] * units; });
+  }
+
+  while (at < end) {
+    // the unit that granule `at` belongs to, and this workgroup's granules [g0, g1) of its n
+    int unit, n, g0, g1;
+    if (whole) {
+      unit = blockIdx.x % units;
+      g0 = 0;
+      g1 = n = (int)end;
+    } else {
+      while ((long long)prefix[b + 1] * units <= at) ++b;  // (sequences without a granule)
+      n = prefix[b + 1] - prefix[b];
+      const long long off = at - (long long)prefix[b] * units;
+      unit = (int)(off / n);
+      g0 = (int)(off % n);
+      g1 = (int)min((long long)n, g0 + (end - at));
+    }
+    const int ct = unit / H, h = unit % H;
+    const int row = cache.rows ? cache.rows[b] : b;
+    const int* pages = cache.table + (size_t)row * cache.width;
+    const int len = tokens_of(p, b);
+    const int cc = kAttnColumns * ct + col, tok = cc / a.G, head = h * a.G + cc % a.G;
+    const bool live = tok < p.K;
+    const int limit = live ? len - p.K + 1 + tok : len;
+    const int least = len - p.K + 1;  // what every row attends to
+
+    // queries as B operands (NT terms): with 16-byte key loads a lane's values are 16 of every 64 in e4m3, 8 of every 32 in bf16
+    bf16x8 q[NT][NS];
+#pragma unroll
+    for (int st = 0; st < NS; ++st) {
+      const int i0 = E4 ? 64 * (st / 2) + 16 * g + 8 * (st % 2) : 32 * st + 8 * g;
+      const size_t x = (((size_t)b * p.K + (live ? tok : 0)) * p.Hq + (live ? head : 0)) * DK + i0;
+      if constexpr (NT == 1) {
+        q[0][st] = *reinterpret_cast<const bf16x8*>(static_cast<const __bf16*>(p.q) + x);
+      } else {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = static_cast<const float*>(p.q)[x + e];
+#pragma unroll
+        for (int n3 = 0; n3 < NT; ++n3)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const __bf16 t = (__bf16)f[e];
+            q[n3][st][e] = t;
+            f[e] -= (float)t;
+          }
+      }
+    }
+    f32x4 o[NM];
+#pragma unroll
+    for (int t = 0; t < NM; ++t) o[t] = (f32x4)0.0f;
+    float m = -__builtin_inff(), l = 0.0f;
+
+    auto load = [&](int k0) {
+      T t;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int idx = (k0 + 16 * u) / pt, slot = (k0 + 16 * u) % pt;
+        int page = k0 + 16 * u < len ? pages[idx] : -1;  // (behind the sequence a row may name any page)
+        if (page < 0 || page >= cache.n_pages) page = -1;
+        t.page[u] = page;
+        const char* base = cache.pool + (size_t)max(page, 0) * cache.page_bytes;
+        const char* kp = base + kv_keys(cache, h) + ((size_t)(slot + col) * DK) * ES + 16 * g;
+#pragma unroll
+        for (int i = 0; i < T::NK; ++i) t.k[u][i] = *reinterpret_cast<const u32x4*>(kp + 64 * i);
+        const char* vp = base + kv_values(cache, h) + ((size_t)(slot + 4 * g) * DV) * ES + col * T::VW * 4;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int i = 0; i < T::VW; ++i) t.v[4 * u + r][i] = *reinterpret_cast<const uint32_t*>(vp + (size_t)r * DV * ES + 4 * i);
+        t.ks[u] = t.vs[u] = 1.0f;
+        if constexpr (E4) {
+          const float* sc = reinterpret_cast<const float*>(base + kv_scales(cache));
+          t.ks[u] = page < 0 ? 1.0f : sc[h];
+          t.vs[u] = page < 0 ? 1.0f : sc[H + h];  // (0 times another page's scale could be NaN)
+        }
+      }
+      return t;
+    };
+
+    const int kend = min(g1 * kGranule, len);
+    int k0 = g0 * kGranule + kTile * wave;
+    T cur;
+    if (k0 < kend) cur = load(k0);
+    for (; k0 < kend; k0 += kGranule) {
+      T nxt;
+      if (k0 + kGranule < kend) nxt = load(k0 + kGranule);
+      // scores of 32 keys
+      f32x4 x[2] = {(f32x4)0.0f, (f32x4)0.0f};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int st = 0; st < NS; ++st) {
+          u32x4 w;
+          if constexpr (E4) {
+            const uint32_t lo = cur.k[u][st / 2][2 * (st % 2)], hi = cur.k[u][st / 2][2 * (st % 2) + 1];
+            w = u32x4{bf16_of_e4m3(lo, false), bf16_of_e4m3(lo, true), bf16_of_e4m3(hi, false), bf16_of_e4m3(hi, true)};
+          } else {
+            w = cur.k[u][st];
+          }
+#pragma unroll
+          for (int n3 = NT - 1; n3 >= 0; --n3)
+            x[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), q[n3][st], x[u], 0, 0, 0);
+        }
+      }
+      const bool partial = k0 + kTile > least || cur.page[0] < 0 || cur.page[1] < 0;  // (the same for the wave)
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float sc = cur.ks[u] * p.scale * kLog2e;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          x[u][r] *= sc;
+          if (partial && (cur.page[u] < 0 || k0 + 16 * u + 4 * g + r >= limit)) x[u][r] = -__builtin_inff();
+          top = fmaxf(top, x[u][r]);
+        }
+      }
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      if (__any(top > m)) {
+        const float now = fmaxf(m, top);
+        const float keep = now == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - now);
+        m = now;
+        l *= keep;
+#pragma unroll
+        for (int t = 0; t < NM; ++t) o[t] *= keep;
+      }
+      const float base = m == -__builtin_inff() ? 0.0f : m;
+      bf16x8 pt8[NT];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float y = __builtin_amdgcn_exp2f(x[u][r] - base);
+          l += y;
+          float z = y * cur.vs[u];
+#pragma unroll
+          for (int n3 = 0; n3 < NT; ++n3) {
+            const __bf16 t = (__bf16)z;
+            pt8[n3][4 * u + r] = t;
+            z -= (float)t;
+          }
+        }
+      if (partial) {  // what nobody attends to may hold anything
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (cur.page[u] < 0 || k0 + 16 * u + 4 * g + r >= len)
+#pragma unroll
+              for (int i = 0; i < T::VW; ++i) cur.v[4 * u + r][i] = 0;
+      }
+      // V^T: 8 keys of channel NV col + t in a lane
+      bf16x8 vt[NM];
+#pragma unroll
+      for (int i = 0; i < T::VW; ++i) {
+        constexpr int CW = E4 ? 4 : 2;  // channels of a dword
+        u32x4 w[CW];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t x0 = cur.v[2 * r][i], x1 = cur.v[2 * r + 1][i];
+          if constexpr (E4) {
+            const uint32_t lo = perm(x1, x0, 0x05010400u), hi = perm(x1, x0, 0x07030602u);
+            w[0][r] = bf16_of_e4m3(lo, false);
+            w[1][r] = bf16_of_e4m3(lo, true);
+            w[2][r] = bf16_of_e4m3(hi, false);
+            w[3][r] = bf16_of_e4m3(hi, true);
+          } else {
+            w[0][r] = perm(x1, x0, 0x05040100u);
+            w[1][r] = perm(x1, x0, 0x07060302u);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < CW; ++e) vt[CW * i + e] = __builtin_bit_cast(bf16x8, w[e]);
+      }
+      bool odd = false;
+      if (partial && p.K > 1) {  // values that are not finite must not reach, as 0 v, tokens that do not see them
+#pragma unroll
+        for (int t = 0; t < NM; ++t)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) odd = odd || !(__builtin_fabsf((float)vt[t][e]) < __builtin_inff());
+      }
+      if (!__any(odd)) {
+#pragma unroll
+        for (int t = 0; t < NM; ++t)
+#pragma unroll
+          for (int n3 = NT - 1; n3 >= 0; --n3)
+            o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt[t], pt8[n3], o[t], 0, 0, 0);
+      } else {
+        for (int k = 0; k < p.K; ++k) {  // one drafted token's keys at a time
+          const int lim = least + k;
+#pragma unroll
+          for (int t = 0; t < NM; ++t) {
+            bf16x8 w = vt[t];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (k0 + 16 * (e / 4) + 4 * g + e % 4 >= lim) w[e] = (__bf16)0.0f;
+            f32x4 y = (f32x4)0.0f;
+#pragma unroll
+            for (int n3 = NT - 1; n3 >= 0; --n3) y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, pt8[n3], y, 0, 0, 0);
+            if (tok == k) o[t] += y;
+          }
+        }
+      }
+      cur = nxt;
+    }
+
+    // join the waves
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (g == 0) sm[wave][col] = m, sl[wave][col] = l;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int t = 0; t < NM; t += 4)
+        *reinterpret_cast<f32x4*>(&so[wave][col][NM * (4 * g + r) + t]) = f32x4{o[t][r], o[t + 1][r], o[t + 2][r], o[t + 3][r]};
+    __syncthreads();
+    const bool complete = g0 == 0 && g1 == n;
+    float* part = nullptr;
+    if (!complete) {
+      part = a.parts + (2 * (size_t)blockIdx.x + (at == mine ? 0 : 1)) * part_floats(DV);
+      if (tid == 0 && g0 == 0) {  // the unit begins here and ends with another worker
+        const long long per = max(((long long)prefix[p.B] * units + a.workers - 1) / a.workers, (long long)kLeastRun);
+        a.joins[blockIdx.x] = Join{b * units + unit, (int)((at + n - 1) / per), at == mine ? 0 : 1, 0};
+      }
+    }
+    for (int i = tid; i < kAttnColumns * DV / 4; i += kThreads) {
+      const int c = i / (DV / 4), d = 4 * (i % (DV / 4));
+      float top = sm[0][c];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sm[w][c]);
+      const float base = top == -__builtin_inff() ? 0.0f : top;
+      f32x4 y = (f32x4)0.0f;
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(sm[w][c] - base);
+        sum += f * sl[w][c];
+        y += f * *reinterpret_cast<const f32x4*>(&so[w][c][d]);
+      }
+      if (!complete) {
+        *reinterpret_cast<f32x4*>(part + c * DV + d) = y;
+        if (d == 0) part[kAttnColumns * DV + c] = top, part[kAttnColumns * (DV + 1) + c] = sum;
+        continue;
+      }
+      const int c2 = kAttnColumns * ct + c, tk = c2 / a.G;
+      if (tk >= p.K) continue;
+      y *= sum == 0.0f ? 0.0f : 1.0f / sum;
+      const size_t x = (((size_t)b * p.K + tk) * p.Hq + h * a.G + c2 % a.G) * DV + d;
+      if (p.o_f32) {
+        *reinterpret_cast<f32x4*>(static_cast<float*>(p.o) + x) = y;
+      } else {
+        bf16x4 z;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] = (__bf16)y[e];
+        *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(p.o) + x) = z;
+      }
+    }
+    __syncthreads();
+    at += g1 - g0;
+  }
+}
+
+// Joins the parts of a unit that several workers share: a wave a row of queries.
+template <int DV>
+__global__ __launch_bounds__(kThreads) void kda_attn_join_kernel(DecodePlan a) {
+  constexpr int ND = DV / 64;
+  const int w0 = blockIdx.x, lane = threadIdx.x % 64, c = blockIdx.y * kWaves + threadIdx.x / 64;
+  const Join j = a.joins[w0];
+  if (j.unit < 0) return;
+  const AttnDecodeParams& p = a.p;
+  const int units = a.CT * p.c.H, b = j.unit / units, ct = j.unit % units / p.c.H, h = j.unit % p.c.H;
+  const int c2 = kAttnColumns * ct + c, tk = c2 / a.G;
+  if (tk >= p.K) return;
+  // worker w0's part is its first or its second, the others' their first
+  auto part = [&](int w) { return a.parts + (2 * (size_t)w + (w == w0 ? j.slot : 0)) * part_floats(DV); };
+  float top = -__builtin_inff();
+  for (int w = w0 + lane; w <= j.last; w += 64) top = fmaxf(top, part(w)[kAttnColumns * DV + c]);
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) top = fmaxf(top, __shfl_xor(top, m));
+  const float base = top == -__builtin_inff() ? 0.0f : top;
+  float y[ND], sum = 0.0f;
+#pragma unroll
+  for (int e = 0; e < ND; ++e) y[e] = 0.0f;
+  for (int w1 = w0; w1 <= j.last; w1 += 64) {
+    float f = 0.0f;
+    if (w1 + lane <= j.last) {
+      const float* x = part(w1 + lane) + kAttnColumns * DV + c;
+      f = __builtin_amdgcn_exp2f(x[0] - base);
+      sum += f * x[kAttnColumns];
+    }
+    const int n = min(64, j.last - w1 + 1);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float fi = __shfl(f, i);
+      const float* x = part(w1 + i) + c * DV + ND * lane;
+#pragma unroll
+      for (int e = 0; e < ND; ++e) y[e] += fi * x[e];
+    }
+  }
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) sum += __shfl_xor(sum, m);
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const size_t at = (((size_t)b * p.K + tk) * p.Hq + h * a.G + c2 % a.G) * DV + ND * lane;
+#pragma unroll
+  for (int e = 0; e < ND; ++e) {
+    if (p.o_f32) static_cast<float*>(p.o)[at + e] = y[e] * inv;
+    else static_cast<__bf16*>(p.o)[at + e] = (__bf16)(y[e] * inv);
+  }
+}
+
+// Whether a call takes its units whole, a workgroup each: no workspace and no second launch.
+bool takes_whole(int page_tokens, int width) { return (long long)width * page_tokens <= kWholeUnits; }
+
+template <int NT, bool E4, int DK, int DV>
+hipError_t launch_one(const AttnDecodeParams& p, hipStream_t s) {
+  DecodePlan a;
+  a.p = p;
+  a.G = p.Hq / p.c.H;
+  a.CT = columns(p.K, a.G);
+  const bool whole = takes_whole(p.c.page_tokens, p.c.width);
+  a.workers = whole ? 0 : kWorkers;
+  a.parts = static_cast<float*>(p.ws);
+  a.joins = whole ? nullptr : reinterpret_cast<Join*>(a.parts + 2 * (size_t)kWorkers * part_floats(DV));
+  const unsigned grid = whole ? (unsigned)p.B * a.CT * p.c.H : kWorkers;
+  hipLaunchKernelGGL((kda_attn_decode_kernel<NT, E4, DK, DV>), dim3(grid), dim3(kThreads),
+                     whole ? 0 : sizeof(int) * ((size_t)p.B + 1), s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || whole) return e;
+  const int rows = std::min(kAttnColumns, p.K * a.G);
+  hipLaunchKernelGGL((kda_attn_join_kernel<DV>), dim3(kWorkers, (rows + kWaves - 1) / kWaves), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int NT, bool E4>
+hipError_t pick_dims(const AttnDecodeParams& p, hipStream_t s) {
+  if (p.c.dk == 128) return p.c.dv == 128 ? launch_one<NT, E4, 128, 128>(p, s) : launch_one<NT, E4, 128, 64>(p, s);
+  return p.c.dv == 128 ? launch_one<NT, E4, 64, 128>(p, s) : launch_one<NT, E4, 64, 64>(p, s);
+}
+
+}  // namespace
+
+size_t attn_decode_workspace(int dv, int page_tokens, int width) {
+  if (takes_whole(page_tokens, width)) return 0;
+  return (size_t)kWorkers * (2 * part_floats(dv) * sizeof(float) + sizeof(Join));
+}
+
+hipError_t launch_attn_decode(const AttnDecodeParams& p, int q_dtype, hipStream_t s) {
+  const KvCache& c = p.c;
+  if (p.B < 1 || p.K < 1 || c.H < 1 || p.Hq % c.H || (c.dk != 64 && c.dk != 128) || (c.dv != 64 && c.dv != 128) ||
+      c.page_tokens % 16)
+    return hipErrorInvalidValue;
+  if (q_dtype == 1) return c.e4m3 ? pick_dims<1, true>(p, s) : pick_dims<1, false>(p, s);
+  return c.e4m3 ? pick_dims<3, true>(p, s) : pick_dims<3, false>(p, s);
+}
+
+}  // namespace kda

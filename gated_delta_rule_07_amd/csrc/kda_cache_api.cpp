@@ -18,43 +18,8 @@ static_assert(kda::kMaxTree == KDA_MAX_TREE && kda::kMaxPages == KDA_MAX_PAGES &
                   kda::kMaxPagedSeqs == KDA_MAX_PAGED_SEQS,
               "limits of the header");
 
-kda_status launched(hipError_t e) {
-  if (e == hipSuccess) return KDA_OK;
-  kda::set_last_hip_error((int)e);
-  return KDA_ERR_HIP;
-}
-
 // One workgroup of up to 512 threads for each of B H states, fewer than 2^32 threads in all.
 bool states_ok(int B, int H) { return (long long)B * H <= (1LL << 22); }
-
-template <size_t N>
-bool any_overlap(Span out, const Span (&ins)[N]) {
-  for (const Span& s : ins)
-    if (overlap(out, s)) return true;
-  return false;
-}
-
-Span opt_span(const void* p, size_t bytes) { return p ? span(p, bytes) : Span{0, 0}; }
-
-// n rows of `len` bytes, `stride` bytes apart.
-struct Rows {
-  uintptr_t at;
-  unsigned long long n, len, stride;
-  Span all() const { return n ? Span{at, at + (n - 1) * stride + len} : Span{0, 0}; }
-};
-
-// Whether two sets of rows share a byte.  Rows of one stride that lie side by
-// side (slices of one wider row) do not; for different strides, sets whose
-// ranges meet are taken to.
-bool rows_overlap(const Rows& a, const Rows& b) {
-  if (!overlap(a.all(), b.all())) return false;
-  if (a.n <= 1 && b.n <= 1) return true;
-  const unsigned long long st = a.n > 1 ? a.stride : b.stride;
-  if ((a.n > 1 && b.n > 1 && a.stride != b.stride) || a.len > st || b.len > st) return true;
-  // offset of b's rows in a's raster
-  const unsigned long long d = b.at >= a.at ? (b.at - a.at) % st : (st - (a.at - b.at) % st) % st;
-  return d < a.len || st - d < b.len;
-}
 
 bool table_ok(int n_rows, int width, int n_pages) {
   return n_rows >= 1 && width >= 1 && (long long)n_rows * width <= (1LL << 26) && n_pages >= 1 && n_pages <= KDA_MAX_PAGES;

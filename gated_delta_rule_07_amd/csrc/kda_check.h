@@ -7,6 +7,8 @@
 
 #include "../../include/kda.h"
 
+#include <hip/hip_runtime_api.h>
+
 namespace kda {
 
 // Records the hipError_t that kda_last_hip_error returns on this thread.
@@ -40,6 +42,35 @@ inline Span span(const void* p, size_t bytes) {
 }
 inline bool overlap(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
 
+template <size_t N>
+inline bool any_overlap(Span out, const Span (&ins)[N]) {
+  for (const Span& s : ins)
+    if (overlap(out, s)) return true;
+  return false;
+}
+
+inline Span opt_span(const void* p, size_t bytes) { return p ? span(p, bytes) : Span{0, 0}; }
+
+// n rows of `len` bytes, `stride` bytes apart.
+struct Rows {
+  uintptr_t at;
+  unsigned long long n, len, stride;
+  Span all() const { return n ? Span{at, at + (n - 1) * stride + len} : Span{0, 0}; }
+};
+
+// Whether two sets of rows share a byte.  Rows of one stride that lie side by
+// side (slices of one wider row) do not; for different strides, sets whose
+// ranges meet are taken to.
+inline bool rows_overlap(const Rows& a, const Rows& b) {
+  if (!overlap(a.all(), b.all())) return false;
+  if (a.n <= 1 && b.n <= 1) return true;
+  const unsigned long long st = a.n > 1 ? a.stride : b.stride;
+  if ((a.n > 1 && b.n > 1 && a.stride != b.stride) || a.len > st || b.len > st) return true;
+  // offset of b's rows in a's raster
+  const unsigned long long d = b.at >= a.at ? (b.at - a.at) % st : (st - (a.at - b.at) % st) % st;
+  return d < a.len || st - d < b.len;
+}
+
 // Element counts fit in size_t and every row index used by the kernels fits in
 // an int64; the kernels index tokens with 64-bit arithmetic.
 inline bool sizes_ok(long long B, long long T, long long H, long long dk, long long dv) {
@@ -49,6 +80,12 @@ inline bool sizes_ok(long long B, long long T, long long H, long long dk, long l
   (void)dk;
   (void)dv;
   return true;
+}
+
+inline kda_status launched(hipError_t e) {
+  if (e == hipSuccess) return KDA_OK;
+  set_last_hip_error((int)e);
+  return KDA_ERR_HIP;
 }
 
 }  // namespace check

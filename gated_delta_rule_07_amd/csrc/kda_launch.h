@@ -338,6 +338,69 @@ hipError_t launch_cache_free(int* table, int* ref, const int* rows, int n, int n
 hipError_t launch_cache_compact(const CompactParams& p, hipStream_t s);
 hipError_t launch_cache_copy(const CopyParams& p, hipStream_t s);
 
+// Pages of keys and values: the attention layers beside the recurrent ones.
+struct KvCache {
+  char* pool;  // [n_pages][page_bytes]
+  size_t page_bytes;
+  const int* table;  // [n_rows][width]
+  const int* rows;   // [N] or null: row b
+  int n_pages, page_tokens, n_rows, width, H, dk, dv, e4m3;
+};
+struct AppendParams {
+  KvCache c;
+  const void* k;
+  const void* v;
+  const void* q;  // null: no queries
+  void* k_out;    // null: not written
+  void* q_out;
+  long long k_stride, v_stride, q_stride, k_out_stride, q_out_stride;  // elements between tokens
+  const int* lens;       // [N], tokens on the pages before the call
+  const int* cu;         // [N + 1] or null: one token a sequence
+  const int* positions;  // [total] or null: the token's place in its sequence
+  const float* inv_freq;
+  int rot, adjacent, N, total, Hq;
+};
+struct ReadParams {
+  KvCache c;
+  const int* cu;      // [N + 1]
+  const int* starts;  // [N] or null: 0
+  void* k_out;
+  void* v_out;
+  int N, total;
+};
+hipError_t launch_kv_append(const AppendParams& p, int io_dtype, hipStream_t s);
+hipError_t launch_kv_read(const ReadParams& p, int out_dtype, hipStream_t s);
+
+// Attention over a whole prompt.
+struct AttnParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  long long q_stride, k_stride, v_stride, o_stride;  // elements between tokens
+  const int* cu_q;  // [N + 1] or null: N sequences of total_q / N tokens
+  const int* cu_k;
+  int N, total_q, total_k, Hq, Hk, dk, dv;
+  int o_f32;
+  float scale;
+};
+hipError_t launch_attn_fwd(const AttnParams& p, int io_dtype, hipStream_t s);
+
+// Attention of one or a few tokens a sequence over its pages.
+constexpr int kAttnColumns = 16;  // rows of queries (tokens x heads of a group) of one matrix-core tile
+struct AttnDecodeParams {
+  KvCache c;
+  const void* q;    // [B][K][Hq][dk]
+  const int* lens;  // [B]
+  void* o;          // [B][K][Hq][dv]
+  void* ws;
+  int B, K, Hq;
+  int o_f32;
+  float scale;
+};
+size_t attn_decode_workspace(int dv, int page_tokens, int width);  // bytes
+hipError_t launch_attn_decode(const AttnDecodeParams& p, int q_dtype, hipStream_t s);
+
 bool decode_supported(int io_dtype, int dk, int dv);
 hipError_t launch_decode(const DecodeParams& p, int io_dtype, hipStream_t s);
 

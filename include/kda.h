@@ -65,7 +65,8 @@ extern "C" {
 
 typedef enum {
   KDA_F32 = 0,  /* IEEE binary32 */
-  KDA_BF16 = 1  /* bfloat16; outputs are rounded to nearest even */
+  KDA_BF16 = 1, /* bfloat16; outputs are rounded to nearest even */
+  KDA_E4M3 = 2  /* 8 bits (4 exponent, 3 mantissa; largest 448, no infinity): of cached keys and values only */
 } kda_dtype;
 
 typedef enum {
@@ -572,6 +573,146 @@ kda_status kda_tree_verify(const void* q, const void* k, const void* v, kda_dtyp
 kda_status kda_tree_commit(const void* k, kda_dtype qkv_dtype, const float* alpha, const float* u, const int* parents,
                            const int* n_nodes, const int* last, float* pool, int n_pages, const int* pages_in,
                            const int* pages_out, int B, int K, int H, int d_k, int d_v, hipStream_t stream);
+
+/* ---- attention layers beside the recurrent ones ----------------------------------------
+ *
+ * A hybrid model has an attention layer after every few recurrent ones.  Query head h
+ * attends with the keys and values of head h / (H_q / H_kv) (grouped heads; H_q a multiple
+ * of H_kv), and its output is
+ *     o = sum_j p_j v_j,    p = softmax over the j it sees of  scale * q . k_j.
+ * Maximum, sum and outputs are carried in fp32.  A query that sees nothing (or only scores of
+ * minus infinity) gives zeros.  What a query does not see has no influence on it, whatever
+ * it holds: infinities and NaN too.
+ *
+ * Keys and values of earlier tokens lie in a pool of pages, page_tokens tokens of one layer
+ * each, named by page tables like those of kda_cache_fork (entry j of a sequence's row: its
+ * tokens [j * page_tokens, (j + 1) * page_tokens)); kda_cache_fork, _free, _compact and _copy serve them as
+ * they serve states.  A page:
+ *     keys   [H_kv][page_tokens][d_k], then values [H_kv][page_tokens][d_v], in kv_dtype;
+ *     KDA_E4M3: then scales [2][H_kv] fp32, of each head's keys, then of its values, and
+ *     zeros or anything up to a multiple of 16 bytes: what a code stands for is code * scale.
+ * Arguments of the calls on pages:
+ *   pool       : [n_pages][page_bytes] (kda_kv_page_bytes), 1 <= n_pages <= KDA_MAX_PAGES
+ *   kv_dtype   : KDA_BF16 or KDA_E4M3
+ *   page_tokens: 16, 32, 64 or 128
+ *   table      : [n_rows][width] int32, DEVICE memory, n_rows * width <= 2^26 and
+ *                width * page_tokens < 2^31 (KDA_ERR_SHAPE)
+ *   rows       : [N] int32, DEVICE memory, the table row of each sequence of the call, or
+ *                NULL: row b.  A row outside [0, n_rows) is padding.
+ *   d_k, d_v   : 64 or 128 (KDA_ERR_UNSUPPORTED otherwise)
+ * Lists in device memory that are wrong never make a kernel access memory out of range.
+ * H_q, H_kv <= KDA_MAX_HEADS and tokens of a call <= KDA_MAX_CALL_TOKENS, else KDA_ERR_SHAPE.
+ */
+
+#define KDA_MAX_HEADS 4096           /* most heads of one call of an attention layer */
+#define KDA_MAX_CALL_TOKENS 4194304  /* most tokens of one call of an attention layer */
+
+/*
+ * Causal attention over whole prompts, with packed sequences of different lengths.
+ * Query i of a sequence with n_q queries and n_k keys sees the keys j <= i + n_k - n_q: with
+ * n_k = n_q the causal mask of a prompt, with more keys that of a prompt behind a cached
+ * prefix (kda_kv_read), with fewer the first queries see nothing.
+ *
+ *   q      : total_q rows of H_q heads of d_k values, dtype, q_stride apart      (read)
+ *   k, v   : total_k rows of H_kv heads of d_k and d_v values                    (read)
+ *            (strides in elements, multiples of 16 bytes: rows may be slices of a fused
+ *            projection's rows; heads and values inside a row are dense)
+ *   cu_seqlens   : [N + 1] int32, DEVICE memory: sequence b's queries are the rows
+ *            [cu[b], cu[b + 1]), clamped to [0, total_q]; NULL: N sequences of total_q / N
+ *            queries and total_k / N keys (both have to divide, KDA_ERR_SHAPE)
+ *   cu_seqlens_k : the same for keys and values, clamped to [0, total_k]; NULL: cu_seqlens,
+ *            total_k = total_q (KDA_ERR_SHAPE).  NULL when cu_seqlens is (KDA_ERR_NULL).
+ *   o      : total_q rows of H_q heads of d_v values, o_dtype, o_stride apart (written; rows
+ *            outside every sequence are left as they were)
+ *   scale  : finite (KDA_ERR_SHAPE)
+ *   d_k, d_v: 16, 32, 64 or 128.  N >= 1; total_q, total_k >= 0 (no queries: nothing is done)
+ *
+ * cu_seqlens may not decrease.  o may share no byte with another array
+ * (KDA_ERR_ALIAS).  fp32 inputs are multiplied in fp32; bf16 inputs on the bf16 matrix
+ * cores with fp32 accumulation, the probabilities rounded to bf16 (d_k = d_v in {64, 128}) or kept in fp32.
+ */
+kda_status kda_attn_fwd(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                        long long v_stride, kda_dtype dtype, float scale, const int* cu_seqlens,
+                        const int* cu_seqlens_k, int N, int total_q, int total_k, void* o, long long o_stride,
+                        kda_dtype o_dtype, int H_q, int H_kv, int d_k, int d_v, hipStream_t stream);
+
+/* Bytes of a page of keys and values, to *bytes.  Host only. */
+kda_status kda_kv_page_bytes(kda_dtype kv_dtype, int page_tokens, int H_kv, int d_k, int d_v, size_t* bytes);
+
+/*
+ * Puts new tokens' keys and values on the pages of their sequences, the keys (and queries, where
+ * given) turned by position on the way as kda_qk_norm does it:
+ *     (a, b) -> (a cos f - b sin f, b cos f + a sin f),  f = pos * inv_freq[i].
+ *
+ *   k, v, q   : `total` rows of H_kv, H_kv and H_q heads, dtype, as kda_attn_fwd's    (read)
+ *               (q NULL: no queries, q_out NULL, H_q is not looked at)
+ *   cu_seqlens: [N + 1] int32, DEVICE memory, the new tokens of each sequence, clamped to
+ *               [0, total]; it may not decrease.  NULL: one token a sequence, total = N (KDA_ERR_SHAPE)
+ *   lens      : [N] int32, DEVICE memory, the tokens that each sequence has on its pages (below
+ *               0: taken as 0).  Token i of sequence b goes to place lens[b] + i of its row.  (read)
+ *   positions : [total] int32 positions for the rotation, or NULL: the token's place
+ *   inv_freq  : [rot / 2] fp32;  rot: a multiple of 16 in [0, d_k]  (0: nothing is turned)
+ *   q_out, k_out: the turned queries and keys as dense rows of `dtype`, with strides; k_out may be
+ *               NULL.  q_out may be q itself with the same stride, and so may k_out be k.
+ *               Rows outside every sequence are left as they were.     (written)
+ *   pool      : the pages' entries for the new tokens                  (written)
+ *   N         : 1 .. KDA_MAX_PAGED_SEQS
+ *
+ * Angles are reduced in fp64, everything else is fp32; what goes to a bf16 page, q_out or k_out is
+ * rounded once.  KDA_E4M3: each head's keys (values) on a page have the scale s, the smallest power
+ * of two >= 2^-100 that brings the largest finite of them to 448 or below; codes are y / s rounded
+ * to nearest even, values that are not finite become NaN.  A page that holds earlier tokens of the
+ * sequence (its place in the row before lens[b]) keeps its scale, or, where the new tokens need a
+ * larger one, has their codes rounded to that one -- exact, but for values below 2^-14 of the largest.
+ *
+ * A token without a page (padding, an entry outside [0, n_pages), a place behind the row's end) is not
+ * stored; its rows of q_out and k_out are written all the same.  Nor is, rather than let them
+ * race, any token whose page another sequence's new tokens go to, or another place of its own row.
+ */
+kda_status kda_kv_append(const void* k, long long k_stride, const void* v, long long v_stride, const void* q,
+                         long long q_stride, kda_dtype dtype, const int* positions, const float* inv_freq, int rot,
+                         kda_pairing pairing, void* q_out, long long q_out_stride, void* k_out,
+                         long long k_out_stride, void* pool, kda_dtype kv_dtype, int n_pages, int page_tokens,
+                         const int* table, int n_rows, int width, const int* rows, const int* lens,
+                         const int* cu_seqlens, int N, int total, int H_q, int H_kv, int d_k, int d_v,
+                         hipStream_t stream);
+
+/*
+ * Cached keys and values back as dense rows: k_out [total][H_kv][d_k], v_out [total][H_kv][d_v], out_dtype
+ * (bf16: exact).  Rows [cu[b], cu[b + 1]) are sequence b's tokens from place starts[b] on
+ * (starts [N] int32, DEVICE memory; NULL or below 0: from 0 on).  A token without a page leaves its rows as they
+ * were.  cu_seqlens as above, not NULL.  N: 1 .. KDA_MAX_PAGED_SEQS.
+ */
+kda_status kda_kv_read(const void* pool, kda_dtype kv_dtype, int n_pages, int page_tokens, const int* table, int n_rows,
+                       int width, const int* rows, const int* starts, const int* cu_seqlens, void* k_out, void* v_out,
+                       kda_dtype out_dtype, int N, int total, int H_kv, int d_k, int d_v, hipStream_t stream);
+
+/*
+ * Attention of the last K tokens of each sequence over its pages: K = 1 is a decode step behind
+ * kda_kv_append, K > 1 a chain of drafted tokens, all of them appended.  Token t of sequence b sees its
+ * first lens[b] - K + 1 + t tokens.
+ *
+ *   q   : [B][K][H_q][d_k] q_dtype (KDA_F32 or KDA_BF16)                    (read)
+ *   pool: as above                                                        (read)
+ *   lens: [B] int32, DEVICE memory, the tokens on each sequence's pages, these K among them;
+ *         clamped to [0, width * page_tokens].  Tokens on a page out of range are not seen.   (read)
+ *   o   : [B][K][H_q][d_v] o_dtype (written; the rows of padding are left as they were)
+ *   workspace: device memory of workspace_bytes bytes (kda_attn_decode_plan), 16-byte aligned;
+ *         its contents on entry do not matter.  NULL when the plan says 0.  Calls that may run
+ *         at the same time need one each.                                   (written)
+ *   B: 1 .. KDA_MAX_PAGED_SEQS, K: 1 .. KDA_MAX_ATTN_TOKENS
+ *
+ * fp32 queries are multiplied as three bf16 terms, and so are their probabilities: results
+ * are fp32's.  With bf16 queries the probabilities are rounded to bf16.  Errors: KDA_ERR_NULL (workspace needed),
+ * KDA_ERR_SHAPE (workspace_bytes too small), KDA_ERR_ALIAS (o or workspace overlaps another array).
+ */
+#define KDA_MAX_ATTN_TOKENS 16 /* most tokens of a sequence in one kda_attn_decode call */
+kda_status kda_attn_decode_plan(kda_dtype kv_dtype, int page_tokens, int width, int B, int K, int H_q, int H_kv, int d_k,
+                                int d_v, size_t* workspace_bytes);
+kda_status kda_attn_decode(const void* q, kda_dtype q_dtype, float scale, const void* pool, kda_dtype kv_dtype, int n_pages,
+                           int page_tokens, const int* table, int n_rows, int width, const int* rows, const int* lens,
+                           void* o, kda_dtype o_dtype, void* workspace, size_t workspace_bytes, int B, int K, int H_q,
+                           int H_kv, int d_k, int d_v, hipStream_t stream);
 
 /* Human-readable text for a status code (static storage; never NULL). */
 const char* kda_status_string(kda_status s);
