@@ -7,6 +7,7 @@
 // Scores are formed transposed, S^T = K Q^T, so that a lane holds one query's scores: the maximum
 // and the sum are then mostly a lane's own, and P^T as the product leaves it is the operand of O^T = V^T P^T.
 #include <algorithm>
+#include <type_traits>
 
 #include "kda_kv_device.h"
 
@@ -178,9 +179,231 @@ __global__ __launch_bounds__(256) void kda_attn_plain_kernel(AttnParams p) {
   }
 }
 
+// ---- bf16 with heads of 64 and 128 ---------------------------------------------------------
+// A wave holds 32 queries, a workgroup of NW waves 32 NW; 64 keys and values at a time are copied
+// straight into LDS, two buffers in turn, one barrier a tile.  32x32x16 matrix cores:
+//   S^T (64 keys x 32 queries) = K Q^T, K's rows read 16 bytes a lane;
+//   O^T (DV x 32) += V^T P^T, V^T read through the LDS transpose (4 keys of 16 channels a group of
+//   16 lanes); the keys of a step are taken in the order in which S^T leaves them in a lane.
+// LDS rows are dense; their 16-byte pieces are exchanged (xor with bits of the row) so that the lanes of a
+// read fall on different banks.
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) void lds_void;
+typedef const __attribute__((address_space(1))) void global_void;
+
+constexpr int kTileKeys = 64;
+
+// 16 bytes a lane from `src` to dst + 16 lane (dst the same for the wave).  Written out because the
+// compiler, which cannot tell the buffer that is filled from the one that is read, would wait for every copy
+// before the next LDS read; it writes no register, and tile_barrier() waits for it.
+__device__ __forceinline__ void copy16(const char* src, char* dst) {
+  const uint32_t at = (uint32_t)(uintptr_t)(lds_void*)dst;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory", "m0");
+}
+// Every wave's copies have landed, and its reads of the other buffer are done.
+__device__ __forceinline__ void tile_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Where the 16-byte piece c of row r lies in its row.
+template <int D>
+__device__ __forceinline__ int key_piece(int r, int c) { return D == 128 ? c ^ (r & 15) : c ^ ((r >> 1) & 7); }
+template <int D>
+__device__ __forceinline__ int value_piece(int r, int c) { return D == 128 ? c ^ (4 * (r & 3)) : c ^ (4 * ((r >> 1) & 1)); }
+
+template <int NW, int DK, int DV>
+struct FastCfg {
+  static constexpr int BM = 32 * NW;
+  static constexpr int NT = 64 * NW;
+  static constexpr int KB = kTileKeys * DK * 2, VB = kTileKeys * DV * 2;  // bytes of a tile
+  static constexpr int NK = KB / 1024 / NW, NV = VB / 1024 / NW;          // 1 KB copies of a wave
+  static constexpr int LDS = 2 * (KB + VB);
+  static_assert(NK * NW * 1024 == KB && NV * NW * 1024 == VB, "whole copies");
+};
+
+template <int NW, int DK, int DV>
+__global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int tiles, unsigned chunk) {
+  using C = FastCfg<NW, DK, DV>;
+  __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
+  const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), c = lane % 32, hf = lane / 32;
+  const int G = p.Hq / p.Hk;
+  // Workgroups go to the 8 dies in turn: each die takes a run of neighbours, which share keys and values in its L2.
+  const unsigned w = blockIdx.x % 8 * chunk + blockIdx.x / 8;
+  if (w >= (unsigned)tiles * p.Hq) return;
+  const int hk = w / ((unsigned)tiles * G), in = w % ((unsigned)tiles * G), h = hk * G + in % G;
+  Part s;
+  if (!part_of<C::BM>(p, in / G, s)) return;
+  const int row = s.r0 + 32 * wave + c;  // this lane's query
+  const int shift = s.nk - s.nq;
+  const int limit = row < s.nq ? row + shift + 1 : 0;
+  const int last = min(s.r0 + C::BM, s.nq) + shift;                       // keys of the workgroup
+  const int wlast = min(min(s.r0 + 32 * wave + 32, s.nq) + shift, last);  // of the wave
+  const int ntiles = (last + kTileKeys - 1) / kTileKeys;
+
+  bf16x8 q[DK / 16];
+  {
+    const __bf16* x = static_cast<const __bf16*>(p.q) + (size_t)(s.q0 + min(row, s.nq - 1)) * p.q_stride + (size_t)h * DK + 8 * hf;
+#pragma unroll
+    for (int st = 0; st < DK / 16; ++st) q[st] = *reinterpret_cast<const bf16x8*>(x + 16 * st);
+    // (waited for here: a wait at their use, inside the loop, would wait for the tiles' copies too)
+#pragma unroll
+    for (int st = 0; st < DK / 16; ++st) asm volatile("" : "+v"(q[st]));
+  }
+  const char* kg = reinterpret_cast<const char*>(static_cast<const __bf16*>(p.k) + (size_t)s.k0 * p.k_stride + (size_t)hk * DK);
+  const char* vg = reinterpret_cast<const char*>(static_cast<const __bf16*>(p.v) + (size_t)s.k0 * p.v_stride + (size_t)hk * DV);
+  auto copy = [&](int t) {
+    char* kl = lds + (t & 1) * (C::KB + C::VB);
+    char* vl = kl + C::KB;
+#pragma unroll
+    for (int i = 0; i < C::NK; ++i) {
+      const int e = (wave * C::NK + i) * 64 + lane, r = e / (DK / 8), cc = key_piece<DK>(r, e % (DK / 8));
+      const char* src = kg + (size_t)min(t * kTileKeys + r, s.nk - 1) * (2 * p.k_stride) + 16 * cc;
+      copy16(src, kl + (wave * C::NK + i) * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < C::NV; ++i) {
+      const int e = (wave * C::NV + i) * 64 + lane, r = e / (DV / 8), cc = value_piece<DV>(r, e % (DV / 8));
+      const char* src = vg + (size_t)min(t * kTileKeys + r, s.nk - 1) * (2 * p.v_stride) + 16 * cc;
+      copy16(src, vl + (wave * C::NV + i) * 1024);
+    }
+  };
+
+  const float scale = p.scale * kLog2e;
+  f32x16 o[DV / 32];
+#pragma unroll
+  for (int t = 0; t < DV / 32; ++t) o[t] = (f32x16)0.0f;
+  float m = -__builtin_inff(), l = 0.0f;
+  if (ntiles > 0) copy(0);
+  // One tile.  EDGE: some of the wave's queries do not see all of it.
+  auto step = [&](int t, auto edge) {
+    constexpr bool EDGE = decltype(edge)::value;
+    const int k0 = t * kTileKeys;
+    const char* kl = lds + (t & 1) * (C::KB + C::VB);
+    const char* vl = kl + C::KB;
+    f32x16 x[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      x[u] = (f32x16)0.0f;
+      const int r = 32 * u + c;
+#pragma unroll
+      for (int st = 0; st < DK / 16; ++st) {
+        const bf16x8 a = *reinterpret_cast<const bf16x8*>(kl + r * (2 * DK) + 16 * key_piece<DK>(r, 2 * st + hf));
+        x[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[st], x[u], 0, 0, 0);
+      }
+    }
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        x[u][r] *= scale;  // (before the maximum: a scale below 0 turns the order round)
+        if constexpr (EDGE) x[u][r] = k0 + 32 * u + 8 * (r / 4) + 4 * hf + r % 4 >= limit ? -__builtin_inff() : x[u][r];
+        top = fmaxf(top, x[u][r]);
+      }
+    top = fmaxf(top, __shfl_xor(top, 32));
+    if (__any(top > m)) {
+      const float now = fmaxf(m, top);
+      const float keep = now == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - now);
+      m = now;
+      l *= keep;
+#pragma unroll
+      for (int i = 0; i < DV / 32; ++i) o[i] *= keep;
+    }
+    const float base = m == -__builtin_inff() ? 0.0f : m;
+    bf16x8 pt[4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float y = __builtin_amdgcn_exp2f(x[u][r] - base);
+        l += y;
+        pt[2 * u + r / 8][r % 8] = (__bf16)y;
+      }
+    // V^T operand of channels [32 i, 32 i + 32), keys [16 st, 16 st + 16): slot e of half hf is key 8 (e / 4) + 4 hf + e % 4
+    auto values = [&](int i, int st) {
+      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+      s16x4 y[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = 16 * st + 8 * j + 4 * hf + lane % 16 / 4;
+        const int cc = 4 * i + 2 * (lane / 16 % 2) + lane % 4 / 2;
+        y[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vl + r * (2 * DV) + 16 * value_piece<DV>(r, cc) + 8 * (lane % 2)));
+      }
+      typedef short s16x8 __attribute__((ext_vector_type(8)));
+      return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(y[0], y[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    if constexpr (EDGE) {  // values that are not finite must not reach, as 0 v, queries that do not see them
+      bool odd = false;
+      for (int i = lane; i < C::VB / 16; i += 64) {
+        const u32x4 y = *reinterpret_cast<const u32x4*>(vl + 16 * i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) odd = odd || (y[e] & 0x7f80u) == 0x7f80u || (y[e] & 0x7f800000u) == 0x7f800000u;
+      }
+      if (__builtin_expect(__any(odd), 0)) {
+        for (int r = 0; r < 32; ++r) {  // one query at a time, with the values that it sees
+          const int lim = __shfl(limit, r);
+#pragma unroll
+          for (int i = 0; i < DV / 32; ++i) {
+            f32x16 y = (f32x16)0.0f;
+#pragma unroll
+            for (int st = 0; st < 4; ++st) {
+              bf16x8 a = values(i, st);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (k0 + 16 * st + 8 * (e / 4) + 4 * hf + e % 4 >= lim) a[e] = (__bf16)0.0f;
+              y = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, pt[st], y, 0, 0, 0);
+            }
+            if (c == r) o[i] += y;
+          }
+        }
+        return;
+      }
+    }
+#pragma unroll
+    for (int st = 0; st < 4; ++st)
+#pragma unroll
+      for (int i = 0; i < DV / 32; ++i) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values(i, st), pt[st], o[i], 0, 0, 0);
+  };
+  const int nfull = max(min((s.r0 + shift + 1) / kTileKeys, ntiles), 0);  // tiles that every query of the workgroup sees whole
+  for (int t = 0; t < nfull; ++t) {
+    tile_barrier();
+    if (t + 1 < ntiles) copy(t + 1);
+    step(t, std::false_type{});
+  }
+  for (int t = nfull; t < ntiles; ++t) {
+    tile_barrier();
+    if (t + 1 < ntiles) copy(t + 1);
+    if (t * kTileKeys < wlast) step(t, std::true_type{});  // (a wave that is done still copies and waits)
+  }
+  l += __shfl_xor(l, 32);
+  if (row >= s.nq) return;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const size_t at = (size_t)(s.q0 + row) * p.o_stride + (size_t)h * DV + 4 * hf;
+  auto store = [&](auto put) {
+#pragma unroll
+    for (int i = 0; i < DV / 32; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        put(32 * i + 8 * r, f32x4{o[i][4 * r], o[i][4 * r + 1], o[i][4 * r + 2], o[i][4 * r + 3]} * inv);
+  };
+  if (p.o_f32) {
+    store([&](int e, f32x4 y) { *reinterpret_cast<f32x4*>(static_cast<float*>(p.o) + at + e) = y; });
+  } else {
+    store([&](int e, f32x4 y) {
+      *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(p.o) + at + e) = bf16x4{(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
+    });
+  }
+}
+
 template <int BM>
 unsigned tiles_of(const AttnParams& p) {
   return p.cu_q ? (unsigned)(p.total_q / BM + p.N) : (unsigned)((p.total_q / p.N + BM - 1) / BM * p.N);
+}
+
+template <int NW, int DK, int DV>
+hipError_t launch_fast(const AttnParams& p, hipStream_t s) {
+  const unsigned tiles = tiles_of<32 * NW>(p), chunk = (tiles * p.Hq + 7) / 8;
+  hipLaunchKernelGGL((kda_attn_kernel<NW, DK, DV>), dim3(8 * chunk), dim3(64 * NW), 0, s, p, (int)tiles, chunk);
+  return hipGetLastError();
 }
 
 template <typename IO, int DK, int DV>
@@ -215,6 +438,10 @@ hipError_t pick_dk(const AttnParams& p, hipStream_t s) {
 
 hipError_t launch_attn_fwd(const AttnParams& p, int io_dtype, hipStream_t s) {
   if (p.total_q < 1 || p.N < 1) return hipErrorInvalidValue;
+  if (io_dtype == 1 && p.dk % 64 == 0 && p.dv % 64 == 0) {
+    if (p.dk == 128) return p.dv == 128 ? launch_fast<4, 128, 128>(p, s) : launch_fast<4, 128, 64>(p, s);
+    return p.dv == 128 ? launch_fast<4, 64, 128>(p, s) : launch_fast<4, 64, 64>(p, s);
+  }
   return io_dtype == 1 ? pick_dk<__bf16>(p, s) : pick_dk<float>(p, s);
 }
 
