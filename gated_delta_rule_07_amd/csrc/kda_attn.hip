@@ -189,10 +189,12 @@ __global__ __launch_bounds__(256) void kda_attn_plain_kernel(AttnParams p) {
 // read fall on different banks.
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef const __attribute__((address_space(1))) void global_void;
 
 constexpr int kTileKeys = 64;
+constexpr float kSlack = 8.0f;
 
 // 16 bytes a lane from `src` to dst + 16 lane (dst the same for the wave).  Written out because the
 // compiler, which cannot tell the buffer that is filled from the one that is read, would wait for every copy
@@ -201,8 +203,21 @@ __device__ __forceinline__ void copy16(const char* src, char* dst) {
   const uint32_t at = (uint32_t)(uintptr_t)(lds_void*)dst;
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory", "m0");
 }
+// The same from base + off.
+__device__ __forceinline__ void copy16(const char* base, uint32_t off, char* dst) {
+  const uint32_t at = (uint32_t)(uintptr_t)(lds_void*)dst;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory", "m0");
+}
 // Every wave's copies have landed, and its reads of the other buffer are done.
 __device__ __forceinline__ void tile_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// The larger of the two halves' values.
+__device__ __forceinline__ float half_max(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto y = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t lo = y[0], hi = y[1];  // (a bit cast of y[1] itself gives y[0])
+  return fmaxf(__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi));
+}
 
 // Where the 16-byte piece c of row r lies in its row.
 template <int D>
@@ -244,40 +259,68 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int 
     const __bf16* x = static_cast<const __bf16*>(p.q) + (size_t)(s.q0 + min(row, s.nq - 1)) * p.q_stride + (size_t)h * DK + 8 * hf;
 #pragma unroll
     for (int st = 0; st < DK / 16; ++st) q[st] = *reinterpret_cast<const bf16x8*>(x + 16 * st);
+    if (p.scale < 0.0f) {  // (so that the largest score has the largest product)
+#pragma unroll
+      for (int st = 0; st < DK / 16; ++st) q[st] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, q[st]) ^ 0x80008000u);
+    }
     // (waited for here: a wait at their use, inside the loop, would wait for the tiles' copies too)
 #pragma unroll
     for (int st = 0; st < DK / 16; ++st) asm volatile("" : "+v"(q[st]));
   }
   const char* kg = reinterpret_cast<const char*>(static_cast<const __bf16*>(p.k) + (size_t)s.k0 * p.k_stride + (size_t)hk * DK);
   const char* vg = reinterpret_cast<const char*>(static_cast<const __bf16*>(p.v) + (size_t)s.k0 * p.v_stride + (size_t)hk * DV);
-  auto copy = [&](int t) {
-    char* kl = lds + (t & 1) * (C::KB + C::VB);
+  // this lane's pieces of a tile: row and offset within the tile's rows
+  const uint32_t krow = (uint32_t)(2 * p.k_stride), vrow = (uint32_t)(2 * p.v_stride);  // (bytes; the launch sees to it that a tile's fit)
+  uint32_t koff[C::NK], voff[C::NV];
+#pragma unroll
+  for (int i = 0; i < C::NK; ++i) {
+    const int e = (wave * C::NK + i) * 64 + lane, r = e / (DK / 8);
+    koff[i] = r * krow + 16 * key_piece<DK>(r, e % (DK / 8));
+  }
+#pragma unroll
+  for (int i = 0; i < C::NV; ++i) {
+    const int e = (wave * C::NV + i) * 64 + lane, r = e / (DV / 8);
+    voff[i] = r * vrow + 16 * value_piece<DV>(r, e % (DV / 8));
+  }
+  auto copy = [&](int t, auto buf) {
+    char* kl = lds + buf * (C::KB + C::VB);
     char* vl = kl + C::KB;
+    const char* kt = kg + (size_t)t * kTileKeys * krow;
+    const char* vt = vg + (size_t)t * kTileKeys * vrow;
+    if ((t + 1) * kTileKeys <= s.nk) {
 #pragma unroll
-    for (int i = 0; i < C::NK; ++i) {
-      const int e = (wave * C::NK + i) * 64 + lane, r = e / (DK / 8), cc = key_piece<DK>(r, e % (DK / 8));
-      const char* src = kg + (size_t)min(t * kTileKeys + r, s.nk - 1) * (2 * p.k_stride) + 16 * cc;
-      copy16(src, kl + (wave * C::NK + i) * 1024);
-    }
+      for (int i = 0; i < C::NK; ++i) copy16(kt, koff[i], kl + (wave * C::NK + i) * 1024);
 #pragma unroll
-    for (int i = 0; i < C::NV; ++i) {
-      const int e = (wave * C::NV + i) * 64 + lane, r = e / (DV / 8), cc = value_piece<DV>(r, e % (DV / 8));
-      const char* src = vg + (size_t)min(t * kTileKeys + r, s.nk - 1) * (2 * p.v_stride) + 16 * cc;
-      copy16(src, vl + (wave * C::NV + i) * 1024);
+      for (int i = 0; i < C::NV; ++i) copy16(vt, voff[i], vl + (wave * C::NV + i) * 1024);
+    } else {  // rows behind the last key: that one again (nobody sees them)
+      const int most = s.nk - 1 - t * kTileKeys;
+#pragma unroll
+      for (int i = 0; i < C::NK; ++i) {
+        const int r = ((wave * C::NK + i) * 64 + lane) / (DK / 8);
+        copy16(kt, koff[i] - max(r - most, 0) * krow, kl + (wave * C::NK + i) * 1024);
+      }
+#pragma unroll
+      for (int i = 0; i < C::NV; ++i) {
+        const int r = ((wave * C::NV + i) * 64 + lane) / (DV / 8);
+        copy16(vt, voff[i] - max(r - most, 0) * vrow, vl + (wave * C::NV + i) * 1024);
+      }
     }
   };
 
-  const float scale = p.scale * kLog2e;
+  const float scale = __builtin_fabsf(p.scale) * kLog2e;
   f32x16 o[DV / 32];
 #pragma unroll
   for (int t = 0; t < DV / 32; ++t) o[t] = (f32x16)0.0f;
   float m = -__builtin_inff(), l = 0.0f;
-  if (ntiles > 0) copy(0);
+  const bf16x2 ones = {(__bf16)1.0f, (__bf16)1.0f};
+  using B0 = std::integral_constant<int, 0>;
+  using B1 = std::integral_constant<int, 1>;
+  if (ntiles > 0) copy(0, B0{});
   // One tile.  EDGE: some of the wave's queries do not see all of it.
-  auto step = [&](int t, auto edge) {
+  auto step = [&](int t, auto buf, auto edge) {
     constexpr bool EDGE = decltype(edge)::value;
     const int k0 = t * kTileKeys;
-    const char* kl = lds + (t & 1) * (C::KB + C::VB);
+    const char* kl = lds + buf * (C::KB + C::VB);
     const char* vl = kl + C::KB;
     f32x16 x[2];
 #pragma unroll
@@ -290,17 +333,19 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int 
         x[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[st], x[u], 0, 0, 0);
       }
     }
+    // the maximum of the raw products; it is taken over only when it has grown by 8 in log2, so that outputs
+    // are rarely rescaled: powers stay below 2^8, and with them what fp32 sums and bf16 can tell apart
     float top = -__builtin_inff();
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        x[u][r] *= scale;  // (before the maximum: a scale below 0 turns the order round)
         if constexpr (EDGE) x[u][r] = k0 + 32 * u + 8 * (r / 4) + 4 * hf + r % 4 >= limit ? -__builtin_inff() : x[u][r];
         top = fmaxf(top, x[u][r]);
       }
-    top = fmaxf(top, __shfl_xor(top, 32));
-    if (__any(top > m)) {
+    top = half_max(top);
+    top = top == -__builtin_inff() ? top : top * scale;  // (a scale of 0 would make NaN of it)
+    if (__any(top > m + kSlack)) {
       const float now = fmaxf(m, top);
       const float keep = now == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - now);
       m = now;
@@ -308,16 +353,21 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int 
 #pragma unroll
       for (int i = 0; i < DV / 32; ++i) o[i] *= keep;
     }
-    const float base = m == -__builtin_inff() ? 0.0f : m;
+    const float base = m == -__builtin_inff() ? 0.0f : -m;
     bf16x8 pt[4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int st = 0; st < 4; ++st) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const float y = __builtin_amdgcn_exp2f(x[u][r] - base);
-        l += y;
-        pt[2 * u + r / 8][r % 8] = (__bf16)y;
+      for (int e = 0; e < 8; ++e) {
+        const float y = x[st / 2][8 * (st % 2) + e];
+        float z = __builtin_amdgcn_exp2f(__builtin_fmaf(y, scale, base));
+        if constexpr (EDGE) z = y == -__builtin_inff() ? 0.0f : z;
+        pt[st][e] = (__bf16)z;
       }
+      // the sum of what the product with V takes: the rounded probabilities, two at a time
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{pt[st][e], pt[st][e + 1]}, ones, l, false);
+    }
     // V^T operand of channels [32 i, 32 i + 32), keys [16 st, 16 st + 16): slot e of half hf is key 8 (e / 4) + 4 hf + e % 4
     auto values = [&](int i, int st) {
       typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -364,15 +414,19 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int 
       for (int i = 0; i < DV / 32; ++i) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values(i, st), pt[st], o[i], 0, 0, 0);
   };
   const int nfull = max(min((s.r0 + shift + 1) / kTileKeys, ntiles), 0);  // tiles that every query of the workgroup sees whole
-  for (int t = 0; t < nfull; ++t) {
+  int t = 0;
+  for (; t + 2 <= nfull; t += 2) {  // (two at a time: the buffers' addresses are constants)
     tile_barrier();
-    if (t + 1 < ntiles) copy(t + 1);
-    step(t, std::false_type{});
+    copy(t + 1, B1{});
+    step(t, B0{}, std::false_type{});
+    tile_barrier();
+    if (t + 2 < ntiles) copy(t + 2, B0{});
+    step(t + 1, B1{}, std::false_type{});
   }
-  for (int t = nfull; t < ntiles; ++t) {
+  for (; t < ntiles; ++t) {
     tile_barrier();
-    if (t + 1 < ntiles) copy(t + 1);
-    if (t * kTileKeys < wlast) step(t, std::true_type{});  // (a wave that is done still copies and waits)
+    if (t + 1 < ntiles) copy(t + 1, (t + 1) & 1);
+    if (t * kTileKeys < wlast) step(t, t & 1, std::true_type{});  // (a wave that is done still copies and waits)
   }
   l += __shfl_xor(l, 32);
   if (row >= s.nq) return;
@@ -438,7 +492,8 @@ hipError_t pick_dk(const AttnParams& p, hipStream_t s) {
 
 hipError_t launch_attn_fwd(const AttnParams& p, int io_dtype, hipStream_t s) {
   if (p.total_q < 1 || p.N < 1) return hipErrorInvalidValue;
-  if (io_dtype == 1 && p.dk % 64 == 0 && p.dv % 64 == 0) {
+  // (64 rows of keys or values have to lie within 2^31 bytes)
+  if (io_dtype == 1 && p.dk % 64 == 0 && p.dv % 64 == 0 && std::max(p.k_stride, p.v_stride) < (1LL << 24)) {
     if (p.dk == 128) return p.dv == 128 ? launch_fast<4, 128, 128>(p, s) : launch_fast<4, 128, 64>(p, s);
     return p.dv == 128 ? launch_fast<4, 64, 128>(p, s) : launch_fast<4, 64, 64>(p, s);
   }
