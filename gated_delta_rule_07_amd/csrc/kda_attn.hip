@@ -29,7 +29,7 @@ __device__ __forceinline__ bool part_of(const AttnParams& p, int tile, Part& s) 
   int b, j;
   if (p.cu_q) {
     auto first = [&](int i) { return (long long)(clamp_to(p.cu_q[i], p.total_q) / BM) + i; };
-    b = last_at_most(p.N, tile, first);
+    b = last_at_most_wave(p.N, tile, first);
     j = tile - (int)first(b);
     s.q0 = clamp_to(p.cu_q[b], p.total_q);
     s.nq = clamp_to(p.cu_q[b + 1], p.total_q) - s.q0;
@@ -254,19 +254,6 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int 
   const int wlast = min(min(s.r0 + 32 * wave + 32, s.nq) + shift, last);  // of the wave
   const int ntiles = (last + kTileKeys - 1) / kTileKeys;
 
-  bf16x8 q[DK / 16];
-  {
-    const __bf16* x = static_cast<const __bf16*>(p.q) + (size_t)(s.q0 + min(row, s.nq - 1)) * p.q_stride + (size_t)h * DK + 8 * hf;
-#pragma unroll
-    for (int st = 0; st < DK / 16; ++st) q[st] = *reinterpret_cast<const bf16x8*>(x + 16 * st);
-    if (p.scale < 0.0f) {  // (so that the largest score has the largest product)
-#pragma unroll
-      for (int st = 0; st < DK / 16; ++st) q[st] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, q[st]) ^ 0x80008000u);
-    }
-    // (waited for here: a wait at their use, inside the loop, would wait for the tiles' copies too)
-#pragma unroll
-    for (int st = 0; st < DK / 16; ++st) asm volatile("" : "+v"(q[st]));
-  }
   const char* kg = reinterpret_cast<const char*>(static_cast<const __bf16*>(p.k) + (size_t)s.k0 * p.k_stride + (size_t)hk * DK);
   const char* vg = reinterpret_cast<const char*>(static_cast<const __bf16*>(p.v) + (size_t)s.k0 * p.v_stride + (size_t)hk * DV);
   // this lane's pieces of a tile: row and offset within the tile's rows
@@ -307,15 +294,28 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int 
     }
   };
 
+  using B0 = std::integral_constant<int, 0>;
+  using B1 = std::integral_constant<int, 1>;
+  if (ntiles > 0) copy(0, B0{});
+  bf16x8 q[DK / 16];
+  {
+    const __bf16* x = static_cast<const __bf16*>(p.q) + (size_t)(s.q0 + min(row, s.nq - 1)) * p.q_stride + (size_t)h * DK + 8 * hf;
+#pragma unroll
+    for (int st = 0; st < DK / 16; ++st) q[st] = *reinterpret_cast<const bf16x8*>(x + 16 * st);
+    if (p.scale < 0.0f) {  // (so that the largest score has the largest product)
+#pragma unroll
+      for (int st = 0; st < DK / 16; ++st) q[st] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, q[st]) ^ 0x80008000u);
+    }
+    // (waited for here: a wait at their use, inside the loop, would wait for the tiles' copies too)
+#pragma unroll
+    for (int st = 0; st < DK / 16; ++st) asm volatile("" : "+v"(q[st]));
+  }
   const float scale = __builtin_fabsf(p.scale) * kLog2e;
   f32x16 o[DV / 32];
 #pragma unroll
   for (int t = 0; t < DV / 32; ++t) o[t] = (f32x16)0.0f;
   float m = -__builtin_inff(), l = 0.0f;
   const bf16x2 ones = {(__bf16)1.0f, (__bf16)1.0f};
-  using B0 = std::integral_constant<int, 0>;
-  using B1 = std::integral_constant<int, 1>;
-  if (ntiles > 0) copy(0, B0{});
   // One tile.  EDGE: some of the wave's queries do not see all of it.
   auto step = [&](int t, auto buf, auto edge) {
     constexpr bool EDGE = decltype(edge)::value;
@@ -431,20 +431,26 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int 
   l += __shfl_xor(l, 32);
   if (row >= s.nq) return;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const size_t at = (size_t)(s.q0 + row) * p.o_stride + (size_t)h * DV + 4 * hf;
-  auto store = [&](auto put) {
+  char* out = static_cast<char*>(p.o) + ((size_t)(s.q0 + row) * p.o_stride + (size_t)h * DV) * (p.o_f32 ? 4 : 2);
 #pragma unroll
-    for (int i = 0; i < DV / 32; ++i)
+  for (int i = 0; i < DV / 32; ++i) {
+    o[i] *= inv;
+    if (p.o_f32) {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        put(32 * i + 8 * r, f32x4{o[i][4 * r], o[i][4 * r + 1], o[i][4 * r + 2], o[i][4 * r + 3]} * inv);
-  };
-  if (p.o_f32) {
-    store([&](int e, f32x4 y) { *reinterpret_cast<f32x4*>(static_cast<float*>(p.o) + at + e) = y; });
-  } else {
-    store([&](int e, f32x4 y) {
-      *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(p.o) + at + e) = bf16x4{(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
-    });
+        *reinterpret_cast<f32x4*>(out + 4 * (32 * i + 8 * r + 4 * hf)) = f32x4{o[i][4 * r], o[i][4 * r + 1], o[i][4 * r + 2], o[i][4 * r + 3]};
+    } else {
+      // halves exchange fours, so that each writes 8 neighbours: 16 bytes
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t a[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          a[e] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)o[i][8 * j + 2 * e], (__bf16)o[i][8 * j + 2 * e + 1]});
+        const auto x = __builtin_amdgcn_permlane32_swap(a[0], a[2], false, false), y = __builtin_amdgcn_permlane32_swap(a[1], a[3], false, false);
+        *reinterpret_cast<u32x4*>(out + 2 * (32 * i + 16 * j + 8 * hf)) = u32x4{x[0], y[0], x[1], y[1]};
+      }
+    }
   }
 }
 

@@ -66,6 +66,21 @@ __device__ __forceinline__ int last_at_most(int n, long long x, F at) {
   return lo;
 }
 
+// The same, by all 64 lanes of a wave together: 64 places at a time, so that up to 64 take one load.
+template <typename F>
+__device__ __forceinline__ int last_at_most_wave(int n, long long x, F at) {
+  int lo = 0, hi = n;
+  const int lane = threadIdx.x % 64;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 63) / 64;
+    const long long i = lo + (long long)lane * step;
+    const int below = __popcll(__ballot(lane == 0 || (i < hi && at((int)i) <= x)));
+    lo = min(lo + (below - 1) * step, hi - 1);  // (in range whatever the list holds)
+    hi = min(lo + step, hi);
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
 __device__ __forceinline__ int clamp_to(int x, int hi) { return min(max(x, 0), hi); }
 
 }  // namespace kda
