@@ -208,6 +208,8 @@ __device__ __forceinline__ void copy16(const char* base, uint32_t off, char* dst
   const uint32_t at = (uint32_t)(uintptr_t)(lds_void*)dst;
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory", "m0");
 }
+// Every wave's LDS writes are there.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 // Every wave's copies have landed, and its reads of the other buffer are done.
 __device__ __forceinline__ void tile_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
@@ -239,6 +241,8 @@ template <int NW, int DK, int DV>
 __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int tiles, unsigned chunk) {
   using C = FastCfg<NW, DK, DV>;
   __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
+  __shared__ unsigned char bad[C::VB / 16];  // a bit for each value of a tile that is not finite
+  __shared__ int some[NW];
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), c = lane % 32, hf = lane / 32;
   const int G = p.Hq / p.Hk;
   // Workgroups go to the 8 dies in turn: each die takes a run of neighbours, which share keys and values in its L2.
@@ -251,7 +255,9 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int 
   const int shift = s.nk - s.nq;
   const int limit = row < s.nq ? row + shift + 1 : 0;
   const int last = min(s.r0 + C::BM, s.nq) + shift;                       // keys of the workgroup
-  const int wlast = min(min(s.r0 + 32 * wave + 32, s.nq) + shift, last);  // of the wave
+  const bool live = s.r0 + 32 * wave < s.nq;                               // whether the wave has queries
+  const int wlast = live ? min(s.r0 + 32 * wave + 32, s.nq) + shift : 0;   // its keys
+  const int wfirst = s.r0 + 32 * wave + shift + 1;                        // its first query's
   const int ntiles = (last + kTileKeys - 1) / kTileKeys;
 
   const char* kg = reinterpret_cast<const char*>(static_cast<const __bf16*>(p.k) + (size_t)s.k0 * p.k_stride + (size_t)hk * DK);
@@ -310,18 +316,47 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int 
 #pragma unroll
     for (int st = 0; st < DK / 16; ++st) asm volatile("" : "+v"(q[st]));
   }
-  const float scale = __builtin_fabsf(p.scale) * kLog2e;
+  // (not 0, which would make NaN of masked scores: 1e-30 of any product is as little)
+  const float scale = fmaxf(__builtin_fabsf(p.scale) * kLog2e, 1e-30f);
   f32x16 o[DV / 32];
 #pragma unroll
   for (int t = 0; t < DV / 32; ++t) o[t] = (f32x16)0.0f;
   float m = -__builtin_inff(), l = 0.0f;
   const bf16x2 ones = {(__bf16)1.0f, (__bf16)1.0f};
-  // One tile.  EDGE: some of the wave's queries do not see all of it.
-  auto step = [&](int t, auto buf, auto edge) {
-    constexpr bool EDGE = decltype(edge)::value;
+  const int nfull = max(min((s.r0 + shift + 1) / kTileKeys, ntiles), 0);  // tiles that every query of the workgroup sees whole
+  auto tile = [&](int t, auto buf) {
+    tile_barrier();
+    if (t + 1 < ntiles) copy(t + 1, std::integral_constant<int, 1 - decltype(buf)::value>{});
     const int k0 = t * kTileKeys;
     const char* kl = lds + buf * (C::KB + C::VB);
-    const char* vl = kl + C::KB;
+    char* vl = lds + buf * (C::KB + C::VB) + C::KB;
+    bool odd = false;
+    if (t >= nfull) {
+      // Some queries do not see all of the tile: values that are not finite must not reach them as 0 v.  They are taken
+      // out, and noted, a bit each.
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < C::NV; ++i) {
+        const int e = (wave * C::NV + i) * 64 + lane;
+        u32x4 y = *reinterpret_cast<const u32x4*>(vl + 16 * e);
+        uint32_t bits = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool lo = (y[j] & 0x7f80u) == 0x7f80u, hi = (y[j] & 0x7f800000u) == 0x7f800000u;
+          bits |= (uint32_t)lo << 2 * j | (uint32_t)hi << 2 * j + 1;
+          y[j] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
+        }
+        bad[e] = (unsigned char)bits;
+        if (bits) *reinterpret_cast<u32x4*>(vl + 16 * e) = y;
+        found = found || bits;
+      }
+      const bool any = __any(found);
+      if (lane == 0) some[wave] = any;
+      lds_barrier();
+#pragma unroll
+      for (int w = 0; w < NW; ++w) odd = odd || some[w];
+    }
+    if (k0 >= wlast) return;  // (a wave that is done still copies and waits)
     f32x16 x[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -333,18 +368,21 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int 
         x[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[st], x[u], 0, 0, 0);
       }
     }
+    const int rel = limit - k0 - 4 * hf;  // the query's keys in the tile, from this half's first on
+    if (wfirst < k0 + kTileKeys) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[u][r] = 32 * u + 8 * (r / 4) + r % 4 >= rel ? -__builtin_inff() : x[u][r];
+    }
     // the maximum of the raw products; it is taken over only when it has grown by 8 in log2, so that outputs
     // are rarely rescaled: powers stay below 2^8, and with them what fp32 sums and bf16 can tell apart
     float top = -__builtin_inff();
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        if constexpr (EDGE) x[u][r] = k0 + 32 * u + 8 * (r / 4) + 4 * hf + r % 4 >= limit ? -__builtin_inff() : x[u][r];
-        top = fmaxf(top, x[u][r]);
-      }
-    top = half_max(top);
-    top = top == -__builtin_inff() ? top : top * scale;  // (a scale of 0 would make NaN of it)
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, x[u][r]);
+    top = half_max(top) * scale;
     if (__any(top > m + kSlack)) {
       const float now = fmaxf(m, top);
       const float keep = now == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - now);
@@ -358,75 +396,52 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int 
 #pragma unroll
     for (int st = 0; st < 4; ++st) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float y = x[st / 2][8 * (st % 2) + e];
-        float z = __builtin_amdgcn_exp2f(__builtin_fmaf(y, scale, base));
-        if constexpr (EDGE) z = y == -__builtin_inff() ? 0.0f : z;
-        pt[st][e] = (__bf16)z;
-      }
+      for (int e = 0; e < 8; ++e) pt[st][e] = (__bf16)__builtin_amdgcn_exp2f(__builtin_fmaf(x[st / 2][8 * (st % 2) + e], scale, base));
       // the sum of what the product with V takes: the rounded probabilities, two at a time
 #pragma unroll
       for (int e = 0; e < 8; e += 2) l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{pt[st][e], pt[st][e + 1]}, ones, l, false);
     }
     // V^T operand of channels [32 i, 32 i + 32), keys [16 st, 16 st + 16): slot e of half hf is key 8 (e / 4) + 4 hf + e % 4
-    auto values = [&](int i, int st) {
-      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-      s16x4 y[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = 16 * st + 8 * j + 4 * hf + lane % 16 / 4;
-        const int cc = 4 * i + 2 * (lane / 16 % 2) + lane % 4 / 2;
-        y[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vl + r * (2 * DV) + 16 * value_piece<DV>(r, cc) + 8 * (lane % 2)));
-      }
-      typedef short s16x8 __attribute__((ext_vector_type(8)));
-      return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(y[0], y[1], 0, 1, 2, 3, 4, 5, 6, 7));
-    };
-    if constexpr (EDGE) {  // values that are not finite must not reach, as 0 v, queries that do not see them
-      bool odd = false;
-      for (int i = lane; i < C::VB / 16; i += 64) {
-        const u32x4 y = *reinterpret_cast<const u32x4*>(vl + 16 * i);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) odd = odd || (y[e] & 0x7f80u) == 0x7f80u || (y[e] & 0x7f800000u) == 0x7f800000u;
-      }
-      if (__builtin_expect(__any(odd), 0)) {
-        for (int r = 0; r < 32; ++r) {  // one query at a time, with the values that it sees
-          const int lim = __shfl(limit, r);
-#pragma unroll
-          for (int i = 0; i < DV / 32; ++i) {
-            f32x16 y = (f32x16)0.0f;
-#pragma unroll
-            for (int st = 0; st < 4; ++st) {
-              bf16x8 a = values(i, st);
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (k0 + 16 * st + 8 * (e / 4) + 4 * hf + e % 4 >= lim) a[e] = (__bf16)0.0f;
-              y = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, pt[st], y, 0, 0, 0);
-            }
-            if (c == r) o[i] += y;
-          }
-        }
-        return;
-      }
-    }
 #pragma unroll
     for (int st = 0; st < 4; ++st)
 #pragma unroll
-      for (int i = 0; i < DV / 32; ++i) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values(i, st), pt[st], o[i], 0, 0, 0);
+      for (int i = 0; i < DV / 32; ++i) {
+        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        s16x4 y[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int r = 16 * st + 8 * j + 4 * hf + lane % 16 / 4;
+          const int cc = 4 * i + 2 * (lane / 16 % 2) + lane % 4 / 2;
+          y[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vl + r * (2 * DV) + 16 * value_piece<DV>(r, cc) + 8 * (lane % 2)));
+        }
+        const bf16x8 a = __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(y[0], y[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, pt[st], o[i], 0, 0, 0);
+      }
+    if (__builtin_expect(odd, 0)) {  // outputs of queries that see a value that is not finite: NaN.  The values are counted by a product.
+#pragma unroll
+      for (int i = 0; i < DV / 32; ++i) {
+        f32x16 y = (f32x16)0.0f;
+#pragma unroll 1
+        for (int st = 0; st < 4; ++st) {
+          bf16x8 n, see;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int r = 16 * st + 8 * (e / 4) + 4 * hf + e % 4;
+            const unsigned bits = bad[r * (DV / 8) + value_piece<DV>(r, 4 * i + c / 8)];
+            n[e] = (__bf16)(float)(bits >> c % 8 & 1);
+            see[e] = (__bf16)(k0 + r < limit ? 1.0f : 0.0f);
+          }
+          y = __builtin_amdgcn_mfma_f32_32x32x16_bf16(n, see, y, 0, 0, 0);
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[i][r] = y[r] > 0.0f ? __builtin_nanf("") : o[i][r];
+      }
+    }
   };
-  const int nfull = max(min((s.r0 + shift + 1) / kTileKeys, ntiles), 0);  // tiles that every query of the workgroup sees whole
-  int t = 0;
-  for (; t + 2 <= nfull; t += 2) {  // (two at a time: the buffers' addresses are constants)
-    tile_barrier();
-    copy(t + 1, B1{});
-    step(t, B0{}, std::false_type{});
-    tile_barrier();
-    if (t + 2 < ntiles) copy(t + 2, B0{});
-    step(t + 1, B1{}, std::false_type{});
-  }
-  for (; t < ntiles; ++t) {
-    tile_barrier();
-    if (t + 1 < ntiles) copy(t + 1, (t + 1) & 1);
-    if (t * kTileKeys < wlast) step(t, t & 1, std::true_type{});  // (a wave that is done still copies and waits)
+  for (int t = 0; t < ntiles; t += 2) {  // (two at a time: the buffers' addresses are constants)
+    tile(t, B0{});
+    if (t + 1 < ntiles) tile(t + 1, B1{});
   }
   l += __shfl_xor(l, 32);
   if (row >= s.nq) return;
