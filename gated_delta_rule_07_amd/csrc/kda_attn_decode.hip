@@ -25,6 +25,7 @@ constexpr int kTile = 32, kGranule = kTile * kWaves;
 constexpr int kWorkers = 512;     // workgroups that share the granules
 constexpr int kLeastRun = 2;      // granules a workgroup takes at least
 constexpr int kWholeUnits = 2048; // up to this many tokens a sequence, a workgroup takes a unit whole
+constexpr float kSlack = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -50,6 +51,20 @@ __device__ __forceinline__ uint32_t bf16_of_e4m3(uint32_t w, bool hi) {
                                          : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
 }
 
+// All ones in the bytes (e4m3) or halves (bf16) of w that are not finite.
+template <bool E4>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  uint32_t r = 0;
+  if constexpr (E4) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) r |= (w >> 8 * b & 0x7fu) == 0x7fu ? 0xffu << 8 * b : 0u;
+  } else {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) r |= (w >> 16 * b & 0x7f80u) == 0x7f80u ? 0xffffu << 16 * b : 0u;
+  }
+  return r;
+}
+
 // Tokens that rows of sequence b attend to, and its granules (0: no row of the table, nothing is written).
 __device__ __forceinline__ int tokens_of(const AttnDecodeParams& p, int b) {
   return min(max(p.lens[b], 0), p.c.width * p.c.page_tokens);
@@ -68,14 +83,26 @@ struct Tile {
   u32x4 k[2][NK];
   uint32_t v[8][VW];
   float ks[2], vs[2];
-  int page[2];
+  bool there[2];  // whether its halves have pages
 };
 
+// The largest of a column's values (in lanes 16 apart).
+__device__ __forceinline__ float column_max(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto y = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t a = y[0], b = y[1];  // (a bit cast of y[1] itself gives y[0])
+  const float z = fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+  const uint32_t w = __builtin_bit_cast(uint32_t, z);
+  const auto t = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+  const uint32_t c = t[0], d = t[1];
+  return fmaxf(__builtin_bit_cast(float, c), __builtin_bit_cast(float, d));
+}
+
 template <int NT, bool E4, int DK, int DV>
-__global__ __launch_bounds__(kThreads) void kda_attn_decode_kernel(DecodePlan a) {
+__global__ __launch_bounds__(kThreads, 2) void kda_attn_decode_kernel(DecodePlan a) {
   using T = Tile<E4, DK, DV>;
   constexpr int NM = DV / 16, NS = DK / 32;
-  constexpr int ES = E4 ? 1 : 2;
+  constexpr int ES = E4 ? 1 : 2, CW = 4 / ES;  // bytes of an element, elements of a dword
   __shared__ __attribute__((aligned(16))) float so[kWaves][kAttnColumns][DV + 4];
   __shared__ float sm[kWaves][kAttnColumns], sl[kWaves][kAttnColumns];
   __shared__ int swave[kWaves];
@@ -83,7 +110,8 @@ __global__ __launch_bounds__(kThreads) void kda_attn_decode_kernel(DecodePlan a)
   const AttnDecodeParams& p = a.p;
   const KvCache& cache = p.c;
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), col = lane % 16, g = lane / 16;
-  const int H = cache.H, units = a.CT * H, pt = cache.page_tokens;
+  const int H = cache.H, units = a.CT * H, pt = cache.page_tokens, lg = 31 - __builtin_clz(pt);
+  const float scale = p.scale * kLog2e;
 
   long long at, end, mine;  // this workgroup's granules; where its run begins
   const bool whole = a.workers == 0;
@@ -171,40 +199,59 @@ __global__ __launch_bounds__(kThreads) void kda_attn_decode_kernel(DecodePlan a)
     for (int t = 0; t < NM; ++t) o[t] = (f32x4)0.0f;
     float m = -__builtin_inff(), l = 0.0f;
 
-    auto load = [&](int k0) {
+    // Offsets of a lane within a half tile's keys and values; the rest of an address is the wave's.
+    const uint32_t koff = (uint32_t)(col * DK * ES + 16 * g), voff = (uint32_t)(4 * g * DV * ES + col * T::VW * 4);
+    const size_t kat = kv_keys(cache, h), vat = kv_values(cache, h), sat = kv_scales(cache);
+    const int kend = min(g1 * kGranule, len);
+    // The pages of a tile's halves, -1 where there is none (behind the sequence a row may name any page).
+    struct Pages {
+      int p[2];
+    };
+    auto pages_of = [&](int k0) {
+      Pages r;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int page = k0 + 16 * u < kend ? pages[(k0 + 16 * u) >> lg] : -1;
+        r.p[u] = page < cache.n_pages ? page : -1;
+      }
+      return r;
+    };
+    auto load = [&](int k0, const Pages& pg) {
       T t;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int idx = (k0 + 16 * u) / pt, slot = (k0 + 16 * u) % pt;
-        int page = k0 + 16 * u < len ? pages[idx] : -1;  // (behind the sequence a row may name any page)
-        if (page < 0 || page >= cache.n_pages) page = -1;
-        t.page[u] = page;
-        const char* base = cache.pool + (size_t)max(page, 0) * cache.page_bytes;
-        const char* kp = base + kv_keys(cache, h) + ((size_t)(slot + col) * DK) * ES + 16 * g;
+        const int slot = (k0 + 16 * u) & (pt - 1);
+        t.there[u] = pg.p[u] >= 0;
+        const char* base = cache.pool + (size_t)max(pg.p[u], 0) * cache.page_bytes;
+        const char* kp = base + kat + (uint32_t)(slot * DK * ES);
+        const char* vp = base + vat + (uint32_t)(slot * DV * ES);
 #pragma unroll
-        for (int i = 0; i < T::NK; ++i) t.k[u][i] = *reinterpret_cast<const u32x4*>(kp + 64 * i);
-        const char* vp = base + kv_values(cache, h) + ((size_t)(slot + 4 * g) * DV) * ES + col * T::VW * 4;
+        for (int i = 0; i < T::NK; ++i) t.k[u][i] = *reinterpret_cast<const u32x4*>(kp + (koff + 64 * i));
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 4; ++r) {
+          const char* x = vp + (voff + r * DV * ES);
+          if constexpr (T::VW == 1) {
+            t.v[4 * u + r][0] = *reinterpret_cast<const uint32_t*>(x);
+          } else if constexpr (T::VW == 2) {
+            const u32x2 y = *reinterpret_cast<const u32x2*>(x);
+            t.v[4 * u + r][0] = y[0], t.v[4 * u + r][1] = y[1];
+          } else {
+            const u32x4 y = *reinterpret_cast<const u32x4*>(x);
 #pragma unroll
-          for (int i = 0; i < T::VW; ++i) t.v[4 * u + r][i] = *reinterpret_cast<const uint32_t*>(vp + (size_t)r * DV * ES + 4 * i);
+            for (int i = 0; i < 4; ++i) t.v[4 * u + r][i] = y[i];
+          }
+        }
         t.ks[u] = t.vs[u] = 1.0f;
         if constexpr (E4) {
-          const float* sc = reinterpret_cast<const float*>(base + kv_scales(cache));
-          t.ks[u] = page < 0 ? 1.0f : sc[h];
-          t.vs[u] = page < 0 ? 1.0f : sc[H + h];  // (0 times another page's scale could be NaN)
+          const float* sc = reinterpret_cast<const float*>(base + sat);
+          t.ks[u] = t.there[u] ? sc[h] : 1.0f;
+          t.vs[u] = t.there[u] ? sc[H + h] : 1.0f;  // (0 times another page's scale could be NaN)
         }
       }
       return t;
     };
 
-    const int kend = min(g1 * kGranule, len);
-    int k0 = g0 * kGranule + kTile * wave;
-    T cur;
-    if (k0 < kend) cur = load(k0);
-    for (; k0 < kend; k0 += kGranule) {
-      T nxt;
-      if (k0 + kGranule < kend) nxt = load(k0 + kGranule);
+    auto compute = [&](int k0, T& cur) {
       // scores of 32 keys
       f32x4 x[2] = {(f32x4)0.0f, (f32x4)0.0f};
 #pragma unroll
@@ -223,21 +270,25 @@ __global__ __launch_bounds__(kThreads) void kda_attn_decode_kernel(DecodePlan a)
             x[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), q[n3][st], x[u], 0, 0, 0);
         }
       }
-      const bool partial = k0 + kTile > least || cur.page[0] < 0 || cur.page[1] < 0;  // (the same for the wave)
-      float top = -__builtin_inff();
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float sc = cur.ks[u] * p.scale * kLog2e;
+      for (int u = 0; u < 2; ++u) x[u] *= cur.ks[u] * scale;
+      const bool partial = k0 + kTile > least || !cur.there[0] || !cur.there[1];  // (the same for the wave)
+      if (partial) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          x[u][r] *= sc;
-          if (partial && (cur.page[u] < 0 || k0 + 16 * u + 4 * g + r >= limit)) x[u][r] = -__builtin_inff();
-          top = fmaxf(top, x[u][r]);
-        }
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if (!cur.there[u] || k0 + 16 * u + 4 * g + r >= limit) x[u][r] = -__builtin_inff();
+            if (!cur.there[u] || k0 + 16 * u + 4 * g + r >= len) {  // what nobody sees may hold anything
+#pragma unroll
+              for (int i = 0; i < T::VW; ++i) cur.v[4 * u + r][i] = 0;
+            }
+          }
       }
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      if (__any(top > m)) {
+      float top = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])), fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
+      top = column_max(top);
+      // (taken over only when it has grown by 8 in log2: powers stay below 2^8, and outputs are rarely rescaled)
+      if (__any(top > m + kSlack)) {
         const float now = fmaxf(m, top);
         const float keep = now == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - now);
         m = now;
@@ -258,23 +309,11 @@ __global__ __launch_bounds__(kThreads) void kda_attn_decode_kernel(DecodePlan a)
           for (int n3 = 0; n3 < NT; ++n3) {
             const __bf16 t = (__bf16)z;
             pt8[n3][4 * u + r] = t;
-            z -= (float)t;
+            if (n3 + 1 < NT) z -= (float)t;
           }
         }
-      if (partial) {  // what nobody attends to may hold anything
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (cur.page[u] < 0 || k0 + 16 * u + 4 * g + r >= len)
-#pragma unroll
-              for (int i = 0; i < T::VW; ++i) cur.v[4 * u + r][i] = 0;
-      }
-      // V^T: 8 keys of channel NV col + t in a lane
-      bf16x8 vt[NM];
-#pragma unroll
-      for (int i = 0; i < T::VW; ++i) {
-        constexpr int CW = E4 ? 4 : 2;  // channels of a dword
+      // V^T: 8 keys of channel NV col + t in a lane, a dword of each key's channels at a time
+      auto values = [&](int i, bf16x8* vt) {
         u32x4 w[CW];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -291,40 +330,68 @@ __global__ __launch_bounds__(kThreads) void kda_attn_decode_kernel(DecodePlan a)
           }
         }
 #pragma unroll
-        for (int e = 0; e < CW; ++e) vt[CW * i + e] = __builtin_bit_cast(bf16x8, w[e]);
-      }
-      bool odd = false;
-      if (partial && p.K > 1) {  // values that are not finite must not reach, as 0 v, tokens that do not see them
+        for (int e = 0; e < CW; ++e) vt[e] = __builtin_bit_cast(bf16x8, w[e]);
+      };
+      if (partial && p.K > 1) {
+        // Values that are not finite must not reach, as 0 v, drafted tokens that do not see them: they are taken
+        // out, and counted for each token that does see them: its outputs become NaN.
+        bool odd = false;
 #pragma unroll
-        for (int t = 0; t < NM; ++t)
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) odd = odd || !(__builtin_fabsf((float)vt[t][e]) < __builtin_inff());
-      }
-      if (!__any(odd)) {
+          for (int i = 0; i < T::VW; ++i) odd = odd || not_finite<E4>(cur.v[j][i]) != 0;
+        if (__builtin_expect(__any(odd), 0)) {
+          bf16x8 see;
 #pragma unroll
-        for (int t = 0; t < NM; ++t)
+          for (int e = 0; e < 8; ++e) see[e] = (__bf16)(k0 + 16 * (e / 4) + 4 * g + e % 4 < limit ? 1.0f : 0.0f);
 #pragma unroll
-          for (int n3 = NT - 1; n3 >= 0; --n3)
-            o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt[t], pt8[n3], o[t], 0, 0, 0);
-      } else {
-        for (int k = 0; k < p.K; ++k) {  // one drafted token's keys at a time
-          const int lim = least + k;
+          for (int i = 0; i < T::VW; ++i) {
+            uint32_t keep[8];
 #pragma unroll
-          for (int t = 0; t < NM; ++t) {
-            bf16x8 w = vt[t];
+            for (int j = 0; j < 8; ++j) {  // their bits in place of the values
+              const uint32_t bad = not_finite<E4>(cur.v[j][i]);
+              keep[j] = cur.v[j][i] & ~bad;
+              cur.v[j][i] = bad & (E4 ? 0x38383838u : 0x3f803f80u);  // 1.0 where it is not finite
+            }
+            bf16x8 n[CW];
+            values(i, n);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (k0 + 16 * (e / 4) + 4 * g + e % 4 >= lim) w[e] = (__bf16)0.0f;
-            f32x4 y = (f32x4)0.0f;
+            for (int e = 0; e < CW; ++e) {
+              const f32x4 y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(n[e], see, (f32x4)0.0f, 0, 0, 0);
 #pragma unroll
-            for (int n3 = NT - 1; n3 >= 0; --n3) y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, pt8[n3], y, 0, 0, 0);
-            if (tok == k) o[t] += y;
+              for (int r = 0; r < 4; ++r) o[CW * i + e][r] = y[r] > 0.0f ? __builtin_nanf("") : o[CW * i + e][r];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) cur.v[j][i] = keep[j];
           }
         }
       }
-      cur = nxt;
+#pragma unroll
+      for (int i = 0; i < T::VW; ++i) {
+        bf16x8 vt[CW];
+        values(i, vt);
+#pragma unroll
+        for (int e = 0; e < CW; ++e)
+#pragma unroll
+          for (int n3 = NT - 1; n3 >= 0; --n3)
+            o[CW * i + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt[e], pt8[n3], o[CW * i + e], 0, 0, 0);
+      }
+    };
+    int k0 = g0 * kGranule + kTile * wave;
+    T ring[2];
+    Pages pg;
+    if (k0 + 0 * kGranule < kend) ring[0] = load(k0 + 0 * kGranule, pages_of(k0 + 0 * kGranule));
+    pg = pages_of(k0 + 1 * kGranule);
+    while (k0 < kend) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (k0 + 1 * kGranule < kend) ring[(i + 1) % 2] = load(k0 + 1 * kGranule, pg);
+        pg = pages_of(k0 + 2 * kGranule);  // (a turn before their tile's loads need them)
+        compute(k0, ring[i]);
+        k0 += kGranule;
+        if (k0 >= kend) break;
+      }
     }
-
     // join the waves
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
