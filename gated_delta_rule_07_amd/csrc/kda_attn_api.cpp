@@ -184,7 +184,7 @@ kda_status kda_attn_decode_plan(kda_dtype kv_dtype, int page_tokens, int width, 
   if (!page_tokens_ok(page_tokens) || !head_dim_ok(d_k) || !head_dim_ok(d_v)) return KDA_ERR_UNSUPPORTED;
   if ((long long)width * page_tokens >= (1LL << 31)) return KDA_ERR_SHAPE;
   if (!workspace_bytes) return KDA_ERR_NULL;
-  *workspace_bytes = kda::attn_decode_workspace(d_v, page_tokens, width);
+  *workspace_bytes = kda::attn_decode_workspace(B, K, H_q, H_kv, d_v, page_tokens, width);
   return KDA_OK;
 }
 
@@ -200,7 +200,7 @@ kda_status kda_attn_decode(const void* q, kda_dtype q_dtype, float scale, const 
   // 32-bit counts: granules of 128 tokens over the sequences, and workgroups
   if ((long long)B * (((long long)width * page_tokens + 127) / 128) >= (1LL << 31) || (long long)B * K * H_q > (1LL << 24))
     return KDA_ERR_SHAPE;
-  const size_t need = kda::attn_decode_workspace(d_v, page_tokens, width);
+  const size_t need = kda::attn_decode_workspace(B, K, H_q, H_kv, d_v, page_tokens, width);
   if (!q || !lens || !o || (need && !workspace)) return KDA_ERR_NULL;
   if (need && workspace_bytes < need) return KDA_ERR_SHAPE;
   if (!need) workspace = nullptr;

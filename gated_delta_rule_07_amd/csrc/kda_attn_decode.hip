@@ -20,11 +20,11 @@
 namespace kda {
 namespace {
 
-constexpr int kWaves = 4, kThreads = 64 * kWaves;
-constexpr int kTile = 32, kGranule = kTile * kWaves;
+constexpr int kTile = 32;         // keys of a wave's turn
+constexpr int kWaves = 4;         // waves of a workgroup that shares the granules (and of a join)
+constexpr int kMoreWaves = 8;     // of one that takes a unit whole where there are few units
 constexpr int kWorkers = 512;     // workgroups that share the granules
 constexpr int kLeastRun = 2;      // granules a workgroup takes at least
-constexpr int kWholeUnits = 2048; // up to this many tokens a sequence, a workgroup takes a unit whole
 constexpr float kSlack = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -51,6 +51,12 @@ __device__ __forceinline__ uint32_t bf16_of_e4m3(uint32_t w, bool hi) {
                                          : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
 }
 
+// Four outputs from element `at` of o on.
+__device__ __forceinline__ void store4(const AttnDecodeParams& p, size_t at, const f32x4& y) {
+  if (p.o_f32) *reinterpret_cast<f32x4*>(static_cast<float*>(p.o) + at) = y;
+  else *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(p.o) + at) = bf16x4{(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
+}
+
 // All ones in the bytes (e4m3) or halves (bf16) of w that are not finite.
 template <bool E4>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
@@ -69,10 +75,10 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
 __device__ __forceinline__ int tokens_of(const AttnDecodeParams& p, int b) {
   return min(max(p.lens[b], 0), p.c.width * p.c.page_tokens);
 }
+template <int NW>
 __device__ __forceinline__ int granules_of(const AttnDecodeParams& p, int b) {
-  const int row = p.c.rows ? p.c.rows[b] : b;
-  if (row < 0 || row >= p.c.n_rows) return 0;
-  return max(1, (tokens_of(p, b) + kGranule - 1) / kGranule);
+  const int row = p.c.rows ? p.c.rows[b] : b, n = tokens_of(p, b);
+  return row < 0 || row >= p.c.n_rows ? 0 : max(1, (n + NW * kTile - 1) / (NW * kTile));
 }
 
 template <bool E4, int DK, int DV>
@@ -98,14 +104,16 @@ __device__ __forceinline__ float column_max(float x) {
   return fmaxf(__builtin_bit_cast(float, c), __builtin_bit_cast(float, d));
 }
 
-template <int NT, bool E4, int DK, int DV>
-__global__ __launch_bounds__(kThreads, 2) void kda_attn_decode_kernel(DecodePlan a) {
+template <int NW, int NT, bool E4, int DK, int DV>
+__global__ __launch_bounds__(64 * NW, 2) void kda_attn_decode_kernel(DecodePlan a) {
+  constexpr int kThreads = 64 * NW, kGranule = NW * kTile;
   using T = Tile<E4, DK, DV>;
+  constexpr int RING = 2;  // tiles of a wave in flight and in work
   constexpr int NM = DV / 16, NS = DK / 32;
   constexpr int ES = E4 ? 1 : 2, CW = 4 / ES;  // bytes of an element, elements of a dword
-  __shared__ __attribute__((aligned(16))) float so[kWaves][kAttnColumns][DV + 4];
-  __shared__ float sm[kWaves][kAttnColumns], sl[kWaves][kAttnColumns];
-  __shared__ int swave[kWaves];
+  __shared__ __attribute__((aligned(16))) float so[NW][kAttnColumns][DV + 4];
+  __shared__ float sm[NW][kAttnColumns], sl[NW][kAttnColumns];
+  __shared__ int swave[NW];
   extern __shared__ int prefix[];  // [B + 1]: granules of the sequences before
   const AttnDecodeParams& p = a.p;
   const KvCache& cache = p.c;
@@ -119,11 +127,11 @@ __global__ __launch_bounds__(kThreads, 2) void kda_attn_decode_kernel(DecodePlan
   if (whole) {
     b = blockIdx.x / units;
     at = mine = 0;
-    end = granules_of(p, b);
+    end = granules_of<NW>(p, b);
   } else {
     const int each = (p.B + kThreads - 1) / kThreads, i0 = min(tid * each, p.B), i1 = min(i0 + each, p.B);
     int sum = 0;
-    for (int i = i0; i < i1; ++i) sum += granules_of(p, i);
+    for (int i = i0; i < i1; ++i) sum += granules_of<NW>(p, i);
     int run = sum;
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) {
@@ -136,7 +144,7 @@ __global__ __launch_bounds__(kThreads, 2) void kda_attn_decode_kernel(DecodePlan
     for (int w = 0; w < wave; ++w) before += swave[w];
     for (int i = i0; i < i1; ++i) {
       prefix[i] = before;
-      before += granules_of(p, i);
+      before += granules_of<NW>(p, i);
     }
     if (tid == kThreads - 1) prefix[p.B] = before;
     __syncthreads();
@@ -164,9 +172,9 @@ __global__ __launch_bounds__(kThreads, 2) void kda_attn_decode_kernel(DecodePlan
       g1 = (int)min((long long)n, g0 + (end - at));
     }
     const int ct = unit / H, h = unit % H;
-    const int row = cache.rows ? cache.rows[b] : b;
+    const int row = __builtin_amdgcn_readfirstlane(cache.rows ? cache.rows[b] : b);
     const int* pages = cache.table + (size_t)row * cache.width;
-    const int len = tokens_of(p, b);
+    const int len = __builtin_amdgcn_readfirstlane(tokens_of(p, b));
     const int cc = kAttnColumns * ct + col, tok = cc / a.G, head = h * a.G + cc % a.G;
     const bool live = tok < p.K;
     const int limit = live ? len - p.K + 1 + tok : len;
@@ -203,16 +211,26 @@ __global__ __launch_bounds__(kThreads, 2) void kda_attn_decode_kernel(DecodePlan
     const uint32_t koff = (uint32_t)(col * DK * ES + 16 * g), voff = (uint32_t)(4 * g * DV * ES + col * T::VW * 4);
     const size_t kat = kv_keys(cache, h), vat = kv_values(cache, h), sat = kv_scales(cache);
     const int kend = min(g1 * kGranule, len);
-    // The pages of a tile's halves, -1 where there is none (behind the sequence a row may name any page).
+    // The pages of a tile's halves, -1 where there is none (behind the sequence a row may name any page).  64 entries of the
+    // row at a time lie in the wave's lanes: a load for each tile would be waited for, and with it all tiles in flight.
     struct Pages {
       int p[2];
     };
+    int first = -64, entries = 0;
     auto pages_of = [&](int k0) {
       Pages r;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int page = k0 + 16 * u < kend ? pages[(k0 + 16 * u) >> lg] : -1;
-        r.p[u] = page < cache.n_pages ? page : -1;
+        r.p[u] = -1;
+        if (k0 + 16 * u < kend) {
+          const int i = (k0 + 16 * u) >> lg;
+          if (i >= first + 64) {
+            first = i;
+            entries = i + lane < cache.width ? pages[i + lane] : -1;
+          }
+          const int page = __builtin_amdgcn_readlane(entries, i - first);
+          r.p[u] = page < cache.n_pages ? page : -1;
+        }
       }
       return r;
     };
@@ -244,8 +262,8 @@ __global__ __launch_bounds__(kThreads, 2) void kda_attn_decode_kernel(DecodePlan
         t.ks[u] = t.vs[u] = 1.0f;
         if constexpr (E4) {
           const float* sc = reinterpret_cast<const float*>(base + sat);
-          t.ks[u] = t.there[u] ? sc[h] : 1.0f;
-          t.vs[u] = t.there[u] ? sc[H + h] : 1.0f;  // (0 times another page's scale could be NaN)
+          t.ks[u] = sc[h];
+          t.vs[u] = sc[H + h];
         }
       }
       return t;
@@ -275,7 +293,8 @@ __global__ __launch_bounds__(kThreads, 2) void kda_attn_decode_kernel(DecodePlan
       const bool partial = k0 + kTile > least || !cur.there[0] || !cur.there[1];  // (the same for the wave)
       if (partial) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
+          cur.vs[u] = cur.there[u] ? cur.vs[u] : 1.0f;  // (0 times another page's scale could be NaN)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             if (!cur.there[u] || k0 + 16 * u + 4 * g + r >= limit) x[u][r] = -__builtin_inff();
@@ -284,6 +303,7 @@ __global__ __launch_bounds__(kThreads, 2) void kda_attn_decode_kernel(DecodePlan
               for (int i = 0; i < T::VW; ++i) cur.v[4 * u + r][i] = 0;
             }
           }
+        }
       }
       float top = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])), fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
       top = column_max(top);
@@ -378,20 +398,22 @@ __global__ __launch_bounds__(kThreads, 2) void kda_attn_decode_kernel(DecodePlan
       }
     };
     int k0 = g0 * kGranule + kTile * wave;
-    T ring[2];
-    Pages pg;
-    if (k0 + 0 * kGranule < kend) ring[0] = load(k0 + 0 * kGranule, pages_of(k0 + 0 * kGranule));
-    pg = pages_of(k0 + 1 * kGranule);
+    T ring[RING];
+#pragma unroll
+    for (int i = 0; i + 1 < RING; ++i)
+      if (k0 + i * kGranule < kend) ring[i] = load(k0 + i * kGranule, pages_of(k0 + i * kGranule));
+    Pages pg = pages_of(k0 + (RING - 1) * kGranule);
     while (k0 < kend) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (k0 + 1 * kGranule < kend) ring[(i + 1) % 2] = load(k0 + 1 * kGranule, pg);
-        pg = pages_of(k0 + 2 * kGranule);  // (a turn before their tile's loads need them)
+      for (int i = 0; i < RING; ++i) {
+        if (k0 + (RING - 1) * kGranule < kend) ring[(i + RING - 1) % RING] = load(k0 + (RING - 1) * kGranule, pg);
+        pg = pages_of(k0 + RING * kGranule);  // (a turn before their tile's loads need them)
         compute(k0, ring[i]);
         k0 += kGranule;
         if (k0 >= kend) break;
       }
     }
+
     // join the waves
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
@@ -415,12 +437,12 @@ __global__ __launch_bounds__(kThreads, 2) void kda_attn_decode_kernel(DecodePlan
       const int c = i / (DV / 4), d = 4 * (i % (DV / 4));
       float top = sm[0][c];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sm[w][c]);
+      for (int w = 1; w < NW; ++w) top = fmaxf(top, sm[w][c]);
       const float base = top == -__builtin_inff() ? 0.0f : top;
       f32x4 y = (f32x4)0.0f;
       float sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
+      for (int w = 0; w < NW; ++w) {
         const float f = __builtin_amdgcn_exp2f(sm[w][c] - base);
         sum += f * sl[w][c];
         y += f * *reinterpret_cast<const f32x4*>(&so[w][c][d]);
@@ -433,71 +455,70 @@ __global__ __launch_bounds__(kThreads, 2) void kda_attn_decode_kernel(DecodePlan
       const int c2 = kAttnColumns * ct + c, tk = c2 / a.G;
       if (tk >= p.K) continue;
       y *= sum == 0.0f ? 0.0f : 1.0f / sum;
-      const size_t x = (((size_t)b * p.K + tk) * p.Hq + h * a.G + c2 % a.G) * DV + d;
-      if (p.o_f32) {
-        *reinterpret_cast<f32x4*>(static_cast<float*>(p.o) + x) = y;
-      } else {
-        bf16x4 z;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] = (__bf16)y[e];
-        *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(p.o) + x) = z;
-      }
+      store4(p, (((size_t)b * p.K + tk) * p.Hq + h * a.G + c2 % a.G) * DV + d, y);
     }
     __syncthreads();
     at += g1 - g0;
   }
 }
 
-// Joins the parts of a unit that several workers share: a wave a row of queries.
+// Joins the parts of a unit that several workers share: a workgroup a row of queries.  DV / 4 lanes hold a row, the
+// groups of lanes take the parts in turn, so that the parts of even a long unit are in flight together.
 template <int DV>
-__global__ __launch_bounds__(kThreads) void kda_attn_join_kernel(DecodePlan a) {
-  constexpr int ND = DV / 64;
-  const int w0 = blockIdx.x, lane = threadIdx.x % 64, c = blockIdx.y * kWaves + threadIdx.x / 64;
+__global__ __launch_bounds__(256) void kda_attn_join_kernel(DecodePlan a) {
+  constexpr int NL = DV / 4, NG = 256 / NL;
+  __shared__ float sf[256], sl[4];
+  __shared__ __attribute__((aligned(16))) float sy[NG][DV];
+  const int w0 = blockIdx.x, tid = threadIdx.x, lane = tid % 64, c = blockIdx.y, e = 4 * (tid % NL), gr = tid / NL;
   const Join j = a.joins[w0];
   if (j.unit < 0) return;
   const AttnDecodeParams& p = a.p;
   const int units = a.CT * p.c.H, b = j.unit / units, ct = j.unit % units / p.c.H, h = j.unit % p.c.H;
-  const int c2 = kAttnColumns * ct + c, tk = c2 / a.G;
+  const int c2 = kAttnColumns * ct + c, tk = c2 / a.G, n = j.last - w0 + 1;
   if (tk >= p.K) return;
   // worker w0's part is its first or its second, the others' their first
-  auto part = [&](int w) { return a.parts + (2 * (size_t)w + (w == w0 ? j.slot : 0)) * part_floats(DV); };
+  auto part = [&](int i) { return a.parts + (2 * (size_t)(w0 + i) + (i == 0 ? j.slot : 0)) * part_floats(DV); };
+  // every wave finds the maximum; thread i holds the weights of the parts i, i + 256, ..
   float top = -__builtin_inff();
-  for (int w = w0 + lane; w <= j.last; w += 64) top = fmaxf(top, part(w)[kAttnColumns * DV + c]);
+  for (int i = lane; i < n; i += 64) top = fmaxf(top, part(i)[kAttnColumns * DV + c]);
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) top = fmaxf(top, __shfl_xor(top, m));
   const float base = top == -__builtin_inff() ? 0.0f : top;
-  float y[ND], sum = 0.0f;
-#pragma unroll
-  for (int e = 0; e < ND; ++e) y[e] = 0.0f;
-  for (int w1 = w0; w1 <= j.last; w1 += 64) {
+  f32x4 y = (f32x4)0.0f;
+  float sum = 0.0f;
+  for (int i0 = 0; i0 < n; i0 += 256) {
     float f = 0.0f;
-    if (w1 + lane <= j.last) {
-      const float* x = part(w1 + lane) + kAttnColumns * DV + c;
+    if (i0 + tid < n) {
+      const float* x = part(i0 + tid) + kAttnColumns * DV + c;
       f = __builtin_amdgcn_exp2f(x[0] - base);
       sum += f * x[kAttnColumns];
     }
-    const int n = min(64, j.last - w1 + 1);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float fi = __shfl(f, i);
-      const float* x = part(w1 + i) + c * DV + ND * lane;
-#pragma unroll
-      for (int e = 0; e < ND; ++e) y[e] += fi * x[e];
-    }
+    __syncthreads();
+    sf[tid] = f;
+    __syncthreads();
+    const int some = min(n - i0, 256);
+#pragma unroll 8
+    for (int i = gr; i < some; i += NG) y += sf[i] * *reinterpret_cast<const f32x4*>(part(i0 + i) + c * DV + e);
   }
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) sum += __shfl_xor(sum, m);
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const size_t at = (((size_t)b * p.K + tk) * p.Hq + h * a.G + c2 % a.G) * DV + ND * lane;
+  if (lane == 0) sl[tid / 64] = sum;
+  *reinterpret_cast<f32x4*>(&sy[gr][e]) = y;
+  __syncthreads();
+  if (tid >= NL) return;
+  sum = sl[0] + sl[1] + sl[2] + sl[3];
 #pragma unroll
-  for (int e = 0; e < ND; ++e) {
-    if (p.o_f32) static_cast<float*>(p.o)[at + e] = y[e] * inv;
-    else static_cast<__bf16*>(p.o)[at + e] = (__bf16)(y[e] * inv);
-  }
+  for (int i = 1; i < NG; ++i) y += *reinterpret_cast<const f32x4*>(&sy[i][e]);
+  store4(p, (((size_t)b * p.K + tk) * p.Hq + h * a.G + c2 % a.G) * DV + e, y * (sum == 0.0f ? 0.0f : 1.0f / sum));
 }
 
-// Whether a call takes its units whole, a workgroup each: no workspace and no second launch.
-bool takes_whole(int page_tokens, int width) { return (long long)width * page_tokens <= kWholeUnits; }
+// Whether a call takes its units whole, a workgroup each: no workspace and no second launch.  With 32 + 8 heads of 128 in
+// e4m3, whole against shared, us: 1 sequence (8 units) of 1,000 tokens 10.8 / 11.4, of 2,000 16.3 / 11.4; 16 sequences of
+// 2,000 17.8 / 22.0, of 4,000 33.0 / 30.1; 64 of 4,000 85.8 / 89.6, of 8,000 163 / 158; 256 of 300 to 9,000 480 / 464.
+bool takes_whole(long long tokens, long long units) { return tokens <= 1536 || (tokens <= 4096 && units >= 128); }
+bool takes_whole(int B, int K, int Hq, int H, int page_tokens, int width) {
+  return takes_whole((long long)page_tokens * width, (long long)B * columns(K, Hq / H) * H);
+}
 
 template <int NT, bool E4, int DK, int DV>
 hipError_t launch_one(const AttnDecodeParams& p, hipStream_t s) {
@@ -505,17 +526,23 @@ hipError_t launch_one(const AttnDecodeParams& p, hipStream_t s) {
   a.p = p;
   a.G = p.Hq / p.c.H;
   a.CT = columns(p.K, a.G);
-  const bool whole = takes_whole(p.c.page_tokens, p.c.width);
+  const bool whole = takes_whole(p.B, p.K, p.Hq, p.c.H, p.c.page_tokens, p.c.width);
   a.workers = whole ? 0 : kWorkers;
   a.parts = static_cast<float*>(p.ws);
   a.joins = whole ? nullptr : reinterpret_cast<Join*>(a.parts + 2 * (size_t)kWorkers * part_floats(DV));
-  const unsigned grid = whole ? (unsigned)p.B * a.CT * p.c.H : kWorkers;
-  hipLaunchKernelGGL((kda_attn_decode_kernel<NT, E4, DK, DV>), dim3(grid), dim3(kThreads),
-                     whole ? 0 : sizeof(int) * ((size_t)p.B + 1), s, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || whole) return e;
+  if (whole) {
+    const unsigned grid = (unsigned)p.B * a.CT * p.c.H;
+    // no more workgroups than compute units: more waves each
+    if (grid <= 256) hipLaunchKernelGGL((kda_attn_decode_kernel<kMoreWaves, NT, E4, DK, DV>), dim3(grid), dim3(64 * kMoreWaves), 0, s, a);
+    else hipLaunchKernelGGL((kda_attn_decode_kernel<kWaves, NT, E4, DK, DV>), dim3(grid), dim3(64 * kWaves), 0, s, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((kda_attn_decode_kernel<kWaves, NT, E4, DK, DV>), dim3(kWorkers), dim3(64 * kWaves),
+                     sizeof(int) * ((size_t)p.B + 1), s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   const int rows = std::min(kAttnColumns, p.K * a.G);
-  hipLaunchKernelGGL((kda_attn_join_kernel<DV>), dim3(kWorkers, (rows + kWaves - 1) / kWaves), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((kda_attn_join_kernel<DV>), dim3(kWorkers, rows), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -527,8 +554,8 @@ hipError_t pick_dims(const AttnDecodeParams& p, hipStream_t s) {
 
 }  // namespace
 
-size_t attn_decode_workspace(int dv, int page_tokens, int width) {
-  if (takes_whole(page_tokens, width)) return 0;
+size_t attn_decode_workspace(int B, int K, int Hq, int H, int dv, int page_tokens, int width) {
+  if (takes_whole(B, K, Hq, H, page_tokens, width)) return 0;
   return (size_t)kWorkers * (2 * part_floats(dv) * sizeof(float) + sizeof(Join));
 }
 

@@ -398,7 +398,7 @@ struct AttnDecodeParams {
   int o_f32;
   float scale;
 };
-size_t attn_decode_workspace(int dv, int page_tokens, int width);  // bytes
+size_t attn_decode_workspace(int B, int K, int Hq, int H, int dv, int page_tokens, int width);  // bytes
 hipError_t launch_attn_decode(const AttnDecodeParams& p, int q_dtype, hipStream_t s);
 
 bool decode_supported(int io_dtype, int dk, int dv);
