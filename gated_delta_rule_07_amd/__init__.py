@@ -9,6 +9,7 @@ fallback: if the library is missing the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 from pathlib import Path
 from typing import NamedTuple
 
@@ -532,7 +533,7 @@ def kda_decode_commit(k, alpha, u, n_accept, S, *, stream=None):
 _NORMS = {"l2": 0, "rms": 1}
 _PAIRINGS = {"halves": 0, "pairs": 1}
 _CODES = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
-_I32, _F32 = torch.int32, torch.float32
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
 
 # The calls below serve single tokens too, where a step's time is the time to issue
 # it: their checks read each property of a tensor once, and say what is wrong with
@@ -884,6 +885,15 @@ def kda_tree_commit(k, alpha, u, parents, last, pool, pages_in, pages_out=None, 
 _KV_CODES = {torch.bfloat16: KDA_BF16, torch.float8_e4m3fn: KDA_E4M3}
 
 
+@functools.lru_cache(maxsize=256)
+def _page_bytes(dtype, page_tokens, H, d_k, d_v):
+    n = ctypes.c_size_t(0)
+    st = (_lib or load_library()).kda_kv_page_bytes(_KV_CODES.get(dtype, -1), page_tokens, H, d_k, d_v, ctypes.byref(n))
+    if st != 0:
+        raise KdaError(st, "kda_kv_page_bytes")
+    return n.value
+
+
 class KVLayout(NamedTuple):
     """What a page of keys and values holds: ``page_tokens`` tokens of ``H`` heads, keys of ``d_k`` and values of
     ``d_v``, as ``dtype`` (torch.bfloat16, or torch.float8_e4m3fn with a scale for each head's keys and values on the
@@ -897,12 +907,7 @@ class KVLayout(NamedTuple):
 
     @property
     def page_bytes(self) -> int:
-        n = ctypes.c_size_t(0)
-        st = (_lib or load_library()).kda_kv_page_bytes(_KV_CODES.get(self.dtype, -1), self.page_tokens, self.H, self.d_k, self.d_v,
-                                                        ctypes.byref(n))
-        if st != 0:
-            raise KdaError(st, "kda_kv_page_bytes")
-        return n.value
+        return _page_bytes(*self)
 
     def pool(self, n_pages: int, device, n_layers: int | None = None) -> torch.Tensor:
         """A pool of zeros."""
@@ -922,13 +927,16 @@ class KVLayout(NamedTuple):
 
 def _kv_cache(pool, layout, table, rows, n, dev):
     """(pool, kv code, n_pages, page_tokens, table, n_rows, width, rows) of the calls on pages of keys and values."""
-    code = _KV_CODES.get(layout.dtype)
+    dtype, pt, H, dk, dv = layout
+    code = _KV_CODES.get(dtype)
     if code is None:
-        raise TypeError(f"libkda: pages hold bfloat16 or float8_e4m3fn, got {layout.dtype}")
-    P = _tensor(pool, "pool").shape[0] if _tensor(pool, "pool").dim() == 2 else -1
-    R, W = _tensor(table, "table").shape if table.dim() == 2 else (-1, -1)
-    return (_need(pool, "pool", torch.uint8, dev, (P, layout.page_bytes)), code, P, layout.page_tokens,
-            _need(table, "table", _I32, dev, (R, W)), R, W, _may(rows, "rows", _I32, dev, (n,)))
+        raise TypeError(f"libkda: pages hold bfloat16 or float8_e4m3fn, got {dtype}")
+    shape, tshape = _tensor(pool, "pool").shape, _tensor(table, "table").shape
+    if len(shape) != 2 or len(tshape) != 2:
+        raise ValueError("libkda: pool must be [n_pages,page_bytes] and table [n_rows,width]")
+    P, (R, W) = shape[0], tshape
+    return (_need(pool, "pool", _U8, dev, (P, _page_bytes(dtype, pt, H, dk, dv))), code, P, pt,
+            _need(table, "table", _I32, dev, tshape), R, W, None if rows is None else _need(rows, "rows", _I32, dev, (n,)))
 
 
 def kda_attn_fwd(q, k, v, *, scale=None, cu_seqlens=None, cu_seqlens_k=None, o=None, o_dtype=None, stream=None):
@@ -1034,6 +1042,7 @@ def kda_kv_read(pool, layout, table, cu_seqlens, total: int, *, rows=None, start
     return k_out, v_out
 
 
+@functools.lru_cache(maxsize=1024)
 def kda_attn_decode_plan(layout, B: int, K: int, H_q: int, width: int) -> int:
     """Bytes of workspace that a ``kda_attn_decode`` call with these sizes needs (``width``: the page table's)."""
     n = ctypes.c_size_t(0)

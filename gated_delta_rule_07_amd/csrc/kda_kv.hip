@@ -8,7 +8,8 @@
 //
 // Append: a workgroup takes one page of one sequence, so that the tokens of a page share the scale's
 // maximum and the cosines and sines (in LDS) serve all heads; a wave takes one head's keys or values.
-// Lanes hold 8 values of a row.  Workgroups behind the pages turn the queries.
+// Workgroups behind the pages turn the queries.  A lane holds two pieces of 8 values of a row, those
+// that turn together, so that a rotation exchanges nothing between lanes.
 #include <algorithm>
 
 #include "kda_kv_device.h"
@@ -20,20 +21,6 @@ constexpr int kThreads = 256, kWaves = kThreads / 64;
 
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
-__device__ __forceinline__ f32x8 load8(const float* p) {
-  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
-  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-__device__ __forceinline__ f32x8 load8(const __bf16* p) {
-  const u32x4 w = *reinterpret_cast<const u32x4*>(p);
-  f32x8 r;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    r[2 * e] = __builtin_bit_cast(float, w[e] << 16);
-    r[2 * e + 1] = __builtin_bit_cast(float, w[e] & 0xffff0000u);
-  }
-  return r;
-}
 __device__ __forceinline__ void store8(float* p, f32x8 x) {
   *reinterpret_cast<f32x4*>(p) = __builtin_shufflevector(x, x, 0, 1, 2, 3);
   *reinterpret_cast<f32x4*>(p + 4) = __builtin_shufflevector(x, x, 4, 5, 6, 7);
@@ -53,37 +40,76 @@ __device__ __forceinline__ float2 turn_of(long long pos, float freq) {
   return float2{c, s};
 }
 
-// y, 8 values from i0 = 8 gl on of a head that `lanes` lanes hold, with the first rot of them turned by ft.
-__device__ __forceinline__ f32x8 rotate8(f32x8 y, const float2* ft, int rot, int adjacent, int gl, int lanes) {
-  if (!rot) return y;
-  const int i0 = 8 * gl, half = rot / 2;
-  if (adjacent) {
-    if (i0 < rot) {
+// The two pieces of 8 values that a lane of a row's d / 16 holds.
+struct Pieces {
+  int c0, c1;
+  bool turned;
+};
+__device__ __forceinline__ Pieces pieces_of(int lane, int lanes, int rot) {
+  const int m = rot / 16;  // the first m lanes hold what turns: pieces j and j + m; the others halves of the rest
+  return lane < m ? Pieces{lane, lane + m, true} : Pieces{m + lane, lanes + lane, false};
+}
+
+// A lane's cosines and sines: of its 8 pairs (i, i + rot/2), or of the 4 + 4 neighbours in its pieces.
+struct Turns {
+  float2 f[8];
+};
+__device__ __forceinline__ Turns turns_at(const float2* ft, const Pieces& c, int adjacent) {
+  Turns t;
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float2 f = ft[(i0 + e) / 2];
-        const float a = y[e], b = y[e + 1];
-        y[e] = a * f.x - b * f.y;
-        y[e + 1] = b * f.x + a * f.y;
-      }
-    }
-    return y;
+  for (int e = 0; e < 8; ++e) t.f[e] = float2{1.0f, 0.0f};
+  if (c.turned) {
+    const float2* lo = ft + (adjacent ? 4 : 8) * c.c0;
+    const float2* hi = adjacent ? ft + 4 * c.c1 : lo + 4;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t.f[e] = lo[e], t.f[4 + e] = hi[e];
   }
-  const int m = half / 8;  // lanes of each half
-  const int partner = gl < m ? gl + m : gl < 2 * m ? gl - m : gl;
-  f32x8 other;
+  return t;
+}
+__device__ __forceinline__ void rotate(f32x8& a, f32x8& b, const Turns& t, int adjacent) {
+  if (adjacent) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) other[e] = __shfl(y[e], partner, lanes);
-  if (gl < 2 * m) {
-    const float sign = gl < m ? -1.0f : 1.0f;
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = t.f[e], g = t.f[4 + e];
+      const float x = a[2 * e], y = a[2 * e + 1], z = b[2 * e], w = b[2 * e + 1];
+      a[2 * e] = x * f.x - y * f.y;
+      a[2 * e + 1] = y * f.x + x * f.y;
+      b[2 * e] = z * g.x - w * g.y;
+      b[2 * e + 1] = w * g.x + z * g.y;
+    }
+  } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float2 f = ft[(gl < m ? i0 : i0 - half) + e];
-      y[e] = y[e] * f.x + sign * other[e] * f.y;
+      const float x = a[e], y = b[e];
+      a[e] = x * t.f[e].x - y * t.f[e].y;
+      b[e] = y * t.f[e].x + x * t.f[e].y;
     }
   }
-  return y;
 }
+
+// 8 values as they lie in memory, so that many rows can be in flight.
+template <typename IO>
+struct Raw {
+  u32x4 w[sizeof(IO) / 2];
+  __device__ __forceinline__ void load(const IO* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(IO) / 2; ++i) w[i] = reinterpret_cast<const u32x4*>(p)[i];
+  }
+  __device__ __forceinline__ f32x8 values() const {
+    f32x8 r;
+    if constexpr (sizeof(IO) == 2) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        r[2 * e] = __builtin_bit_cast(float, w[0][e] << 16);
+        r[2 * e + 1] = __builtin_bit_cast(float, w[0][e] & 0xffff0000u);
+      }
+    } else {
+      const f32x4 lo = __builtin_bit_cast(f32x4, w[0]), hi = __builtin_bit_cast(f32x4, w[1]);
+      r = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    return r;
+  }
+};
 
 // Tokens [t0, t0 + n) of the call are sequence b's, behind the `before` it has.
 struct Span {
@@ -103,66 +129,98 @@ __device__ __forceinline__ long long touched(const Span& s, int pt) {
 }
 
 // Whether another page of the call than the j-th of sequence b is `page` too (seen by any thread of the workgroup).
+// The loads of a turn do not wait for one another: indexes are brought into range instead of being tested first.
 __device__ bool shared_page(const AppendParams& p, int page, int b, long long j, int tid) {
-  const int lane = tid % 64, wave = tid / 64;
+  const int lane = tid % 64, wave = tid / 64, pt = p.c.page_tokens;
+  auto names = [&](int row, long long at) {
+    const int e = p.c.table[(size_t)clamp_to(row, p.c.n_rows - 1) * p.c.width + min(max(at, 0LL), p.c.width - 1LL)];
+    return row >= 0 && row < p.c.n_rows && at >= 0 && at < p.c.width && e == page;
+  };
   bool hit = false;
-  for (int c0 = 64 * wave; c0 < p.N; c0 += 64 * kWaves) {
-    // a lane looks after one sequence; where one has many pages, the wave takes sequence after sequence
-    const int c = c0 + lane;
-    long long first = 0, n = 0;
-    if (c < p.N) {
-      const Span s = span_of(p, c);
-      first = s.before / p.c.page_tokens;
-      n = min(touched(s, p.c.page_tokens), max(0LL, p.c.width - first));
-    }
-    if (!__any(n > 8)) {
-      for (long long i = 0; i < n; ++i) hit |= !(c == b && i == j) && kv_page(p.c, c, first + i) == page;
+  if (!p.cu) {  // one page a sequence
+    for (int c = tid; c < p.N; c += kThreads) hit |= c != b && names(p.c.rows ? p.c.rows[c] : c, max(p.lens[c], 0) / pt);
+    return hit;
+  }
+  for (int c0 = 0; c0 < p.N; c0 += 64) {
+    // a lane looks after one sequence; where one has many pages, the wave takes every kWaves-th sequence after the other
+    const int c = min(c0 + lane, p.N - 1);
+    const Span s = span_of(p, c);
+    const int row = p.c.rows ? p.c.rows[c] : c;
+    const long long first = s.before / pt;
+    const int n = c0 + lane < p.N ? (int)min(touched(s, pt), max(0LL, p.c.width - first)) : 0;
+    if (!__any(n > 4)) {
+      if (c0 / 64 % kWaves == wave)
+        for (int i = 0; i < 4; ++i) hit |= i < n && !(c == b && i == j) && names(row, first + i);
     } else {
-      for (int l = 0; l < 64 && c0 + l < p.N; ++l) {
-        const long long f = __shfl(first, l), m = __shfl(n, l);
-        for (long long i = lane; i < m; i += 64) hit |= !(c0 + l == b && i == j) && kv_page(p.c, c0 + l, f + i) == page;
+#pragma unroll 4
+      for (int l = wave; l < 64; l += kWaves) {
+        const int m = __shfl(n, l), r = __shfl(row, l), q = c0 + l;
+        const long long f = __shfl(first, l);
+        for (int i = lane; i < m; i += 64) hit |= !(q == b && i == j) && names(r, f + i);
       }
     }
   }
   return hit;
 }
 
+constexpr int kMostQueryTokens = 8;
+
 template <typename IO>
 __device__ void append_queries(const AppendParams& p, int block, int tokens, float2* turn, int tid) {
   const int t0 = block * tokens, nt = min(tokens, p.total - t0), half = p.rot / 2;
+  const int b0 = p.cu && !p.positions && half ? last_at_most_wave(p.N, t0, [&](int i) { return (long long)p.cu[i]; }) : 0;
   for (int e = tid; e < nt * half; e += kThreads) {
     const int t = t0 + e / half;
     long long pos = 0;
     if (p.positions) {
       pos = p.positions[t];
     } else {
-      const int b = p.cu ? last_at_most(p.N, t, [&](int i) { return (long long)p.cu[i]; }) : t;
+      int b = p.cu ? b0 : t;
+      if (p.cu)
+        while (b + 1 < p.N && p.cu[b + 1] <= t) ++b;
       const Span s = span_of(p, b);
       pos = s.before + t - s.t0;
     }
     turn[e] = turn_of(pos, p.inv_freq[e % half]);
   }
   __syncthreads();
-  const int lanes = p.c.dk / 8, gl = tid % lanes;
+  // a group of lanes takes one token, and some of its heads: its cosines and sines stay in registers
+  const int lanes = p.c.dk / 16, groups = kThreads / lanes, gr = tid / lanes, d = p.c.dk;
+  const int t = gr % tokens, tok = t0 + t;
   // tokens behind the last sequence's are left as they were
-  const int end = p.cu ? clamp_to(p.cu[p.N], p.total) : p.total;
-  for (int r = tid / lanes; r < nt * p.Hq; r += kThreads / lanes) {
-    const int t = r / p.Hq, h = r % p.Hq;
-    const size_t tok = (size_t)(t0 + t);
-    if ((int)tok >= end || (p.cu && (int)tok < p.cu[0])) continue;
-    const f32x8 x = load8(static_cast<const IO*>(p.q) + tok * p.q_stride + (size_t)h * p.c.dk + 8 * gl);
-    store8(static_cast<IO*>(p.q_out) + tok * p.q_out_stride + (size_t)h * p.c.dk + 8 * gl,
-           rotate8(x, turn + t * half, p.rot, p.adjacent, gl, lanes));
+  if (t >= nt || (p.cu && (tok < p.cu[0] || tok >= clamp_to(p.cu[p.N], p.total)))) return;
+  const Pieces c = pieces_of(tid % lanes, lanes, p.rot);
+  const Turns f = turns_at(turn + t * half, c, p.adjacent);
+  const IO* x = static_cast<const IO*>(p.q) + (size_t)tok * p.q_stride;
+  IO* y = static_cast<IO*>(p.q_out) + (size_t)tok * p.q_out_stride;
+  constexpr int NB = 4;  // heads in flight
+  const int step = groups / tokens;
+  for (int h0 = gr / tokens; h0 < p.Hq; h0 += NB * step) {
+    Raw<IO> a[NB], b[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int h = h0 + i * step;
+      if (h < p.Hq) a[i].load(x + (size_t)h * d + 8 * c.c0), b[i].load(x + (size_t)h * d + 8 * c.c1);
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int h = h0 + i * step;
+      if (h >= p.Hq) break;
+      f32x8 u = a[i].values(), v = b[i].values();
+      if (c.turned) rotate(u, v, f, p.adjacent);
+      store8(y + (size_t)h * d + 8 * c.c0, u);
+      store8(y + (size_t)h * d + 8 * c.c1, v);
+    }
   }
 }
 
-template <typename IO, bool E4>
+template <typename IO, bool E4, int NB>
 __global__ __launch_bounds__(kThreads) void kda_kv_append_kernel(AppendParams p, int page_blocks, int q_tokens) {
-  extern __shared__ float2 turn[];  // [tokens][rot / 2]: cosine and sine
+  extern __shared__ __attribute__((aligned(16))) float2 turn[];  // [tokens][rot / 2]: cosine and sine
   __shared__ int flag[kWaves];
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
   if ((int)blockIdx.x >= page_blocks) {
-    if (blockIdx.y == 0) append_queries<IO>(p, blockIdx.x - page_blocks, q_tokens, turn, tid);
+    append_queries<IO>(p, (blockIdx.x - page_blocks) * gridDim.y + blockIdx.y, q_tokens, turn, tid);
     return;
   }
   const KvCache& c = p.c;
@@ -172,7 +230,7 @@ __global__ __launch_bounds__(kThreads) void kda_kv_append_kernel(AppendParams p,
   long long j = 0;
   if (p.cu) {
     auto first = [&](int i) { return (long long)(clamp_to(p.cu[i], p.total) / pt) + 2LL * i; };
-    b = last_at_most(p.N, blockIdx.x, first);
+    b = last_at_most_wave(p.N, blockIdx.x, first);
     j = blockIdx.x - first(b);
   }
   const Span s = span_of(p, b);
@@ -182,6 +240,34 @@ __global__ __launch_bounds__(kThreads) void kda_kv_append_kernel(AppendParams p,
   const int first = j == 0 ? 0 : (int)(at * pt - s.before);  // its first token among the sequence's new ones
   const int nt = min(pt - slot0, s.n - first);
   const int t0 = s.t0 + first, half = p.rot / 2;
+  // a wave's head: of the keys, then of the values
+  int pair = blockIdx.y * kWaves + wave, h = 0, d = 0, rows = 0, r0 = 0;
+  bool is_v = false;
+  Pieces pc{0, 0, false};
+  long long stride = 0;
+  const IO* x = nullptr;
+  Raw<IO> ra[NB], rb[NB];
+  auto fetch = [&](int t1) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int t = t1 + i * rows + r0;
+      if (t < nt) {
+        const IO* y = x + (size_t)t * stride;
+        ra[i].load(y + 8 * pc.c0), rb[i].load(y + 8 * pc.c1);
+      }
+    }
+  };
+  auto begin = [&] {  // its first rows in flight
+    is_v = pair >= c.H;
+    h = is_v ? pair - c.H : pair, d = is_v ? c.dv : c.dk;
+    const int lanes = d / 16;
+    rows = 64 / lanes, r0 = lane / lanes;
+    pc = pieces_of(lane % lanes, lanes, is_v ? 0 : p.rot);
+    stride = is_v ? p.v_stride : p.k_stride;
+    x = static_cast<const IO*>(is_v ? p.v : p.k) + (size_t)t0 * stride + (size_t)h * d;
+    fetch(0);
+  };
+  if (pair < 2 * c.H) begin();
   const int page = kv_page(c, b, at);
   const bool any = __any(page >= 0 && shared_page(p, page, b, j, tid));
   if (lane == 0) flag[wave] = any;
@@ -194,27 +280,29 @@ __global__ __launch_bounds__(kThreads) void kda_kv_append_kernel(AppendParams p,
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) store = store && !flag[w];
 
-  for (int pair = blockIdx.y * kWaves + wave; pair < 2 * c.H; pair += gridDim.y * kWaves) {
-    const bool is_v = pair >= c.H;
-    const int h = is_v ? pair - c.H : pair, d = is_v ? c.dv : c.dk;
-    const int lanes = d / 8, gl = lane % lanes, rows = 64 / lanes;
-    const long long stride = is_v ? p.v_stride : p.k_stride;
-    const IO* x = static_cast<const IO*>(is_v ? p.v : p.k) + (size_t)t0 * stride + (size_t)h * d + 8 * gl;
+  for (; pair < 2 * c.H;) {
     char* block = c.pool + (size_t)max(page, 0) * c.page_bytes + (is_v ? kv_values(c, h) : kv_keys(c, h));
-    auto row = [&](int t) {
-      f32x8 y = (f32x8)0.0f;
-      if (t < nt) y = load8(x + (size_t)t * stride);
-      return is_v ? y : rotate8(y, turn + min(t, nt - 1) * half, p.rot, p.adjacent, gl, lanes);
+    auto value = [&](int i, int t, f32x8& a, f32x8& b8) {
+      a = ra[i].values(), b8 = rb[i].values();
+      if (pc.turned) rotate(a, b8, turns_at(turn + t * half, pc, p.adjacent), p.adjacent);
     };
     float inv = 1.0f;
     if (E4 && store) {
       float amax = 0.0f;
-      for (int t = lane / lanes; t < nt + lane / lanes; t += rows) {  // (all lanes take part in every turn: rotations exchange values)
-        const f32x8 y = row(t);
+      for (int t1 = 0; t1 < nt; t1 += NB * rows) {
+        if (t1) fetch(t1);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float a = __builtin_fabsf(y[e]);
-          amax = a < __builtin_inff() ? fmaxf(amax, a) : amax;
+        for (int i = 0; i < NB; ++i) {
+          const int t = t1 + i * rows + r0;
+          if (t >= nt) break;
+          f32x8 a, b8;
+          value(i, t, a, b8);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float u = __builtin_fabsf(a[e]), v = __builtin_fabsf(b8[e]);
+            amax = u < __builtin_inff() ? fmaxf(amax, u) : amax;
+            amax = v < __builtin_inff() ? fmaxf(amax, v) : amax;
+          }
         }
       }
 #pragma unroll
@@ -235,83 +323,129 @@ __global__ __launch_bounds__(kThreads) void kda_kv_append_kernel(AppendParams p,
       }
       if (lane == 0) *scale = now;
       inv = 1.0f / now;  // (a power of two: exact)
+      if (nt > NB * rows) fetch(0);
     }
-    for (int t = lane / lanes; t < nt + lane / lanes; t += rows) {
-      const f32x8 y = row(t);
-      if (t >= nt) continue;
-      if (store) {
-        if constexpr (E4) {
-          const f32x8 z = y * inv;
-          *reinterpret_cast<u32x2*>(block + ((size_t)(slot0 + t) * d + 8 * gl)) =
-              u32x2{to_e4m3x4(z[0], z[1], z[2], z[3]), to_e4m3x4(z[4], z[5], z[6], z[7])};
-        } else {
-          store8(reinterpret_cast<__bf16*>(block) + (size_t)(slot0 + t) * d + 8 * gl, y);
+    for (int t1 = 0; t1 < nt; t1 += NB * rows) {
+      if (t1) fetch(t1);
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const int t = t1 + i * rows + r0;
+        if (t >= nt) break;
+        f32x8 a, b8;
+        value(i, t, a, b8);
+        if (store) {
+          const size_t to = (size_t)(slot0 + t) * d;
+          if constexpr (E4) {
+            const f32x8 u = a * inv, v = b8 * inv;
+            *reinterpret_cast<u32x2*>(block + to + 8 * pc.c0) = u32x2{to_e4m3x4(u[0], u[1], u[2], u[3]), to_e4m3x4(u[4], u[5], u[6], u[7])};
+            *reinterpret_cast<u32x2*>(block + to + 8 * pc.c1) = u32x2{to_e4m3x4(v[0], v[1], v[2], v[3]), to_e4m3x4(v[4], v[5], v[6], v[7])};
+          } else {
+            store8(reinterpret_cast<__bf16*>(block) + to + 8 * pc.c0, a);
+            store8(reinterpret_cast<__bf16*>(block) + to + 8 * pc.c1, b8);
+          }
+        }
+        if (!is_v && p.k_out) {
+          IO* y = static_cast<IO*>(p.k_out) + (size_t)(t0 + t) * p.k_out_stride + (size_t)h * d;
+          store8(y + 8 * pc.c0, a);
+          store8(y + 8 * pc.c1, b8);
         }
       }
-      if (!is_v && p.k_out)
-        store8(static_cast<IO*>(p.k_out) + (size_t)(t0 + t) * p.k_out_stride + (size_t)h * d + 8 * gl, y);
     }
+    pair += gridDim.y * kWaves;
+    if (pair < 2 * c.H) begin();
   }
 }
 
-template <typename IO, bool E4>
-hipError_t append_one(const AppendParams& p, hipStream_t s) {
+template <typename IO, bool E4, int NB>
+hipError_t append_nb(const AppendParams& p, hipStream_t s) {
   const long long pages = p.cu ? (long long)p.total / p.c.page_tokens + 2LL * p.N : p.N;
-  const int q_tokens = p.q ? std::max(1, std::min(16, 4 * kThreads / (p.Hq * (p.c.dk / 8)))) : 1;
+  // more tokens a workgroup where there are enough of them to fill the compute units
+  int q_tokens = 1;
+  while (q_tokens < kMostQueryTokens && (long long)p.total >= 2048LL * q_tokens) q_tokens *= 2;
   const long long q_blocks = p.q ? (p.total + q_tokens - 1) / q_tokens : 0;
   // a wave a head where the pages alone would not fill the compute units
   const int most = (2 * p.c.H + kWaves - 1) / kWaves;
   const int split = (int)std::max(1LL, std::min((long long)most, 2048 / std::max(pages, 1LL)));
   const size_t lds = (size_t)std::max(p.cu ? p.c.page_tokens : 1, q_tokens) * (p.rot / 2) * sizeof(float2);
   if (lds > 65000) {  // more than the default has to be asked for
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&kda_kv_append_kernel<IO, E4>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&kda_kv_append_kernel<IO, E4, NB>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((kda_kv_append_kernel<IO, E4>), dim3((unsigned)(pages + q_blocks), split), dim3(kThreads), lds, s, p,
-                     (int)pages, q_tokens);
+  hipLaunchKernelGGL((kda_kv_append_kernel<IO, E4, NB>), dim3((unsigned)(pages + (q_blocks + split - 1) / split), split),
+                     dim3(kThreads), lds, s, p, (int)pages, q_tokens);
   return hipGetLastError();
+}
+
+template <typename IO, bool E4>
+hipError_t append_one(const AppendParams& p, hipStream_t s) {
+  return p.cu ? append_nb<IO, E4, sizeof(IO) == 2 ? 4 : 2>(p, s) : append_nb<IO, E4, 1>(p, s);
 }
 
 // ---- back ---------------------------------------------------------------------------------
 
-constexpr int kReadTokens = 32;
+constexpr int kReadTokens = 8;
 
-// A lane moves V values (16 bytes of the page) of a token's head.
+// A lane moves V values (16 bytes of the page) of a token's head: always the same ones, of one token after another.
 template <typename OUT, bool E4>
 __global__ __launch_bounds__(kThreads) void kda_kv_read_kernel(ReadParams p) {
   __shared__ int page[kReadTokens], slot[kReadTokens];
-  constexpr int V = E4 ? 16 : 8;
+  constexpr int V = E4 ? 16 : 8, NB = 4;
   const KvCache& c = p.c;
-  const int tid = threadIdx.x, t0 = blockIdx.x * kReadTokens, nt = min(kReadTokens, p.total - t0);
-  if (tid < nt) {
-    const int t = t0 + tid;
-    const int b = last_at_most(p.N, t, [&](int i) { return (long long)p.cu[i]; });
-    const int begin = clamp_to(p.cu[b], p.total), end = clamp_to(p.cu[b + 1], p.total);
-    const long long pos = (p.starts ? max(p.starts[b], 0) : 0) + (long long)(t - begin);
-    page[tid] = t >= begin && t < end ? kv_page(c, b, pos / c.page_tokens) : -1;
-    slot[tid] = (int)(pos % c.page_tokens);
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, t0 = blockIdx.x * kReadTokens, nt = min(kReadTokens, p.total - t0);
+  if (wave == 0) {
+    const int b0 = last_at_most_wave(p.N, t0, [&](int i) { return (long long)p.cu[i]; });
+    if (lane < nt) {
+      const int t = t0 + lane;
+      int b = b0;
+      while (b + 1 < p.N && p.cu[b + 1] <= t) ++b;
+      const int begin = clamp_to(p.cu[b], p.total), end = clamp_to(p.cu[b + 1], p.total);
+      const long long pos = (p.starts ? max(p.starts[b], 0) : 0) + (long long)(t - begin);
+      page[lane] = t >= begin && t < end ? kv_page(c, b, pos / c.page_tokens) : -1;
+      slot[lane] = (int)(pos % c.page_tokens);
+    }
   }
   __syncthreads();
-  const int nk = c.H * c.dk / V, nv = c.H * c.dv / V;  // lanes of a token's keys, values
-  for (int i = tid; i < nt * (nk + nv); i += kThreads) {
-    const int t = i / (nk + nv), r = i % (nk + nv);
-    if (page[t] < 0) continue;
+  const int nk = c.H * c.dk / V, n = nk + c.H * c.dv / V;  // pieces of a token: of its keys, then of its values
+  int lanes = 64;                                          // of a wave for one token
+  while (lanes / 2 >= n) lanes /= 2;
+  const int step = kWaves * (64 / lanes);
+  for (int r = lane % lanes; r < n; r += lanes) {
     const bool is_v = r >= nk;
     const int d = is_v ? c.dv : c.dk, j = (is_v ? r - nk : r) * V, h = j / d;
-    const char* base = c.pool + (size_t)page[t] * c.page_bytes;
-    const char* from = base + (is_v ? kv_values(c, h) : kv_keys(c, h)) + ((size_t)slot[t] * d + j % d) * (E4 ? 1 : 2);
-    OUT* to = static_cast<OUT*>(is_v ? p.v_out : p.k_out) + (size_t)(t0 + t) * c.H * d + j;
-    if constexpr (E4) {
-      const float s = reinterpret_cast<const float*>(base + kv_scales(c))[(is_v ? c.H : 0) + h];
-      const u32x4 w = *reinterpret_cast<const u32x4*>(from);
+    const size_t at = (is_v ? kv_values(c, h) : kv_keys(c, h)) + (size_t)(j % d) * (E4 ? 1 : 2);
+    const size_t sat = kv_scales(c) + 4 * (size_t)((is_v ? c.H : 0) + h);
+    OUT* to = static_cast<OUT*>(is_v ? p.v_out : p.k_out) + (size_t)t0 * c.H * d + j;
+    for (int t1 = wave * (64 / lanes) + lane / lanes; t1 < nt; t1 += NB * step) {
+      u32x4 w[NB];
+      float s[NB];
+      bool there[NB];
 #pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        const f32x4 lo = from_e4m3x4(w[e]) * s, hi = from_e4m3x4(w[e + 1]) * s;
-        store8(to + 4 * e, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      for (int i = 0; i < NB; ++i) {
+        const int t = t1 + i * step;
+        there[i] = t < nt && page[min(t, nt - 1)] >= 0;
+        if (there[i]) {
+          const char* base = c.pool + (size_t)page[t] * c.page_bytes;
+          w[i] = *reinterpret_cast<const u32x4*>(base + at + (size_t)slot[t] * d * (E4 ? 1 : 2));
+          if constexpr (E4) s[i] = *reinterpret_cast<const float*>(base + sat);
+        }
       }
-    } else {
-      store8(to, load8(reinterpret_cast<const __bf16*>(from)));
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        if (!there[i]) continue;
+        OUT* y = to + (size_t)(t1 + i * step) * c.H * d;
+        if constexpr (E4) {
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const f32x4 lo = from_e4m3x4(w[i][e]) * s[i], hi = from_e4m3x4(w[i][e + 1]) * s[i];
+            store8(y + 4 * e, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+          }
+        } else {
+          Raw<__bf16> x;
+          x.w[0] = w[i];
+          store8(y, x.values());
+        }
+      }
     }
   }
 }
