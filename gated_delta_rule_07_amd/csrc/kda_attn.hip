@@ -53,129 +53,194 @@ __device__ __forceinline__ bool part_of(const AttnParams& p, int tile, Part& s) 
 }
 
 // ---- every type and head size: fp32 matrix cores -------------------------------------------
+// The fp32 matrix cores are slow enough for the operands to come straight from the caches into registers: a
+// workgroup takes 16 queries, each of its waves every fourth tile of 32 keys, and they are joined at the end.  So a
+// few queries behind a long prefix already fill many waves.
+//   S^T = K Q^T: a lane holds 8 of every 32 values of a key's row;
+//   O^T = V^T P^T: a lane holds DV / 16 neighbouring channels of 8 keys, and tile t of the output is the t-th of them.
 
-constexpr int kRows = 64, kKeys = 32, kPad = 4;
+constexpr int kRows = 16, kKeys = 32, kPlainWaves = 4;
+
+// n neighbouring values as fp32.
+template <int N>
+__device__ __forceinline__ void load_values(const float* p, float* r) {
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(p + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[i + e] = x[e];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = p[i];
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_values(const __bf16* p, float* r) {
+  typedef __bf16 vec __attribute__((ext_vector_type(N > 1 ? N : 2)));
+  if constexpr (N > 1) {
+    const vec x = *reinterpret_cast<const vec*>(p);
+#pragma unroll
+    for (int e = 0; e < N; ++e) r[e] = (float)x[e];
+  } else {
+    r[0] = (float)p[0];
+  }
+}
 
 template <typename IO, int DK, int DV>
-__global__ __launch_bounds__(256) void kda_attn_plain_kernel(AttnParams p) {
-  __shared__ __attribute__((aligned(16))) float sk[kKeys][DK + kPad];
-  __shared__ __attribute__((aligned(16))) float sv[DV][kKeys + kPad];  // transposed
-  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, c = lane % 16, g = lane / 16;
+__global__ __launch_bounds__(64 * kPlainWaves, 2) void kda_attn_plain_kernel(AttnParams p) {
+  constexpr int NS = (DK + 31) / 32, NT = DV / 16;
+  __shared__ __attribute__((aligned(16))) float so[kPlainWaves][kRows][DV + 4];
+  __shared__ float sm[kPlainWaves][kRows], sl[kPlainWaves][kRows];
+  const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), c = lane % 16, g = lane / 16;
   const int h = blockIdx.y, hk = h / (p.Hq / p.Hk);
   Part s;
   if (!part_of<kRows>(p, blockIdx.x, s)) return;
-  const int row = s.r0 + 16 * wave + c;  // this lane's query
-  // queries as B operands: values 32 step + 8 g + e
-  constexpr int NS = (DK + 31) / 32;
-  Frag<float> q[NS];
+  const int row = s.r0 + c;  // this lane's query
+  Frag<float> q[NS];         // as a B operand: values 32 step + 8 g + e
 #pragma unroll
   for (int st = 0; st < NS; ++st) {
     q[st].zero();
     const int i0 = 32 * st + 8 * g;
-    if (row < s.nq && i0 < DK) {
-      const IO* x = static_cast<const IO*>(p.q) + (size_t)(s.q0 + row) * p.q_stride + (size_t)h * DK + i0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q[st].v[e] = to_f32(x[e]);
-    }
+    if (row < s.nq && i0 < DK)
+      load_values<8>(static_cast<const IO*>(p.q) + (size_t)(s.q0 + row) * p.q_stride + (size_t)h * DK + i0, q[st].v);
   }
   const int shift = s.nk - s.nq;
-  const int limit = row < s.nq ? row + shift + 1 : 0;              // this query's keys
-  const int last = min(s.r0 + kRows, s.nq) + shift;                // the workgroup's
-  const int wfirst = s.r0 + 16 * wave + shift + 1;                 // the least of the wave's rows
+  const int limit = row < s.nq ? row + shift + 1 : 0;  // this query's keys
+  const int last = min(s.r0 + kRows, s.nq) + shift;    // the workgroup's
+  const int least = s.r0 + shift + 1;                  // what all of its queries see
   const float scale = p.scale * kLog2e;
-  constexpr int NT = DV / 16;
   f32x4 o[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) o[t] = (f32x4)0.0f;
   float m = -__builtin_inff(), l = 0.0f;
-  for (int k0 = 0; k0 < last; k0 += kKeys) {
-    __syncthreads();
-    for (int i = tid; i < kKeys * DK; i += 256) {
-      const int r = i / DK, e = i % DK;
-      sk[r][e] = k0 + r < s.nk ? to_f32(static_cast<const IO*>(p.k)[(size_t)(s.k0 + k0 + r) * p.k_stride + (size_t)hk * DK + e]) : 0.0f;
+
+  const IO* kg = static_cast<const IO*>(p.k) + (size_t)s.k0 * p.k_stride + (size_t)hk * DK;
+  const IO* vg = static_cast<const IO*>(p.v) + (size_t)s.k0 * p.v_stride + (size_t)hk * DV;
+  Frag<float> k[2][NS];
+  float v[8][NT];
+  // (rows behind the last key: that one again)
+  auto keys = [&](int k0) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const IO* x = kg + (size_t)min(k0 + 16 * u + c, s.nk - 1) * p.k_stride;
+#pragma unroll
+      for (int st = 0; st < NS; ++st) {
+        const int i0 = 32 * st + 8 * g;
+        if (DK % 32 == 0 || i0 < DK) load_values<8>(x + i0, k[u][st].v);
+        else k[u][st].zero();
+      }
     }
-    for (int i = tid; i < kKeys * DV; i += 256) {
-      const int r = i / DV, e = i % DV;
-      sv[e][r] = k0 + r < s.nk ? to_f32(static_cast<const IO*>(p.v)[(size_t)(s.k0 + k0 + r) * p.v_stride + (size_t)hk * DV + e]) : 0.0f;
-    }
-    __syncthreads();
+  };
+  auto values = [&](int k0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      load_values<NT>(vg + (size_t)min(k0 + 16 * (e / 4) + 4 * g + e % 4, s.nk - 1) * p.v_stride + NT * c, v[e]);
+  };
+
+  int k0 = wave * kKeys;
+  if (k0 < last) keys(k0), values(k0);
+  for (; k0 < last; k0 += kPlainWaves * kKeys) {
+    const int next = k0 + kPlainWaves * kKeys;
     f32x4 x[2] = {(f32x4)0.0f, (f32x4)0.0f};  // S^T of keys 0..15 and 16..31
 #pragma unroll
-    for (int st = 0; st < NS; ++st) {
+    for (int st = 0; st < NS; ++st)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-        x[u] = mma(lds_frag<float>(&sk[0][0], DK + kPad, 16 * u + c, 32 * st + 8 * g, DK), q[st], x[u]);
-    }
+      for (int u = 0; u < 2; ++u) x[u] = mma(k[u][st], q[st], x[u]);
+    if (next < last) keys(next);
+    const bool partial = k0 + kKeys > least;
     float top = -__builtin_inff();
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        x[u][r] = k0 + 16 * u + 4 * g + r < limit ? x[u][r] * scale : -__builtin_inff();
+        x[u][r] *= scale;
+        if (partial && k0 + 16 * u + 4 * g + r >= limit) x[u][r] = -__builtin_inff();
         top = fmaxf(top, x[u][r]);
       }
     }
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
     const float now = fmaxf(m, top), base = now == -__builtin_inff() ? 0.0f : now;
-    const float keep = exp2f(m - base);
+    const float keep = __builtin_amdgcn_exp2f(m - base);
     m = now;
     l *= keep;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        x[u][r] = exp2f(x[u][r] - base);
+        x[u][r] = __builtin_amdgcn_exp2f(x[u][r] - base);
         l += x[u][r];
       }
     }
     const Frag<float> pt = frag_from_tiles<float>(x[0], x[1], 1.0f);
-    // Where some of the wave's queries do not see all of the tile, values that are not finite must not reach
-    // them as 0 v: each query's keys are then taken by themselves.
-    bool odd = false;
-    if (wfirst < k0 + kKeys) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) o[t] *= keep;
+    if (!partial) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const Frag<float> a = lds_frag_stacked<float>(&sv[0][0], kKeys + kPad, 16 * t + c, 0, g, kKeys);
+        Frag<float> a;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) odd = odd || !(__builtin_fabsf(a.v[e]) < __builtin_inff());
-      }
-    }
-    const bool slow = __any(odd);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      o[t] *= keep;
-      Frag<float> a = lds_frag_stacked<float>(&sv[0][0], kKeys + kPad, 16 * t + c, 0, g, kKeys);
-      if (!slow) {
+        for (int e = 0; e < 8; ++e) a.v[e] = v[e][t];
         o[t] = mma(a, pt, o[t]);
-      } else {
-        for (int r = 0; r < 16; ++r) {
-          const int lim = __shfl(limit, r);
-          Frag<float> b = a;
+      }
+    } else {
+      // What no query sees is left out.  Values that are not finite must not reach, as 0 v, queries that do not see them:
+      // they are left out too, and counted for each query that does see them: its outputs become NaN.
+      Frag<float> see;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) b.v[e] = k0 + (e / 4) * 16 + 4 * g + e % 4 < lim ? a.v[e] : 0.0f;
-          const f32x4 y = mma(b, pt, (f32x4)0.0f);
-          if (c == r) o[t] += y;
+      for (int e = 0; e < 8; ++e) see.v[e] = k0 + 16 * (e / 4) + 4 * g + e % 4 < limit ? 1.0f : 0.0f;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        Frag<float> a, n;
+        bool odd = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const bool there = k0 + 16 * (e / 4) + 4 * g + e % 4 < last, fine = __builtin_fabsf(v[e][t]) < __builtin_inff();
+          a.v[e] = there & fine ? v[e][t] : 0.0f;
+          n.v[e] = there & !fine ? 1.0f : 0.0f;
+          odd |= there & !fine;
+        }
+        o[t] = mma(a, pt, o[t]);
+        if (__builtin_expect(__any(odd), 0)) {
+          const f32x4 y = mma(n, see, (f32x4)0.0f);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[t][r] = y[r] > 0.0f ? __builtin_nanf("") : o[t][r];
         }
       }
     }
+    if (next < last) values(next);
   }
+
+  // join the waves
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
-  if (row >= s.nq) return;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const size_t at = (size_t)(s.q0 + row) * p.o_stride + (size_t)h * DV + 4 * g;
+  if (g == 0) sm[wave][c] = m, sl[wave][c] = l;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const f32x4 y = o[t] * inv;
-    if (p.o_f32) {
-      *reinterpret_cast<f32x4*>(static_cast<float*>(p.o) + at + 16 * t) = y;
-    } else {
-      bf16x4 z;
+  for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) z[r] = (__bf16)y[r];
-      *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(p.o) + at + 16 * t) = z;
+    for (int t = 0; t < NT; ++t) so[wave][c][NT * (4 * g + r) + t] = o[t][r];
+  __syncthreads();
+  for (int i = tid; i < kRows * DV / 4; i += 64 * kPlainWaves) {
+    const int r = i / (DV / 4), e = 4 * (i % (DV / 4));
+    if (s.r0 + r >= s.nq) break;
+    float top = sm[0][r];
+#pragma unroll
+    for (int w = 1; w < kPlainWaves; ++w) top = fmaxf(top, sm[w][r]);
+    const float base = top == -__builtin_inff() ? 0.0f : top;
+    f32x4 y = (f32x4)0.0f;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kPlainWaves; ++w) {
+      const float f = __builtin_amdgcn_exp2f(sm[w][r] - base);
+      sum += f * sl[w][r];
+      y += f * *reinterpret_cast<const f32x4*>(&so[w][r][e]);
     }
+    y *= sum == 0.0f ? 0.0f : 1.0f / sum;
+    const size_t at = (size_t)(s.q0 + s.r0 + r) * p.o_stride + (size_t)h * DV + e;
+    if (p.o_f32) *reinterpret_cast<f32x4*>(static_cast<float*>(p.o) + at) = y;
+    else *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(p.o) + at) = bf16x4{(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
   }
 }
 
@@ -348,7 +413,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int 
         }
         bad[e] = (unsigned char)bits;
         if (bits) *reinterpret_cast<u32x4*>(vl + 16 * e) = y;
-        found = found || bits;
+        found |= bits != 0;
       }
       const bool any = __any(found);
       if (lane == 0) some[wave] = any;
@@ -483,7 +548,7 @@ hipError_t launch_fast(const AttnParams& p, hipStream_t s) {
 
 template <typename IO, int DK, int DV>
 hipError_t launch_plain(const AttnParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((kda_attn_plain_kernel<IO, DK, DV>), dim3(tiles_of<kRows>(p), p.Hq), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((kda_attn_plain_kernel<IO, DK, DV>), dim3(tiles_of<kRows>(p), p.Hq), dim3(64 * kPlainWaves), 0, s, p);
   return hipGetLastError();
 }
 

@@ -359,7 +359,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_decode_kernel(DecodePlan 
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
-          for (int i = 0; i < T::VW; ++i) odd = odd || not_finite<E4>(cur.v[j][i]) != 0;
+          for (int i = 0; i < T::VW; ++i) odd |= not_finite<E4>(cur.v[j][i]) != 0;
         if (__builtin_expect(__any(odd), 0)) {
           bf16x8 see;
 #pragma unroll
