@@ -52,6 +52,12 @@ __device__ __forceinline__ bool part_of(const AttnParams& p, int tile, Part& s) 
   return j >= 0 && s.nq > 0 && j < tiles;
 }
 
+// Four outputs from element `at` of o on.
+__device__ __forceinline__ void store4(const AttnParams& p, size_t at, const f32x4& y) {
+  if (p.o_f32) *reinterpret_cast<f32x4*>(static_cast<float*>(p.o) + at) = y;
+  else *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(p.o) + at) = bf16x4{(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
+}
+
 // ---- every type and head size: fp32 matrix cores -------------------------------------------
 // The fp32 matrix cores are slow enough for the operands to come straight from the caches into registers: a
 // workgroup takes 16 queries, each of its waves every fourth tile of 32 keys, and they are joined at the end.  So a
@@ -237,10 +243,7 @@ __global__ __launch_bounds__(64 * kPlainWaves, 2) void kda_attn_plain_kernel(Att
       sum += f * sl[w][r];
       y += f * *reinterpret_cast<const f32x4*>(&so[w][r][e]);
     }
-    y *= sum == 0.0f ? 0.0f : 1.0f / sum;
-    const size_t at = (size_t)(s.q0 + s.r0 + r) * p.o_stride + (size_t)h * DV + e;
-    if (p.o_f32) *reinterpret_cast<f32x4*>(static_cast<float*>(p.o) + at) = y;
-    else *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(p.o) + at) = bf16x4{(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
+    store4(p, (size_t)(s.q0 + s.r0 + r) * p.o_stride + (size_t)h * DV + e, y * (sum == 0.0f ? 0.0f : 1.0f / sum));
   }
 }
 
@@ -291,6 +294,34 @@ template <int D>
 __device__ __forceinline__ int key_piece(int r, int c) { return D == 128 ? c ^ (r & 15) : c ^ ((r >> 1) & 7); }
 template <int D>
 __device__ __forceinline__ int value_piece(int r, int c) { return D == 128 ? c ^ (4 * (r & 3)) : c ^ (4 * ((r >> 1) & 1)); }
+
+// V^T as an operand: channels [32 i, 32 i + 32) of keys [16 st, 16 st + 16); slot e of half hf is key 8 (e / 4) + 4 hf + e % 4.
+template <int DV>
+__device__ __forceinline__ bf16x8 value_operand(char* vl, int i, int st, int lane) {
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  typedef short s16x8 __attribute__((ext_vector_type(8)));
+  s16x4 y[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int r = 16 * st + 8 * j + 4 * (lane / 32) + lane % 16 / 4;
+    const int cc = 4 * i + 2 * (lane / 16 % 2) + lane % 4 / 2;
+    y[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vl + r * (2 * DV) + 16 * value_piece<DV>(r, cc) + 8 * (lane % 2)));
+  }
+  return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(y[0], y[1], 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// The operands that count the values noted in `bad` (n) for the queries that see them (see); seen: the lane's query's keys of the tile.
+template <int DV>
+__device__ __forceinline__ void counted(const unsigned char* bad, int i, int st, int lane, int seen, bf16x8& n, bf16x8& see) {
+  const int c = lane % 32;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int r = 16 * st + 8 * (e / 4) + 4 * (lane / 32) + e % 4;
+    const unsigned bits = bad[r * (DV / 8) + value_piece<DV>(r, 4 * i + c / 8)];
+    n[e] = (__bf16)(float)(bits >> c % 8 & 1);
+    see[e] = (__bf16)(r < seen ? 1.0f : 0.0f);
+  }
+}
 
 template <int NW, int DK, int DV>
 struct FastCfg {
@@ -408,7 +439,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const bool lo = (y[j] & 0x7f80u) == 0x7f80u, hi = (y[j] & 0x7f800000u) == 0x7f800000u;
-          bits |= (uint32_t)lo << 2 * j | (uint32_t)hi << 2 * j + 1;
+          bits |= (uint32_t)lo << 2 * j | (uint32_t)hi << (2 * j + 1);
           y[j] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
         }
         bad[e] = (unsigned char)bits;
@@ -466,23 +497,10 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int 
 #pragma unroll
       for (int e = 0; e < 8; e += 2) l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{pt[st][e], pt[st][e + 1]}, ones, l, false);
     }
-    // V^T operand of channels [32 i, 32 i + 32), keys [16 st, 16 st + 16): slot e of half hf is key 8 (e / 4) + 4 hf + e % 4
 #pragma unroll
     for (int st = 0; st < 4; ++st)
 #pragma unroll
-      for (int i = 0; i < DV / 32; ++i) {
-        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-        typedef short s16x8 __attribute__((ext_vector_type(8)));
-        s16x4 y[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = 16 * st + 8 * j + 4 * hf + lane % 16 / 4;
-          const int cc = 4 * i + 2 * (lane / 16 % 2) + lane % 4 / 2;
-          y[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vl + r * (2 * DV) + 16 * value_piece<DV>(r, cc) + 8 * (lane % 2)));
-        }
-        const bf16x8 a = __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(y[0], y[1], 0, 1, 2, 3, 4, 5, 6, 7));
-        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, pt[st], o[i], 0, 0, 0);
-      }
+      for (int i = 0; i < DV / 32; ++i) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(value_operand<DV>(vl, i, st, lane), pt[st], o[i], 0, 0, 0);
     if (__builtin_expect(odd, 0)) {  // outputs of queries that see a value that is not finite: NaN.  The values are counted by a product.
 #pragma unroll
       for (int i = 0; i < DV / 32; ++i) {
@@ -490,13 +508,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int 
 #pragma unroll 1
         for (int st = 0; st < 4; ++st) {
           bf16x8 n, see;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int r = 16 * st + 8 * (e / 4) + 4 * hf + e % 4;
-            const unsigned bits = bad[r * (DV / 8) + value_piece<DV>(r, 4 * i + c / 8)];
-            n[e] = (__bf16)(float)(bits >> c % 8 & 1);
-            see[e] = (__bf16)(k0 + r < limit ? 1.0f : 0.0f);
-          }
+          counted<DV>(bad, i, st, lane, limit - k0, n, see);
           y = __builtin_amdgcn_mfma_f32_32x32x16_bf16(n, see, y, 0, 0, 0);
         }
 #pragma unroll
@@ -534,13 +546,203 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int 
   }
 }
 
+// ---- the same for few queries ---------------------------------------------------------------
+// Where the workgroups above would not fill the compute units -- a short prompt, or a few new tokens behind a long
+// prefix -- a workgroup takes 32 queries, and each of its four waves every fourth tile of 32 keys, through two
+// buffers of its own in LDS: no barrier until the waves are joined.
+
+constexpr int kSplitWaves = 4, kSplitKeys = 32;
+constexpr unsigned kFewTiles = 256;  // workgroups of it that the card's compute units hold at once
+
+template <int DK, int DV>
+__global__ __launch_bounds__(64 * kSplitWaves, 1) void kda_attn_split_kernel(AttnParams p) {
+  constexpr int KB = kSplitKeys * DK * 2, VB = kSplitKeys * DV * 2, NK = KB / 1024, NV = VB / 1024;
+  constexpr int RING = 2 * (KB + VB), JOIN = 32 * (DV + 4) * 4;  // bytes of a wave
+  __shared__ __attribute__((aligned(1024))) char lds[kSplitWaves * (RING > JOIN ? RING : JOIN)];
+  __shared__ unsigned char bads[kSplitWaves][VB / 16];
+  __shared__ float sm[kSplitWaves][32], sl[kSplitWaves][32];
+  const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), c = lane % 32, hf = lane / 32;
+  const int h = blockIdx.y, hk = h / (p.Hq / p.Hk);
+  Part s;
+  if (!part_of<32>(p, blockIdx.x, s)) return;
+  const int row = s.r0 + c, shift = s.nk - s.nq;
+  const int limit = row < s.nq ? row + shift + 1 : 0;  // this lane's query's keys
+  const int last = min(s.r0 + 32, s.nq) + shift;       // the workgroup's
+  const int least = s.r0 + shift + 1;                  // what all of its queries see
+  const int ntiles = (last + kSplitKeys - 1) / kSplitKeys;
+  char* ring = lds + wave * RING;
+  unsigned char* bad = bads[wave];
+
+  const char* kg = reinterpret_cast<const char*>(static_cast<const __bf16*>(p.k) + (size_t)s.k0 * p.k_stride + (size_t)hk * DK);
+  const char* vg = reinterpret_cast<const char*>(static_cast<const __bf16*>(p.v) + (size_t)s.k0 * p.v_stride + (size_t)hk * DV);
+  const uint32_t krow = (uint32_t)(2 * p.k_stride), vrow = (uint32_t)(2 * p.v_stride);
+  auto copy = [&](int t, int buf) {
+    const char* kt = kg + (size_t)t * kSplitKeys * krow;
+    const char* vt = vg + (size_t)t * kSplitKeys * vrow;
+    const int most = s.nk - 1 - t * kSplitKeys;  // (rows behind the last key: that one again)
+    char* to = ring + buf * (KB + VB);
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const int e = i * 64 + lane, r = e / (DK / 8);
+      copy16(kt, (uint32_t)min(r, most) * krow + 16 * key_piece<DK>(r, e % (DK / 8)), to + i * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = i * 64 + lane, r = e / (DV / 8);
+      copy16(vt, (uint32_t)min(r, most) * vrow + 16 * value_piece<DV>(r, e % (DV / 8)), to + KB + i * 1024);
+    }
+  };
+  if (wave < ntiles) copy(wave, 0);
+  bf16x8 q[DK / 16];
+  const __bf16* qx = static_cast<const __bf16*>(p.q) + (size_t)(s.q0 + min(row, s.nq - 1)) * p.q_stride + (size_t)h * DK + 8 * hf;
+#pragma unroll
+  for (int st = 0; st < DK / 16; ++st) q[st] = *reinterpret_cast<const bf16x8*>(qx + 16 * st);
+  if (p.scale < 0.0f) {  // (so that the largest score has the largest product)
+#pragma unroll
+    for (int st = 0; st < DK / 16; ++st) q[st] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, q[st]) ^ 0x80008000u);
+  }
+#pragma unroll
+  for (int st = 0; st < DK / 16; ++st) asm volatile("" : "+v"(q[st]));  // (waited for here, not inside the loop)
+  const float scale = fmaxf(__builtin_fabsf(p.scale) * kLog2e, 1e-30f);
+  const bf16x2 ones = {(__bf16)1.0f, (__bf16)1.0f};
+  f32x16 o[DV / 32];
+#pragma unroll
+  for (int t = 0; t < DV / 32; ++t) o[t] = (f32x16)0.0f;
+  float m = -__builtin_inff(), l = 0.0f;
+  int buf = 0;
+  for (int t = wave; t < ntiles; t += kSplitWaves, buf ^= 1) {
+    // the reads of the buffer that is filled next are done; then this tile's copies have landed
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (t + kSplitWaves < ntiles) {
+      copy(t + kSplitWaves, buf ^ 1);
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NK + NV) : "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    const int k0 = t * kSplitKeys;
+    const char* kl = ring + buf * (KB + VB);
+    char* vl = ring + buf * (KB + VB) + KB;
+    const int rel = limit - k0 - 4 * hf;
+    const bool cut = k0 + kSplitKeys > least;
+    bool odd = false;
+    if (cut) {  // as above: values that are not finite are taken out and noted
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int e = i * 64 + lane;
+        u32x4 y = *reinterpret_cast<const u32x4*>(vl + 16 * e);
+        uint32_t bits = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool lo = (y[j] & 0x7f80u) == 0x7f80u, hi = (y[j] & 0x7f800000u) == 0x7f800000u;
+          bits |= (uint32_t)lo << 2 * j | (uint32_t)hi << (2 * j + 1);
+          y[j] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
+        }
+        bad[e] = (unsigned char)bits;
+        if (bits) *reinterpret_cast<u32x4*>(vl + 16 * e) = y;
+        found |= bits != 0;
+      }
+      odd = __any(found);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+    f32x16 x = (f32x16)0.0f;
+#pragma unroll
+    for (int st = 0; st < DK / 16; ++st) {
+      const bf16x8 a = *reinterpret_cast<const bf16x8*>(kl + c * (2 * DK) + 16 * key_piece<DK>(c, 2 * st + hf));
+      x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[st], x, 0, 0, 0);
+    }
+    if (cut) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) x[r] = 8 * (r / 4) + r % 4 >= rel ? -__builtin_inff() : x[r];
+    }
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int r = 0; r < 16; ++r) top = fmaxf(top, x[r]);
+    top = half_max(top) * scale;
+    if (__any(top > m + kSlack)) {
+      const float now = fmaxf(m, top);
+      const float keep = now == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - now);
+      m = now;
+      l *= keep;
+#pragma unroll
+      for (int i = 0; i < DV / 32; ++i) o[i] *= keep;
+    }
+    const float base = m == -__builtin_inff() ? 0.0f : -m;
+    bf16x8 pt[2];
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) pt[st][e] = (__bf16)__builtin_amdgcn_exp2f(__builtin_fmaf(x[8 * st + e], scale, base));
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{pt[st][e], pt[st][e + 1]}, ones, l, false);
+    }
+#pragma unroll
+    for (int st = 0; st < 2; ++st)
+#pragma unroll
+      for (int i = 0; i < DV / 32; ++i) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(value_operand<DV>(vl, i, st, lane), pt[st], o[i], 0, 0, 0);
+    if (__builtin_expect(odd, 0)) {
+#pragma unroll
+      for (int i = 0; i < DV / 32; ++i) {
+        f32x16 y = (f32x16)0.0f;
+#pragma unroll 1
+        for (int st = 0; st < 2; ++st) {
+          bf16x8 n, see;
+          counted<DV>(bad, i, st, lane, limit - k0, n, see);
+          y = __builtin_amdgcn_mfma_f32_32x32x16_bf16(n, see, y, 0, 0, 0);
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[i][r] = y[r] > 0.0f ? __builtin_nanf("") : o[i][r];
+      }
+    }
+  }
+
+  // join the waves, in the memory of the tiles
+  l += __shfl_xor(l, 32);
+  __syncthreads();
+  float* so = reinterpret_cast<float*>(lds);
+  if (hf == 0) sm[wave][c] = m, sl[wave][c] = l;
+#pragma unroll
+  for (int i = 0; i < DV / 32; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      *reinterpret_cast<f32x4*>(so + (wave * 32 + c) * (DV + 4) + 32 * i + 8 * r + 4 * hf) =
+          f32x4{o[i][4 * r], o[i][4 * r + 1], o[i][4 * r + 2], o[i][4 * r + 3]};
+  __syncthreads();
+  for (int i = tid; i < 32 * DV / 4; i += 64 * kSplitWaves) {
+    const int r = i / (DV / 4), e = 4 * (i % (DV / 4));
+    if (s.r0 + r >= s.nq) break;
+    float top = sm[0][r];
+#pragma unroll
+    for (int w = 1; w < kSplitWaves; ++w) top = fmaxf(top, sm[w][r]);
+    const float base = top == -__builtin_inff() ? 0.0f : top;
+    f32x4 y = (f32x4)0.0f;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kSplitWaves; ++w) {
+      const float f = __builtin_amdgcn_exp2f(sm[w][r] - base);
+      sum += f * sl[w][r];
+      y += f * *reinterpret_cast<const f32x4*>(so + (w * 32 + r) * (DV + 4) + e);
+    }
+    store4(p, (size_t)(s.q0 + s.r0 + r) * p.o_stride + (size_t)h * DV + e, y * (sum == 0.0f ? 0.0f : 1.0f / sum));
+  }
+}
+
 template <int BM>
 unsigned tiles_of(const AttnParams& p) {
   return p.cu_q ? (unsigned)(p.total_q / BM + p.N) : (unsigned)((p.total_q / p.N + BM - 1) / BM * p.N);
 }
 
-template <int NW, int DK, int DV>
+template <int DK, int DV>
 hipError_t launch_fast(const AttnParams& p, hipStream_t s) {
+  constexpr int NW = 4;
+  // Waves that share the keys against waves that share the queries, us, heads of 128: 1,000 tokens of 8 heads (256 workgroups
+  // of the first kind) 14.2 / 24.4, 2,000 (504) 38 / 43, 4,000 95 / 78; 300 tokens of 32 heads (320) 15.3 / 11.1; behind 32,000
+  // cached ones 128 tokens of 32 heads (128) 262 / 577, 512 (512) 663 / 582.
+  const unsigned few = tiles_of<32>(p);
+  if ((unsigned long long)few * p.Hq <= kFewTiles) {
+    hipLaunchKernelGGL((kda_attn_split_kernel<DK, DV>), dim3(few, p.Hq), dim3(64 * kSplitWaves), 0, s, p);
+    return hipGetLastError();
+  }
   const unsigned tiles = tiles_of<32 * NW>(p), chunk = (tiles * p.Hq + 7) / 8;
   hipLaunchKernelGGL((kda_attn_kernel<NW, DK, DV>), dim3(8 * chunk), dim3(64 * NW), 0, s, p, (int)tiles, chunk);
   return hipGetLastError();
@@ -580,8 +782,8 @@ hipError_t launch_attn_fwd(const AttnParams& p, int io_dtype, hipStream_t s) {
   if (p.total_q < 1 || p.N < 1) return hipErrorInvalidValue;
   // (64 rows of keys or values have to lie within 2^31 bytes)
   if (io_dtype == 1 && p.dk % 64 == 0 && p.dv % 64 == 0 && std::max(p.k_stride, p.v_stride) < (1LL << 24)) {
-    if (p.dk == 128) return p.dv == 128 ? launch_fast<4, 128, 128>(p, s) : launch_fast<4, 128, 64>(p, s);
-    return p.dv == 128 ? launch_fast<4, 64, 128>(p, s) : launch_fast<4, 64, 64>(p, s);
+    if (p.dk == 128) return p.dv == 128 ? launch_fast<128, 128>(p, s) : launch_fast<128, 64>(p, s);
+    return p.dv == 128 ? launch_fast<64, 128>(p, s) : launch_fast<64, 64>(p, s);
   }
   return io_dtype == 1 ? pick_dk<__bf16>(p, s) : pick_dk<float>(p, s);
 }
