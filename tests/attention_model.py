@@ -1,4 +1,4 @@
-"""Plain models of the attention layers' calls, for the tests: 64-bit arithmetic on the host, sharing nothing with the
+"""Plain models of the attention layers' calls, for the tests: 64-bit arithmetic (where its inputs lie), sharing nothing with the
 library, with bounds on what the calls' arithmetic may differ by."""
 from __future__ import annotations
 
@@ -22,24 +22,28 @@ def attend(q, k, v, seen, scale, p_half):
     q, k, v = q.double(), k.double(), v.double()
     n, m, d = q.shape[0], k.shape[0], q.shape[1]
     if m == 0:
-        return torch.zeros(n, v.shape[1], dtype=torch.float64), torch.zeros(n, v.shape[1], dtype=torch.float64)
-    there = torch.arange(m) < torch.as_tensor(seen)[:, None]
+        return q.new_zeros(n, v.shape[1]), q.new_zeros(n, v.shape[1])
+    there = torch.arange(m, device=q.device) < torch.as_tensor(seen, device=q.device)[:, None]
     s = (q @ k.T) * scale
     s = torch.where(there, s, -math.inf)
     p = torch.softmax(s, -1)
     p = torch.where(there, p, 0.0)  # (rows that see nothing)
     used = there.any(0)  # (what nobody sees may be anything)
     k, v, p, s, there = k[used], v[used], p[:, used], s[:, used], there[:, used]
-    o = torch.stack([(p[:, :, None] * torch.where(there[:, :, None], v[None, :, c:c + 1], 0.0)).sum(1)[:, 0] for c in range(v.shape[1])], 1)
+    if torch.isfinite(v).all():
+        o = p @ v
+    else:  # (0 times what a row does not see could be NaN)
+        o = torch.stack([(p[:, :, None] * torch.where(there[:, :, None], v[None, :, c:c + 1], 0.0)).sum(1)[:, 0] for c in range(v.shape[1])], 1)
     size = torch.where(there, (q.abs() @ k.abs().T) * abs(scale), 0.0)
-    e = (2 * (d + 2) + 6) * U * size.amax(1) + 4 * U * torch.where(there, s.abs(), 0.0).amax(1) if there.shape[1] else torch.zeros(n)
+    e = (2 * (d + 2) + 6) * U * size.amax(1) + 4 * U * torch.where(there, s.abs(), 0.0).amax(1) if there.shape[1] else q.new_zeros(n)
     va = torch.where(torch.isfinite(v), v, 0.0).abs()
     return o, (2 * (e + 2 * U) + p_half + 4 * m * U + 2 * U)[:, None] * (p @ va)
 
 
 def close(got, ref, slack, what=""):
     """got is the rounding (of its type) of a value within slack of ref; NaN passes only where ref is not finite."""
-    g, fine = got.double().cpu(), torch.isfinite(ref)
+    ref, slack = ref.to(got.device), slack.to(got.device)
+    g, fine = got.double(), torch.isfinite(ref)
     assert g.shape == ref.shape, f"{what}: shape {tuple(g.shape)}, not {tuple(ref.shape)}"
     assert bool((torch.isfinite(g) == fine).all()), f"{what}: {int((torch.isfinite(g) != fine).sum())} values finite, or not, by mistake"
     tol = slack + HALF[got.dtype] * (ref.abs() + slack) + 1e-37
@@ -51,14 +55,13 @@ def close(got, ref, slack, what=""):
 def fwd(q, k, v, scale, lens_q, lens_k=None):
     """(o, slack) of packed prompts: q [n][Hq][dk], k [m][Hk][dk], v [m][Hk][dv]."""
     lens_k = lens_q if lens_k is None else lens_k
-    q, k, v = (x.detach().cpu() for x in (q, k, v))
     G = q.shape[1] // k.shape[1]
-    o = torch.zeros(q.shape[0], q.shape[1], v.shape[2], dtype=torch.float64)
+    o = torch.zeros(q.shape[0], q.shape[1], v.shape[2], dtype=torch.float64, device=q.device)
     slack = torch.zeros_like(o)
     p_half = HALF[torch.bfloat16] if q.dtype == torch.bfloat16 else 0.0
     a = b = 0
     for n, m in zip(lens_q, lens_k):
-        seen = (torch.arange(n) + m - n + 1).clamp(min=0)
+        seen = (torch.arange(n, device=q.device) + m - n + 1).clamp(min=0)
         for h in range(q.shape[1]):
             o[a:a + n, h], slack[a:a + n, h] = attend(q[a:a + n, h], k[b:b + m, h // G], v[b:b + m, h // G], seen, scale, p_half)
         a, b = a + n, b + m

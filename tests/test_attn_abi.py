@@ -171,7 +171,7 @@ def test_attention_model():
     assert 0 < float(slack.max()) < 1e-3
     v[5:] = math.nan  # what a query does not see does not reach it
     o2, _ = am.fwd(q, k, v, 0.3, [7], [9])
-    assert torch.equal(o2[:3], o[:3]) and torch.isnan(o2[3:]).all()
+    assert float((o2[:3] - o[:3]).abs().max()) < 1e-14 and torch.isnan(o2[3:]).all()  # (sums of 5 products in another order)
     o3, _ = am.fwd(q, k[:2], v[:2], 0.3, [7], [2])
     assert not o3[:5].any() and o3[5:].any()
     with pytest.raises(AssertionError):

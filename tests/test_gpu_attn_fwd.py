@@ -47,11 +47,23 @@ def test_head_sizes(gpu, dtype, dk, dv):
     _check(q, k, v, [149], o_dtype=F)
 
 
+# Heads: few, so that the waves of a workgroup share the keys, and so many that even one row a sequence makes more workgroups
+# than the card holds at once, so that they share the queries.
+HEADS = [(4, 2), (258, 2)]
+
+
+@pytest.mark.parametrize("hq,hk", HEADS)
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300, 511, 513])
-def test_lengths(gpu, d, n):
-    q, k, v = _qkv(gpu, n, n, n, 2, 1, d, d, BF)
+def test_lengths(gpu, d, n, hq, hk):
+    q, k, v = _qkv(gpu, n, n, n, hq, hk, d, d, BF)
     _check(q, k, v, [n])
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 128), (128, 64)])
+def test_head_sizes_of_many_heads(gpu, dk, dv):
+    q, k, v = _qkv(gpu, dk, 200, 200, 258, 2, dk, dv, BF)
+    _check(q, k, v, [200], o_dtype=F)
 
 
 @pytest.mark.parametrize("dtype", [BF, F])
@@ -61,26 +73,26 @@ def test_groups(gpu, dtype, hq, hk):
     _check(q, k, v, [130])
 
 
-@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 128), (F, 64), (BF, 32)])
-def test_packed(gpu, dtype, d):
+@pytest.mark.parametrize("dtype,d,hq", [(BF, 64, 4), (BF, 128, 4), (F, 64, 4), (BF, 32, 4), (BF, 64, 12), (BF, 128, 12)])
+def test_packed(gpu, dtype, d, hq):
     lens = [1, 0, 300, 64, 0, 0, 7, 129, 256, 31, 1, 513, 0]
-    q, k, v = _qkv(gpu, 3, sum(lens), sum(lens), 4, 2, d, d, dtype)
+    q, k, v = _qkv(gpu, 3, sum(lens), sum(lens), hq, 2, d, d, dtype)
     _check(q, k, v, lens)
 
 
-@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 128), (F, 128)])
-def test_prefixes(gpu, dtype, d):
+@pytest.mark.parametrize("dtype,d,hq", [(BF, 64, 4), (BF, 128, 4), (F, 128, 4), (BF, 64, 24), (BF, 128, 24)])
+def test_prefixes(gpu, dtype, d, hq):
     """More keys than queries, as many, fewer (queries that see nothing give zeros), none."""
     lens, lens_k = [5, 130, 64, 9, 40, 17, 3, 0, 70], [300, 130, 65, 4, 0, 1000, 3, 50, 69]
-    q, k, v = _qkv(gpu, 4, sum(lens), sum(lens_k), 4, 2, d, d, dtype)
+    q, k, v = _qkv(gpu, 4, sum(lens), sum(lens_k), hq, 2, d, d, dtype)
     o = _check(q, k, v, lens, lens_k)
     a = sum(lens[:3])
     assert not o[a:a + 5].any() and o[a + 5:a + 9].any() and not o[a + 9:a + 49].any()
 
 
-@pytest.mark.parametrize("dtype", [BF, F])
-def test_long_keys(gpu, dtype):
-    q, k, v = _qkv(gpu, 5, 40, 5003, 2, 1, 128, 128, dtype)
+@pytest.mark.parametrize("dtype,hq", [(BF, 2), (F, 2), (BF, 140)])
+def test_long_keys(gpu, dtype, hq):
+    q, k, v = _qkv(gpu, 5, 40, 5003, hq, 1, 128, 128, dtype)
     _check(q, k, v, [40], [5003])
 
 
@@ -103,9 +115,9 @@ def test_strides(gpu, dtype, d):
 
 
 @pytest.mark.parametrize("scale", [0.0, 1.0, -0.3, 20.0])
-@pytest.mark.parametrize("dtype", [BF, F])
-def test_scales(gpu, dtype, scale):
-    q, k, v = _qkv(gpu, 7, 100, 100, 2, 2, 64, 64, dtype)
+@pytest.mark.parametrize("dtype,hq", [(BF, 2), (F, 2), (BF, 80)])
+def test_scales(gpu, dtype, hq, scale):
+    q, k, v = _qkv(gpu, 7, 100, 100, hq, 2, 64, 64, dtype)
     if scale == 20.0:  # (scores of hundreds: a softmax that picks one key)
         q, k = (x * 0.5 for x in (q, k))
     _check(q, k, v, [100], scale=scale)
@@ -129,14 +141,14 @@ def test_rows_outside_sequences_are_left(gpu):
     torch.cuda.synchronize()
 
 
-@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 128), (F, 64), (BF, 32)])
+@pytest.mark.parametrize("dtype,d,hq", [(BF, 64, 4), (BF, 128, 4), (F, 64, 4), (F, 128, 4), (BF, 32, 4), (BF, 64, 24), (BF, 128, 24)])
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
-def test_what_a_query_does_not_see_has_no_influence(gpu, dtype, d, bad):
+def test_what_a_query_does_not_see_has_no_influence(gpu, dtype, d, hq, bad):
     kda = _kda()
-    lens = [100, 70, 300]
-    q, k, v = _qkv(gpu, 9, 470, 470, 4, 2, d, d, dtype)
+    lens, G = [100, 70, 300], hq // 2
+    q, k, v = _qkv(gpu, 9, 470, 470, hq, 2, d, d, dtype)
     cu = _cu(lens, gpu)
-    clean = kda.kda_attn_fwd(q, k, v, cu_seqlens=cu)
+    clean, want = kda.kda_attn_fwd(q, k, v, cu_seqlens=cu), am.fwd(q, k, v, d ** -0.5, lens)
     for t in (99, 100, 135, 169, 170, 200, 469):
         for x in (k, v):
             y = x.clone()
@@ -146,21 +158,21 @@ def test_what_a_query_does_not_see_has_no_influence(gpu, dtype, d, bad):
             end = sum(lens[:b + 1])
             same = torch.ones(470, dtype=torch.bool, device=gpu)
             same[t:end] = False
-            assert torch.equal(o[:, :2], clean[:, :2]), "another head"
+            assert torch.equal(o[:, :G], clean[:, :G]), "another head"
             # (the rows of the tile that holds it may be summed in another order)
-            am.close(o[same], *(z[same.cpu()] for z in am.fwd(q, k, v, d ** -0.5, lens)), f"before token {t}")
+            am.close(o[same], *(z[same] for z in want), f"before token {t}")
             if x is v or bad != -math.inf:
-                assert not torch.isfinite(o[t:end, 2:]).all(-1).all() if x is k else not torch.isfinite(o[t:end, 2:]).any()
+                assert not torch.isfinite(o[t:end, G:]).all(-1).all() if x is k else not torch.isfinite(o[t:end, G:]).any()
 
 
 def test_nothing_but_minus_infinity(gpu):
     """A row all of whose scores are minus infinity gives zeros, as one that sees nothing."""
     kda = _kda()
-    for dtype in (BF, F):
-        q, k, v = torch.ones(3, 1, 64, device=gpu, dtype=dtype), torch.full((3, 1, 64), -math.inf, device=gpu, dtype=dtype), torch.ones(3, 1, 64, device=gpu, dtype=dtype)
+    for dtype, hq in ((BF, 1), (F, 1), (BF, 300)):
+        q, k, v = torch.ones(3, hq, 64, device=gpu, dtype=dtype), torch.full((3, 1, 64), -math.inf, device=gpu, dtype=dtype), torch.ones(3, 1, 64, device=gpu, dtype=dtype)
         assert not kda.kda_attn_fwd(q, k, v).any()
         k[2] = 1.0
-        assert kda.kda_attn_fwd(q, k, v)[:, 0, 0].tolist() == [0.0, 0.0, 1.0]
+        assert kda.kda_attn_fwd(q, k, v)[:, -1, 0].tolist() == [0.0, 0.0, 1.0]
 
 
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (F, 64)])
@@ -191,19 +203,21 @@ def test_far_rows(gpu):
     am.close(o[-200:], *am.fwd(q[-200:], k[-200:], v[-200:], d ** -0.5, [200]))
 
 
+@pytest.mark.parametrize("dtype,n,hq", [(BF, 2000, 8), (BF, 900, 8), (F, 900, 8)])
 @pytest.mark.parametrize("d", [64, 128])
-def test_repeats_are_bit_equal(gpu, d):
+def test_repeats_are_bit_equal(gpu, dtype, n, hq, d):
     kda = _kda()
-    q, k, v = _qkv(gpu, 12, 2000, 2000, 8, 2, d, d, BF)
+    q, k, v = _qkv(gpu, 12, n, n, hq, 2, d, d, dtype)
     a = kda.kda_attn_fwd(q, k, v)
     for _ in range(5):
         assert torch.equal(kda.kda_attn_fwd(q, k, v), a)
 
 
-def test_side_stream_and_graph(gpu):
+@pytest.mark.parametrize("dtype,hq", [(BF, 4), (BF, 40), (F, 4)])
+def test_side_stream_and_graph(gpu, dtype, hq):
     kda = _kda()
     lens = [70, 130, 3]
-    q, k, v = _qkv(gpu, 13, 203, 203, 4, 2, 128, 128, BF)
+    q, k, v = _qkv(gpu, 13, 203, 203, hq, 2, 128, 128, dtype)
     cu = _cu(lens, gpu)
     want = kda.kda_attn_fwd(q, k, v, cu_seqlens=cu)
     side = torch.cuda.Stream()
