@@ -310,17 +310,50 @@ __device__ __forceinline__ bf16x8 value_operand(char* vl, int i, int st, int lan
   return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(y[0], y[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// The operands that count the values noted in `bad` (n) for the queries that see them (see); seen: the lane's query's keys of the tile.
-template <int DV>
-__device__ __forceinline__ void counted(const unsigned char* bad, int i, int st, int lane, int seen, bf16x8& n, bf16x8& see) {
+// The operands that count the values noted in `bad` (n) for the queries that see them (see); seen: the lane's query's keys of the
+// tile; noted(e): whether the byte of piece e was written.
+template <int DV, typename F>
+__device__ __forceinline__ void counted(const unsigned char* bad, int i, int st, int lane, int seen, bf16x8& n, bf16x8& see, F noted) {
   const int c = lane % 32;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int r = 16 * st + 8 * (e / 4) + 4 * (lane / 32) + e % 4;
-    const unsigned bits = bad[r * (DV / 8) + value_piece<DV>(r, 4 * i + c / 8)];
+    const int piece = r * (DV / 8) + value_piece<DV>(r, 4 * i + c / 8);
+    const unsigned bits = noted(piece) ? bad[piece] : 0u;
     n[e] = (__bf16)(float)(bits >> c % 8 & 1);
     see[e] = (__bf16)(r < seen ? 1.0f : 0.0f);
   }
+}
+
+// Takes the values of NC pieces of 16 bytes (the at(i)-th of a tile, i < NC) that are not finite out of the tile at vl, and notes them
+// in `bad`, a bit each; returns whether there are any (in any lane: only then `bad` is written).  Times 0, every finite value is 0.
+template <int NC, typename F>
+__device__ __forceinline__ bool take_out(char* vl, unsigned char* bad, F at) {
+  u32x4 y[NC];
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    y[i] = *reinterpret_cast<const u32x4*>(vl + 16 * at(i));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t w = y[i][j];
+      sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), bf16x2{(__bf16)0.0f, (__bf16)0.0f}, sum, false);
+    }
+  }
+  if (__builtin_expect(!__any(sum != 0.0f), 1)) return false;  // (NaN is not 0 either)
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool lo = (y[i][j] & 0x7f80u) == 0x7f80u, hi = (y[i][j] & 0x7f800000u) == 0x7f800000u;
+      bits |= (uint32_t)lo << 2 * j | (uint32_t)hi << (2 * j + 1);
+      y[i][j] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
+    }
+    bad[at(i)] = (unsigned char)bits;
+    *reinterpret_cast<u32x4*>(vl + 16 * at(i)) = y[i];
+  }
+  return true;
 }
 
 template <int NW, int DK, int DV>
@@ -430,27 +463,11 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int 
     if (t >= nfull) {
       // Some queries do not see all of the tile: values that are not finite must not reach them as 0 v.  They are taken
       // out, and noted, a bit each.
-      bool found = false;
-#pragma unroll
-      for (int i = 0; i < C::NV; ++i) {
-        const int e = (wave * C::NV + i) * 64 + lane;
-        u32x4 y = *reinterpret_cast<const u32x4*>(vl + 16 * e);
-        uint32_t bits = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool lo = (y[j] & 0x7f80u) == 0x7f80u, hi = (y[j] & 0x7f800000u) == 0x7f800000u;
-          bits |= (uint32_t)lo << 2 * j | (uint32_t)hi << (2 * j + 1);
-          y[j] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
-        }
-        bad[e] = (unsigned char)bits;
-        if (bits) *reinterpret_cast<u32x4*>(vl + 16 * e) = y;
-        found |= bits != 0;
-      }
-      const bool any = __any(found);
+      const bool any = take_out<C::NV>(vl, bad, [&](int i) { return (wave * C::NV + i) * 64 + lane; });
       if (lane == 0) some[wave] = any;
       lds_barrier();
 #pragma unroll
-      for (int w = 0; w < NW; ++w) odd = odd || some[w];
+      for (int w = 0; w < NW; ++w) odd |= some[w] != 0;
     }
     if (k0 >= wlast) return;  // (a wave that is done still copies and waits)
     f32x16 x[2];
@@ -508,7 +525,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int 
 #pragma unroll 1
         for (int st = 0; st < 4; ++st) {
           bf16x8 n, see;
-          counted<DV>(bad, i, st, lane, limit - k0, n, see);
+          counted<DV>(bad, i, st, lane, limit - k0, n, see, [&](int e) { return some[e / (64 * C::NV)]; });
           y = __builtin_amdgcn_mfma_f32_32x32x16_bf16(n, see, y, 0, 0, 0);
         }
 #pragma unroll
@@ -626,23 +643,7 @@ __global__ __launch_bounds__(64 * kSplitWaves, 1) void kda_attn_split_kernel(Att
     const bool cut = k0 + kSplitKeys > least;
     bool odd = false;
     if (cut) {  // as above: values that are not finite are taken out and noted
-      bool found = false;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int e = i * 64 + lane;
-        u32x4 y = *reinterpret_cast<const u32x4*>(vl + 16 * e);
-        uint32_t bits = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool lo = (y[j] & 0x7f80u) == 0x7f80u, hi = (y[j] & 0x7f800000u) == 0x7f800000u;
-          bits |= (uint32_t)lo << 2 * j | (uint32_t)hi << (2 * j + 1);
-          y[j] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
-        }
-        bad[e] = (unsigned char)bits;
-        if (bits) *reinterpret_cast<u32x4*>(vl + 16 * e) = y;
-        found |= bits != 0;
-      }
-      odd = __any(found);
+      odd = take_out<NV>(vl, bad, [&](int i) { return i * 64 + lane; });
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
     f32x16 x = (f32x16)0.0f;
@@ -687,7 +688,7 @@ __global__ __launch_bounds__(64 * kSplitWaves, 1) void kda_attn_split_kernel(Att
 #pragma unroll 1
         for (int st = 0; st < 2; ++st) {
           bf16x8 n, see;
-          counted<DV>(bad, i, st, lane, limit - k0, n, see);
+          counted<DV>(bad, i, st, lane, limit - k0, n, see, [](int) { return 1; });
           y = __builtin_amdgcn_mfma_f32_32x32x16_bf16(n, see, y, 0, 0, 0);
         }
 #pragma unroll
