@@ -197,8 +197,8 @@ kda_status kda_attn_decode(const void* q, kda_dtype q_dtype, float scale, const 
   kda::KvCache c;
   const kda_status bad = cache_of(pool, raw_enum(kv_dtype), n_pages, page_tokens, table, n_rows, width, rows, B, H_kv, d_k, d_v, &c);
   if (bad != KDA_OK) return bad;
-  // 32-bit counts: granules of 128 tokens over the sequences, and workgroups
-  if ((long long)B * (((long long)width * page_tokens + 127) / 128) >= (1LL << 31) || (long long)B * K * H_q > (1LL << 24))
+  // 32-bit counts: granules of 128 tokens over the sequences, and threads (a workgroup of up to 512 for each unit)
+  if ((long long)B * (((long long)width * page_tokens + 127) / 128) >= (1LL << 31) || (long long)B * K * H_q > (1LL << 22))
     return KDA_ERR_SHAPE;
   const size_t need = kda::attn_decode_workspace(B, K, H_q, H_kv, d_v, page_tokens, width);
   if (!q || !lens || !o || (need && !workspace)) return KDA_ERR_NULL;

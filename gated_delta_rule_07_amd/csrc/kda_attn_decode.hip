@@ -34,7 +34,7 @@ __host__ __device__ inline int columns(int K, int G) { return (K * G + kAttnColu
 
 // The workspace: for each worker two partial results, then the units that have to be joined.
 struct Join {
-  int unit, last, slot, unused;  // unit = (b column tiles + column tile) H + head, or -1; the worker that ends it; which part it is here
+  int unit, last, slot, unused;  // unit = (b H + head) column tiles + column tile, or -1; the worker that ends it; which part it is here
 };
 __host__ __device__ inline size_t part_floats(int dv) { return (size_t)kAttnColumns * (dv + 2); }
 
@@ -171,7 +171,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_decode_kernel(DecodePlan 
       g0 = (int)(off % n);
       g1 = (int)min((long long)n, g0 + (end - at));
     }
-    const int ct = unit / H, h = unit % H;
+    const int h = unit / a.CT, ct = unit % a.CT;
     const int row = __builtin_amdgcn_readfirstlane(cache.rows ? cache.rows[b] : b);
     const int* pages = cache.table + (size_t)row * cache.width;
     const int len = __builtin_amdgcn_readfirstlane(tokens_of(p, b));
@@ -473,7 +473,7 @@ __global__ __launch_bounds__(256) void kda_attn_join_kernel(DecodePlan a) {
   const Join j = a.joins[w0];
   if (j.unit < 0) return;
   const AttnDecodeParams& p = a.p;
-  const int units = a.CT * p.c.H, b = j.unit / units, ct = j.unit % units / p.c.H, h = j.unit % p.c.H;
+  const int units = a.CT * p.c.H, b = j.unit / units, h = j.unit % units / a.CT, ct = j.unit % a.CT;
   const int c2 = kAttnColumns * ct + c, tk = c2 / a.G, n = j.last - w0 + 1;
   if (tk >= p.K) return;
   // worker w0's part is its first or its second, the others' their first

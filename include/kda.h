@@ -580,14 +580,17 @@ kda_status kda_tree_commit(const void* k, kda_dtype qkv_dtype, const float* alph
  * attends with the keys and values of head h / (H_q / H_kv) (grouped heads; H_q a multiple
  * of H_kv), and its output is
  *     o = sum_j p_j v_j,    p = softmax over the j it sees of  scale * q . k_j.
- * Maximum, sum and outputs are carried in fp32.  A query that sees nothing (or only scores of
- * minus infinity) gives zeros.  What a query does not see has no influence on it, whatever
- * it holds: infinities and NaN too.
+ * Maximum, sum and outputs are carried in fp32, for values below 1e30.  A query that sees
+ * nothing (or only scores of minus infinity) gives zeros.  What a query does not see has no
+ * influence on it, whatever it holds: infinities and NaN too.  A query that sees a value
+ * that is not finite has outputs that are not finite.
  *
  * Keys and values of earlier tokens lie in a pool of pages, page_tokens tokens of one layer
- * each, named by page tables like those of kda_cache_fork (entry j of a sequence's row: its
- * tokens [j * page_tokens, (j + 1) * page_tokens)); kda_cache_fork, _free, _compact and _copy serve them as
- * they serve states.  A page:
+ * each, named by page tables like those of kda_cache_fork: entry j of a sequence's row is the
+ * page of its tokens [j * page_tokens, (j + 1) * page_tokens).  kda_cache_fork with
+ * n_private = 0 shares a prefix's pages (the one that is still being filled is then copied
+ * with kda_cache_copy, whose page_bytes are these); kda_cache_free and kda_cache_compact
+ * serve these tables as they serve those of states.  A page:
  *     keys   [H_kv][page_tokens][d_k], then values [H_kv][page_tokens][d_v], in kv_dtype;
  *     KDA_E4M3: then scales [2][H_kv] fp32, of each head's keys, then of its values, and
  *     zeros or anything up to a multiple of 16 bytes: what a code stands for is code * scale.
@@ -602,6 +605,7 @@ kda_status kda_tree_commit(const void* k, kda_dtype qkv_dtype, const float* alph
  *   d_k, d_v   : 64 or 128 (KDA_ERR_UNSUPPORTED otherwise)
  * Lists in device memory that are wrong never make a kernel access memory out of range.
  * H_q, H_kv <= KDA_MAX_HEADS and tokens of a call <= KDA_MAX_CALL_TOKENS, else KDA_ERR_SHAPE.
+ * No call of the library has a backward pass.
  */
 
 #define KDA_MAX_HEADS 4096           /* most heads of one call of an attention layer */
@@ -629,7 +633,8 @@ kda_status kda_tree_commit(const void* k, kda_dtype qkv_dtype, const float* alph
  *
  * cu_seqlens may not decrease.  o may share no byte with another array
  * (KDA_ERR_ALIAS).  fp32 inputs are multiplied in fp32; bf16 inputs on the bf16 matrix
- * cores with fp32 accumulation, the probabilities rounded to bf16 (d_k = d_v in {64, 128}) or kept in fp32.
+ * cores with fp32 accumulation, the probabilities rounded to bf16, where d_k and d_v are each
+ * 64 or 128 (and k_stride and v_stride below 2^24), and else in fp32 too.
  */
 kda_status kda_attn_fwd(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
                         long long v_stride, kda_dtype dtype, float scale, const int* cu_seqlens,
@@ -700,7 +705,9 @@ kda_status kda_kv_read(const void* pool, kda_dtype kv_dtype, int n_pages, int pa
  *   workspace: device memory of workspace_bytes bytes (kda_attn_decode_plan), 16-byte aligned;
  *         its contents on entry do not matter.  NULL when the plan says 0.  Calls that may run
  *         at the same time need one each.                                   (written)
- *   B: 1 .. KDA_MAX_PAGED_SEQS, K: 1 .. KDA_MAX_ATTN_TOKENS
+ *   B: 1 .. KDA_MAX_PAGED_SEQS, K: 1 .. KDA_MAX_ATTN_TOKENS, B * K * H_q <= 2^22
+ *   (KDA_ERR_SHAPE).  The cache is read once for every 16 rows of queries that share a head
+ *   (there are K * H_q / H_kv of them).
  *
  * fp32 queries are multiplied as three bf16 terms, and so are their probabilities: results
  * are fp32's.  With bf16 queries the probabilities are rounded to bf16.  Errors: KDA_ERR_NULL (workspace needed),

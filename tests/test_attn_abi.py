@@ -95,7 +95,7 @@ DEC = dict(q=_a(0), dt=1, scale=0.1, pool=_a(1), kv=2, P=64, pt=64, table=_a(2),
 @pytest.mark.parametrize("over,code", [
     (dict(dt=2), 3), (dict(odt=2), 3), (dict(kv=0), 3), (dict(B=0), 2), (dict(B=4097), 2), (dict(K=0), 2), (dict(K=17), 2), (dict(hq=31), 2),
     (dict(scale=math.inf), 2), (dict(wn=1000), 2), (dict(R=1, W=1 << 25, pt=64), 2), (dict(R=5, rows=None, B=6), 2),
-    (dict(R=1, W=1 << 20, pt=128, B=4096), 2), (dict(B=4096, K=16, hq=512), 2),
+    (dict(R=1, W=1 << 20, pt=128, B=4096), 2), (dict(B=4096, K=16, hq=512), 2), (dict(B=1025, hq=4096, K=1, R=2000), 2),
     (dict(pt=24), 4), (dict(dv=32), 4), (dict(q=None), 1), (dict(lens=None), 1), (dict(o=None), 1), (dict(ws=None), 1), (dict(pool=None), 1),
     (dict(q=_a(0, 8)), 5), (dict(ws=_a(6, 8)), 5), (dict(o=_a(0)), 6), (dict(o=_a(1)), 6), (dict(ws=_a(5)), 6), (dict(ws=_a(1)), 6), (dict(o=_a(4)), 6),
     (dict(ws=_a(2)), 6),

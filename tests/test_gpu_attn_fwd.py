@@ -165,6 +165,19 @@ def test_what_a_query_does_not_see_has_no_influence(gpu, dtype, d, hq, bad):
                 assert not torch.isfinite(o[t:end, G:]).all(-1).all() if x is k else not torch.isfinite(o[t:end, G:]).any()
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_nothing_to_attend_with_or_to(gpu, dtype):
+    kda = _kda()
+    q, k, v = _qkv(gpu, 15, 3, 3, 4, 2, 64, 64, dtype)
+    assert kda.kda_attn_fwd(q[:0], k, v).shape == (0, 4, 64)
+    o = torch.full((3, 4, 64), 7.0, device=gpu, dtype=dtype)
+    kda.kda_attn_fwd(q, k[:0], v[:0], o=o)
+    assert not o.any()
+    kda.kda_attn_fwd(q, k[:0], v[:0], cu_seqlens=_i([0, 2, 3], gpu), cu_seqlens_k=_i([0, 0, 0], gpu), o=o.fill_(7))
+    assert not o.any()
+    assert kda.kda_attn_fwd(q[:0].unflatten(0, (2, 0)), k[:2].unflatten(0, (2, 1)), v[:2].unflatten(0, (2, 1))).shape == (2, 0, 4, 64)
+
+
 def test_nothing_but_minus_infinity(gpu):
     """A row all of whose scores are minus infinity gives zeros, as one that sees nothing."""
     kda = _kda()
