@@ -52,6 +52,22 @@ __device__ __forceinline__ bool part_of(const AttnParams& p, int tile, Part& s) 
   return j >= 0 && s.nq > 0 && j < tiles;
 }
 
+// Workgroups go to the 8 dies in turn, and what a die's workgroups read is shared in its L2: each die takes whole key heads
+// or, where there are fewer than dies (or an odd number of them), every R-th tile of its heads, so that tiles with many keys
+// are spread.  Measured on 8,000 tokens, us, against runs of neighbouring tiles a die: 8 heads of queries on 1 of keys
+// 175 / 203, 16 on 4 264 / 317, 12 on 3 233 / 293; fp32, 3,000 tokens, 8 on 2 261 against 326 in the order of the heads.
+// pair_of returns whether this workgroup has a tile; its heads and tile.
+__host__ __device__ inline unsigned dies_of_head(const AttnParams& p) { return 8 / std::min(p.Hk & -p.Hk, 8); }
+__host__ __device__ inline unsigned tiles_of_die(const AttnParams& p, unsigned tiles) { return (tiles + dies_of_head(p) - 1) / dies_of_head(p); }
+inline dim3 grid_of(const AttnParams& p, unsigned tiles) { return dim3(dies_of_head(p) * p.Hq * tiles_of_die(p, tiles)); }
+__device__ __forceinline__ bool pair_of(const AttnParams& p, unsigned tiles, int& h, int& hk, int& tile) {
+  const unsigned G = p.Hq / p.Hk, R = dies_of_head(p), per = tiles_of_die(p, tiles), die = blockIdx.x % 8, i = blockIdx.x / 8;
+  hk = die / R + 8 / R * (i / (per * G));
+  h = hk * G + i % G;
+  tile = i % (per * G) / G * R + die % R;
+  return (unsigned)tile < tiles;
+}
+
 // Four outputs from element `at` of o on.
 __device__ __forceinline__ void store4(const AttnParams& p, size_t at, const f32x4& y) {
   if (p.o_f32) *reinterpret_cast<f32x4*>(static_cast<float*>(p.o) + at) = y;
@@ -61,7 +77,9 @@ __device__ __forceinline__ void store4(const AttnParams& p, size_t at, const f32
 // ---- every type and head size: fp32 matrix cores -------------------------------------------
 // The fp32 matrix cores are slow enough for the operands to come straight from the caches into registers: a
 // workgroup takes 16 queries, each of its waves every fourth tile of 32 keys, and they are joined at the end.  So a
-// few queries behind a long prefix already fill many waves.
+// few queries behind a long prefix already fill many waves.  Measured: 391 queries of 8 heads of 64 / 128 behind 3 cached
+// prefixes 26 us, 3,000 tokens of 8 heads of 128 240 us (76 TFLOP/s).  Bound by the matrix cores, of which a wave fills
+// three quarters alone, and then by the 32 KB of a tile that a compute unit takes from the L2 (eight waves are slower: 29.6 us).
 //   S^T = K Q^T: a lane holds 8 of every 32 values of a key's row;
 //   O^T = V^T P^T: a lane holds DV / 16 neighbouring channels of 8 keys, and tile t of the output is the t-th of them.
 
@@ -95,23 +113,15 @@ __device__ __forceinline__ void load_values(const __bf16* p, float* r) {
 }
 
 template <typename IO, int DK, int DV>
-__global__ __launch_bounds__(64 * kPlainWaves, 2) void kda_attn_plain_kernel(AttnParams p) {
+__global__ __launch_bounds__(64 * kPlainWaves, 2) void kda_attn_plain_kernel(AttnParams p, unsigned tiles) {
   constexpr int NS = (DK + 31) / 32, NT = DV / 16;
   __shared__ __attribute__((aligned(16))) float so[kPlainWaves][kRows][DV + 4];
   __shared__ float sm[kPlainWaves][kRows], sl[kPlainWaves][kRows];
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), c = lane % 16, g = lane / 16;
-  const int h = blockIdx.y, hk = h / (p.Hq / p.Hk);
+  int h, hk, at;
   Part s;
-  if (!part_of<kRows>(p, blockIdx.x, s)) return;
+  if (!pair_of(p, tiles, h, hk, at) || !part_of<kRows>(p, at, s)) return;
   const int row = s.r0 + c;  // this lane's query
-  Frag<float> q[NS];         // as a B operand: values 32 step + 8 g + e
-#pragma unroll
-  for (int st = 0; st < NS; ++st) {
-    q[st].zero();
-    const int i0 = 32 * st + 8 * g;
-    if (row < s.nq && i0 < DK)
-      load_values<8>(static_cast<const IO*>(p.q) + (size_t)(s.q0 + row) * p.q_stride + (size_t)h * DK + i0, q[st].v);
-  }
   const int shift = s.nk - s.nq;
   const int limit = row < s.nq ? row + shift + 1 : 0;  // this query's keys
   const int last = min(s.r0 + kRows, s.nq) + shift;    // the workgroup's
@@ -124,6 +134,7 @@ __global__ __launch_bounds__(64 * kPlainWaves, 2) void kda_attn_plain_kernel(Att
 
   const IO* kg = static_cast<const IO*>(p.k) + (size_t)s.k0 * p.k_stride + (size_t)hk * DK;
   const IO* vg = static_cast<const IO*>(p.v) + (size_t)s.k0 * p.v_stride + (size_t)hk * DV;
+  Frag<float> q[NS];  // as a B operand: values 32 step + 8 g + e
   Frag<float> k[2][NS];
   float v[8][NT];
   // (rows behind the last key: that one again)
@@ -145,27 +156,23 @@ __global__ __launch_bounds__(64 * kPlainWaves, 2) void kda_attn_plain_kernel(Att
       load_values<NT>(vg + (size_t)min(k0 + 16 * (e / 4) + 4 * g + e % 4, s.nk - 1) * p.v_stride + NT * c, v[e]);
   };
 
-  int k0 = wave * kKeys;
-  if (k0 < last) keys(k0), values(k0);
-  for (; k0 < last; k0 += kPlainWaves * kKeys) {
-    const int next = k0 + kPlainWaves * kKeys;
-    f32x4 x[2] = {(f32x4)0.0f, (f32x4)0.0f};  // S^T of keys 0..15 and 16..31
+  // The order of loads and uses is kept (the scheduler would mix them, and then wait for all): a tile's keys are loaded
+  // while the last one's values are used, its values while its keys are.
+  auto scores = [&](f32x4 (&x)[2]) {  // S^T of keys 0..15 and 16..31
+#pragma unroll
+    for (int u = 0; u < 2; ++u) x[u] = (f32x4)0.0f;
 #pragma unroll
     for (int st = 0; st < NS; ++st)
 #pragma unroll
       for (int u = 0; u < 2; ++u) x[u] = mma(k[u][st], q[st], x[u]);
-    if (next < last) keys(next);
-    const bool partial = k0 + kKeys > least;
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto powers = [&](f32x4 (&x)[2]) {
     float top = -__builtin_inff();
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        x[u][r] *= scale;
-        if (partial && k0 + 16 * u + 4 * g + r >= limit) x[u][r] = -__builtin_inff();
-        top = fmaxf(top, x[u][r]);
-      }
-    }
+      for (int r = 0; r < 4; ++r) top = fmaxf(top, x[u][r]);
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
     const float now = fmaxf(m, top), base = now == -__builtin_inff() ? 0.0f : now;
@@ -180,10 +187,35 @@ __global__ __launch_bounds__(64 * kPlainWaves, 2) void kda_attn_plain_kernel(Att
         l += x[u][r];
       }
     }
-    const Frag<float> pt = frag_from_tiles<float>(x[0], x[1], 1.0f);
 #pragma unroll
     for (int t = 0; t < NT; ++t) o[t] *= keep;
-    if (!partial) {
+    return frag_from_tiles<float>(x[0], x[1], 1.0f);
+  };
+  int k0 = wave * kKeys;
+  if (k0 < last) {
+    keys(k0);
+    const IO* y = static_cast<const IO*>(p.q) + (size_t)(s.q0 + min(row, s.nq - 1)) * p.q_stride + (size_t)h * DK + 8 * g;
+#pragma unroll
+    for (int st = 0; st < NS; ++st) {
+      if (DK % 32 == 0 || 32 * st + 8 * g < DK) load_values<8>(y + 32 * st, q[st].v);
+      else q[st].zero();
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    values(k0);
+    __builtin_amdgcn_sched_barrier(0);
+    // (waited for here: a wait inside the loop would wait for the tiles' loads too)
+#pragma unroll
+    for (int st = 0; st < NS; ++st)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) asm volatile("" : "+v"(q[st].v[e]));
+    f32x4 x[2];
+    for (; k0 + kKeys <= least; k0 += kPlainWaves * kKeys) {  // tiles that every query sees whole
+      scores(x);
+      keys(k0 + kPlainWaves * kKeys);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) x[u] *= scale;
+      const Frag<float> pt = powers(x);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         Frag<float> a;
@@ -191,7 +223,17 @@ __global__ __launch_bounds__(64 * kPlainWaves, 2) void kda_attn_plain_kernel(Att
         for (int e = 0; e < 8; ++e) a.v[e] = v[e][t];
         o[t] = mma(a, pt, o[t]);
       }
-    } else {
+      __builtin_amdgcn_sched_barrier(0);
+      values(k0 + kPlainWaves * kKeys);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (k0 < last) {  // one that is cut: the borders of 16 queries lie in two tiles at most, of two waves
+      scores(x);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[u][r] = k0 + 16 * u + 4 * g + r >= limit ? -__builtin_inff() : x[u][r] * scale;
+      const Frag<float> pt = powers(x);
       // What no query sees is left out.  Values that are not finite must not reach, as 0 v, queries that do not see them:
       // they are left out too, and counted for each query that does see them: its outputs become NaN.
       Frag<float> see;
@@ -216,7 +258,6 @@ __global__ __launch_bounds__(64 * kPlainWaves, 2) void kda_attn_plain_kernel(Att
         }
       }
     }
-    if (next < last) values(next);
   }
 
   // join the waves
@@ -367,19 +408,15 @@ struct FastCfg {
 };
 
 template <int NW, int DK, int DV>
-__global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, int tiles, unsigned chunk) {
+__global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, unsigned tiles) {
   using C = FastCfg<NW, DK, DV>;
   __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
   __shared__ unsigned char bad[C::VB / 16];  // a bit for each value of a tile that is not finite
   __shared__ int some[NW];
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), c = lane % 32, hf = lane / 32;
-  const int G = p.Hq / p.Hk;
-  // Workgroups go to the 8 dies in turn: each die takes a run of neighbours, which share keys and values in its L2.
-  const unsigned w = blockIdx.x % 8 * chunk + blockIdx.x / 8;
-  if (w >= (unsigned)tiles * p.Hq) return;
-  const int hk = w / ((unsigned)tiles * G), in = w % ((unsigned)tiles * G), h = hk * G + in % G;
+  int h, hk, at;
   Part s;
-  if (!part_of<C::BM>(p, in / G, s)) return;
+  if (!pair_of(p, tiles, h, hk, at) || !part_of<C::BM>(p, at, s)) return;
   const int row = s.r0 + 32 * wave + c;  // this lane's query
   const int shift = s.nk - s.nq;
   const int limit = row < s.nq ? row + shift + 1 : 0;
@@ -572,16 +609,16 @@ constexpr int kSplitWaves = 4, kSplitKeys = 32;
 constexpr unsigned kFewTiles = 256;  // workgroups of it that the card's compute units hold at once
 
 template <int DK, int DV>
-__global__ __launch_bounds__(64 * kSplitWaves, 1) void kda_attn_split_kernel(AttnParams p) {
+__global__ __launch_bounds__(64 * kSplitWaves, 1) void kda_attn_split_kernel(AttnParams p, unsigned tiles) {
   constexpr int KB = kSplitKeys * DK * 2, VB = kSplitKeys * DV * 2, NK = KB / 1024, NV = VB / 1024;
   constexpr int RING = 2 * (KB + VB), JOIN = 32 * (DV + 4) * 4;  // bytes of a wave
   __shared__ __attribute__((aligned(1024))) char lds[kSplitWaves * (RING > JOIN ? RING : JOIN)];
   __shared__ unsigned char bads[kSplitWaves][VB / 16];
   __shared__ float sm[kSplitWaves][32], sl[kSplitWaves][32];
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), c = lane % 32, hf = lane / 32;
-  const int h = blockIdx.y, hk = h / (p.Hq / p.Hk);
+  int h, hk, at;
   Part s;
-  if (!part_of<32>(p, blockIdx.x, s)) return;
+  if (!pair_of(p, tiles, h, hk, at) || !part_of<32>(p, at, s)) return;
   const int row = s.r0 + c, shift = s.nk - s.nq;
   const int limit = row < s.nq ? row + shift + 1 : 0;  // this lane's query's keys
   const int last = min(s.r0 + 32, s.nq) + shift;       // the workgroup's
@@ -741,17 +778,18 @@ hipError_t launch_fast(const AttnParams& p, hipStream_t s) {
   // cached ones 128 tokens of 32 heads (128) 262 / 577, 512 (512) 663 / 582.
   const unsigned few = tiles_of<32>(p);
   if ((unsigned long long)few * p.Hq <= kFewTiles) {
-    hipLaunchKernelGGL((kda_attn_split_kernel<DK, DV>), dim3(few, p.Hq), dim3(64 * kSplitWaves), 0, s, p);
+    hipLaunchKernelGGL((kda_attn_split_kernel<DK, DV>), grid_of(p, few), dim3(64 * kSplitWaves), 0, s, p, few);
     return hipGetLastError();
   }
-  const unsigned tiles = tiles_of<32 * NW>(p), chunk = (tiles * p.Hq + 7) / 8;
-  hipLaunchKernelGGL((kda_attn_kernel<NW, DK, DV>), dim3(8 * chunk), dim3(64 * NW), 0, s, p, (int)tiles, chunk);
+  const unsigned tiles = tiles_of<32 * NW>(p);
+  hipLaunchKernelGGL((kda_attn_kernel<NW, DK, DV>), grid_of(p, tiles), dim3(64 * NW), 0, s, p, tiles);
   return hipGetLastError();
 }
 
 template <typename IO, int DK, int DV>
 hipError_t launch_plain(const AttnParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((kda_attn_plain_kernel<IO, DK, DV>), dim3(tiles_of<kRows>(p), p.Hq), dim3(64 * kPlainWaves), 0, s, p);
+  const unsigned tiles = tiles_of<kRows>(p);
+  hipLaunchKernelGGL((kda_attn_plain_kernel<IO, DK, DV>), grid_of(p, tiles), dim3(64 * kPlainWaves), 0, s, p, tiles);
   return hipGetLastError();
 }
 

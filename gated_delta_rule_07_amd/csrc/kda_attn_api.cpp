@@ -72,8 +72,8 @@ kda_status kda_attn_fwd(const void* q, long long q_stride, const void* k, long l
   if (!cu_seqlens && cu_seqlens_k) return KDA_ERR_NULL;
   if (!cu_seqlens && (total_q % N || total_k % N)) return KDA_ERR_SHAPE;
   if (cu_seqlens && !cu_seqlens_k && total_q != total_k) return KDA_ERR_SHAPE;
-  // tiles of 64 rows, a workgroup of up to 512 threads for each and head, fewer than 2^32 threads in all
-  if (((long long)total_q / 64 + N + 1) * H_q > (1LL << 22)) return KDA_ERR_SHAPE;
+  // fewer than 2^32 threads: 256 for each head and 16 rows, each sequence's rounded up, and all rounded up to 8
+  if (((long long)total_q / 64 + N + 2) * H_q > (1LL << 22)) return KDA_ERR_SHAPE;
   if (total_q == 0) return KDA_OK;
   if (!q || !o || (total_k > 0 && (!k || !v))) return KDA_ERR_NULL;
   const int io = io_of(raw_enum(dtype)), oo = io_of(raw_enum(o_dtype));

@@ -629,7 +629,8 @@ kda_status kda_tree_commit(const void* k, kda_dtype qkv_dtype, const float* alph
  *   o      : total_q rows of H_q heads of d_v values, o_dtype, o_stride apart (written; rows
  *            outside every sequence are left as they were)
  *   scale  : finite (KDA_ERR_SHAPE)
- *   d_k, d_v: 16, 32, 64 or 128.  N >= 1; total_q, total_k >= 0 (no queries: nothing is done)
+ *   d_k, d_v: 16, 32, 64 or 128.  N >= 1; total_q, total_k >= 0 (no queries: nothing is done);
+ *            (total_q / 64 + N + 2) * H_q <= 2^22 (KDA_ERR_SHAPE)
  *
  * cu_seqlens may not decrease.  o may share no byte with another array
  * (KDA_ERR_ALIAS).  fp32 inputs are multiplied in fp32; bf16 inputs on the bf16 matrix
