@@ -278,6 +278,31 @@ def test_read(gpu, cache, out, pt, dk, dv):
     assert ko.dtype == vo.dtype == out and not ko[at:].any() and not vo[at:].any()
 
 
+@pytest.mark.parametrize("cache", [BF, E])
+@pytest.mark.parametrize("out", [BF, F])
+def test_read_of_more_rows_than_a_cache_holds(gpu, cache, out):
+    """As many rows as are stored past the caches: those of calls with few rows each."""
+    kda = _kda()
+    lay = kda.KVLayout(cache, 64, 5, 128, 64)
+    lens = [150001, 1, 4444, 77]
+    P, table = _tables(lay, [-(-n // 64) for n in lens], gpu, 30)
+    table[0, 1000] = -1
+    pool = _filled(kda, lay, P, gpu, 31)
+    n = sum(lens) + 3
+    ko, vo = torch.full((n, 5, 128), 7.0, device=gpu, dtype=out), torch.full((n, 5, 64), 7.0, device=gpu, dtype=out)
+    assert (ko.numel() + vo.numel()) * ko.element_size() > 256 << 20
+    kda.kda_kv_read(pool, lay, table, _cu(lens, gpu), n, k_out=ko, v_out=vo)
+    at = 0
+    for b, ln in enumerate(lens):
+        for a in range(0, ln, 30000):
+            m = min(30000, ln - a)
+            x, y = torch.full((m, 5, 128), 7.0, device=gpu, dtype=out), torch.full((m, 5, 64), 7.0, device=gpu, dtype=out)
+            kda.kda_kv_read(pool, lay, table, _i([0, m], gpu), m, rows=_i([b], gpu), starts=_i([a], gpu), k_out=x, v_out=y)
+            assert torch.equal(ko[at + a:at + a + m], x) and torch.equal(vo[at + a:at + a + m], y), (b, a)
+        at += ln
+    assert bool((ko[at:] == 7).all()) and bool((vo[at:] == 7).all())
+
+
 def test_far_pages(gpu):
     """Pages that start past 2^32 bytes."""
     if torch.cuda.mem_get_info()[0] < 24 << 30:
