@@ -40,12 +40,22 @@ __device__ __forceinline__ u32x4 bits_of(const f32x4& lo, const f32x4& hi) {
   return __builtin_bit_cast(u32x4, h);
 }
 
-// Cosine and sine of pos * freq: the angle's reduction to a fraction of a turn in fp64.
-__device__ __forceinline__ float2 turn_of(long long pos, float freq) {
-  const double turns = (double)pos * (double)freq * 0.15915494309189535;  // 1 / (2 pi)
+// Cosine and sine of pos times a frequency in turns: the angle's reduction to a fraction of a turn in fp64.
+__device__ __forceinline__ float2 turn_of(double pos, double freq) {
+  const double turns = pos * freq;
   float s, c;
   sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
   return float2{c, s};
+}
+
+// The turns of nt tokens at positions pos(t) to turn[t][half]: a thread keeps to one frequency.
+template <typename F>
+__device__ __forceinline__ void turns_of(float2* turn, const float* inv_freq, int half, int nt, int tid, F pos) {
+  if (!half) return;
+  const int step = kThreads / half, i = tid % half;
+  if (tid >= step * half) return;
+  const double freq = (double)inv_freq[i] * 0.15915494309189535;  // 1 / (2 pi)
+  for (int t = tid / half; t < nt; t += step) turn[t * half + i] = turn_of(pos(t), freq);
 }
 
 // The two pieces of 8 values that a lane of a row's d / 16 holds.
@@ -150,22 +160,23 @@ __device__ bool shared_page(const AppendParams& p, int page, int b, long long j,
     return hit;
   }
   for (int c0 = 0; c0 < p.N; c0 += 64) {
-    // a lane looks after one sequence; where one has many pages, the wave takes every kWaves-th sequence after the other
+    // a lane looks after one sequence: four of its first 16 pages in each wave
     const int c = min(c0 + lane, p.N - 1);
     const Span s = span_of(p, c);
     const int row = p.c.rows ? p.c.rows[c] : c;
     const long long first = s.before / pt;
     const int n = c0 + lane < p.N ? (int)min(touched(s, pt), max(0LL, p.c.width - first)) : 0;
-    if (!__any(n > 4)) {
-      if (c0 / 64 % kWaves == wave)
-        for (int i = 0; i < 4; ++i) hit |= i < n && !(c == b && i == j) && names(row, first + i);
-    } else {
+#pragma unroll
+    for (int i = wave; i < 4 * kWaves; i += kWaves) hit |= i < n && !(c == b && i == j) && names(row, first + i);
+    // the others of the sequences that have more: the waves take these sequences in turn, or all of them the few there are
+    unsigned long long more = __ballot(n > 4 * kWaves);
+    const bool few = __popcll(more) < kWaves;
+    for (int k = 0; more; ++k, more &= more - 1) {
+      if (!few && k % kWaves != wave) continue;
+      const int l = __builtin_ctzll(more), m = __shfl(n, l), r = __shfl(row, l), q = c0 + l;
+      const long long f = __shfl(first, l);
 #pragma unroll 4
-      for (int l = wave; l < 64; l += kWaves) {
-        const int m = __shfl(n, l), r = __shfl(row, l), q = c0 + l;
-        const long long f = __shfl(first, l);
-        for (int i = lane; i < m; i += 64) hit |= !(q == b && i == j) && names(r, f + i);
-      }
+      for (int i = 4 * kWaves + (few ? tid : lane); i < m; i += few ? kThreads : 64) hit |= !(q == b && i == j) && names(r, f + i);
     }
   }
   return hit;
@@ -177,20 +188,15 @@ template <typename IO>
 __device__ void append_queries(const AppendParams& p, int block, int tokens, float2* turn, int tid) {
   const int t0 = block * tokens, nt = min(tokens, p.total - t0), half = p.rot / 2;
   const int b0 = p.cu && !p.positions && half ? last_at_most_wave(p.N, t0, [&](int i) { return (long long)p.cu[i]; }) : 0;
-  for (int e = tid; e < nt * half; e += kThreads) {
-    const int t = t0 + e / half;
-    long long pos = 0;
-    if (p.positions) {
-      pos = p.positions[t];
-    } else {
-      int b = p.cu ? b0 : t;
-      if (p.cu)
-        while (b + 1 < p.N && p.cu[b + 1] <= t) ++b;
-      const Span s = span_of(p, b);
-      pos = s.before + t - s.t0;
-    }
-    turn[e] = turn_of(pos, p.inv_freq[e % half]);
-  }
+  turns_of(turn, p.inv_freq, half, nt, tid, [&](int i) {
+    const int t = t0 + i;
+    if (p.positions) return (double)p.positions[t];
+    int b = p.cu ? b0 : t;
+    if (p.cu)
+      while (b + 1 < p.N && p.cu[b + 1] <= t) ++b;
+    const Span s = span_of(p, b);
+    return (double)(s.before + t - s.t0);
+  });
   __syncthreads();
   // a group of lanes takes one token, and some of its heads: its cosines and sines stay in registers
   const int lanes = p.c.dk / 16, groups = kThreads / lanes, gr = tid / lanes, d = p.c.dk;
@@ -279,10 +285,8 @@ __global__ __launch_bounds__(kThreads) void kda_kv_append_kernel(AppendParams p,
   const int page = kv_page(c, b, at);
   const bool any = __any(page >= 0 && shared_page(p, page, b, j, tid));
   if (lane == 0) flag[wave] = any;
-  for (int e = tid; e < nt * half; e += kThreads) {
-    const int t = e / half;
-    turn[e] = turn_of(p.positions ? (long long)p.positions[t0 + t] : s.before + first + t, p.inv_freq[e % half]);
-  }
+  const double place = (double)(s.before + first);
+  turns_of(turn, p.inv_freq, half, nt, tid, [&](int t) { return p.positions ? (double)p.positions[t0 + t] : place + (double)t; });
   __syncthreads();
   bool store = page >= 0;
 #pragma unroll

@@ -582,8 +582,8 @@ kda_status kda_tree_commit(const void* k, kda_dtype qkv_dtype, const float* alph
  *     o = sum_j p_j v_j,    p = softmax over the j it sees of  scale * q . k_j.
  * Maximum, sum and outputs are carried in fp32, for values below 1e30.  A query that sees
  * nothing (or only scores of minus infinity) gives zeros.  What a query does not see has no
- * influence on it, whatever it holds: infinities and NaN too.  A query that sees a value
- * that is not finite has outputs that are not finite.
+ * influence on it, whatever it holds: infinities and NaN too.  An infinity or NaN in a value
+ * that it does see makes that channel of its output NaN or infinite.
  *
  * Keys and values of earlier tokens lie in a pool of pages, page_tokens tokens of one layer
  * each, named by page tables like those of kda_cache_fork: entry j of a sequence's row is the

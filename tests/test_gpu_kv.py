@@ -193,6 +193,29 @@ def test_pages_that_may_not_be_written(gpu, cache, table, before, lens, rows):
     assert torch.equal(ko, k)  # (a rotation by nothing; tokens that are not stored have their rows too)
 
 
+@pytest.mark.parametrize("cache", [BF, E])
+@pytest.mark.parametrize("lens,same", [
+    ([700], [(0, 3, 0, 40)]),                                                      # a page early and late in one row
+    ([350, 20, 400], [(0, 18, 2, 24), (2, 1, 1, 0)]),                              # among pages behind the sixteenth, and before it
+    ([300, 310, 17, 330, 290, 500, 280], [(1, 17, 5, 30), (4, 2, 6, 16), (0, 16, 0, 17)]),  # more long sequences than waves
+    ([40] * 70 + [600, 1, 320], [(70, 37, 3, 1), (72, 19, 69, 2), (71, 0, 70, 5)]),        # sequences behind the 64th
+])
+def test_shared_pages_of_long_sequences(gpu, cache, lens, same):
+    kda = _kda()
+    lay = kda.KVLayout(cache, 16, 2, 64, 64)
+    need = [-(-(n + 5) // 16) for n in lens]
+    P, table = _tables(lay, need, gpu, 32)
+    for b, i, c, j in same:
+        table[c, j] = table[b, i]
+    pool = _filled(kda, lay, P, gpu, 33)
+    g = torch.Generator(device=gpu).manual_seed(34)
+    k, v = (torch.randn(sum(lens), 2, 64, generator=g, device=gpu).to(BF) for _ in range(2))
+    want = am.Pages(lay, pool)
+    want.append(table.tolist(), [5] * len(lens), list(k.cpu().double().split(lens)), list(v.cpu().double().split(lens)))
+    kda.kda_kv_append(k, v, pool, lay, table, _i([5] * len(lens), gpu), cu_seqlens=_cu(lens, gpu))
+    _same_pages(lay, pool, want)
+
+
 def test_lists_that_are_wrong(gpu):
     """Offsets that decrease or lie out of range: nothing out of range is touched, rows outside every sequence are left."""
     kda = _kda()
