@@ -76,14 +76,14 @@ __device__ __forceinline__ void store4(const AttnParams& p, size_t at, const f32
 
 // ---- every type and head size: fp32 matrix cores -------------------------------------------
 // The fp32 matrix cores are slow enough for the operands to come straight from the caches into registers: a
-// workgroup takes 16 queries, each of its waves every fourth tile of 32 keys, and they are joined at the end.  So a
+// workgroup takes 16 or 32 queries, each of its waves every fourth tile of 32 keys, and they are joined at the end.  So a
 // few queries behind a long prefix already fill many waves.  Measured: 391 queries of 8 heads of 64 / 128 behind 3 cached
-// prefixes 26 us, 3,000 tokens of 8 heads of 128 240 us (76 TFLOP/s).  Bound by the matrix cores, of which a wave fills
-// three quarters alone, and then by the 32 KB of a tile that a compute unit takes from the L2 (eight waves are slower: 29.6 us).
+// prefixes 26 us (eight waves: 29.6), 3,000 tokens of 8 heads of 128 196 us (94 TFLOP/s of 154).  Bound by the matrix
+// cores, of which a wave with a SIMD to itself fills three quarters, and by what a compute unit takes from the L2, 32 KB a tile.
 //   S^T = K Q^T: a lane holds 8 of every 32 values of a key's row;
 //   O^T = V^T P^T: a lane holds DV / 16 neighbouring channels of 8 keys, and tile t of the output is the t-th of them.
 
-constexpr int kRows = 16, kKeys = 32, kPlainWaves = 4;
+constexpr int kKeys = 32, kPlainWaves = 4;
 
 // n neighbouring values as fp32.
 template <int N>
@@ -112,29 +112,36 @@ __device__ __forceinline__ void load_values(const __bf16* p, float* r) {
   }
 }
 
-template <typename IO, int DK, int DV>
-__global__ __launch_bounds__(64 * kPlainWaves, 2) void kda_attn_plain_kernel(AttnParams p, unsigned tiles) {
-  constexpr int NS = (DK + 31) / 32, NT = DV / 16;
+// A workgroup takes RT tiles of 16 queries.
+template <typename IO, int DK, int DV, int RT>
+__global__ __launch_bounds__(64 * kPlainWaves, RT == 1 ? 2 : 1) void kda_attn_plain_kernel(AttnParams p, unsigned tiles) {
+  constexpr int NS = (DK + 31) / 32, NT = DV / 16, kRows = 16 * RT;
   __shared__ __attribute__((aligned(16))) float so[kPlainWaves][kRows][DV + 4];
   __shared__ float sm[kPlainWaves][kRows], sl[kPlainWaves][kRows];
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), c = lane % 16, g = lane / 16;
   int h, hk, at;
   Part s;
   if (!pair_of(p, tiles, h, hk, at) || !part_of<kRows>(p, at, s)) return;
-  const int row = s.r0 + c;  // this lane's query
   const int shift = s.nk - s.nq;
-  const int limit = row < s.nq ? row + shift + 1 : 0;  // this query's keys
-  const int last = min(s.r0 + kRows, s.nq) + shift;    // the workgroup's
-  const int least = s.r0 + shift + 1;                  // what all of its queries see
+  const int last = min(s.r0 + kRows, s.nq) + shift;  // the workgroup's keys
+  const int least = s.r0 + shift + 1;                // what all of its queries see
   const float scale = p.scale * kLog2e;
-  f32x4 o[NT];
+  // of the lane's queries, r0 + 16 j + c
+  int limit[RT];  // their keys
+  f32x4 o[RT][NT];
+  float m[RT], l[RT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) o[t] = (f32x4)0.0f;
-  float m = -__builtin_inff(), l = 0.0f;
+  for (int j = 0; j < RT; ++j) {
+    const int row = s.r0 + 16 * j + c;
+    limit[j] = row < s.nq ? row + shift + 1 : 0;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) o[j][t] = (f32x4)0.0f;
+    m[j] = -__builtin_inff(), l[j] = 0.0f;
+  }
 
   const IO* kg = static_cast<const IO*>(p.k) + (size_t)s.k0 * p.k_stride + (size_t)hk * DK;
   const IO* vg = static_cast<const IO*>(p.v) + (size_t)s.k0 * p.v_stride + (size_t)hk * DV;
-  Frag<float> q[NS];  // as a B operand: values 32 step + 8 g + e
+  Frag<float> q[RT][NS];  // as B operands: values 32 step + 8 g + e
   Frag<float> k[2][NS];
   float v[8][NT];
   // (rows behind the last key: that one again)
@@ -158,16 +165,18 @@ __global__ __launch_bounds__(64 * kPlainWaves, 2) void kda_attn_plain_kernel(Att
 
   // The order of loads and uses is kept (the scheduler would mix them, and then wait for all): a tile's keys are loaded
   // while the last one's values are used, its values while its keys are.
-  auto scores = [&](f32x4 (&x)[2]) {  // S^T of keys 0..15 and 16..31
+  auto scores = [&](f32x4 (&x)[RT][2]) {  // S^T of keys 0..15 and 16..31
 #pragma unroll
-    for (int u = 0; u < 2; ++u) x[u] = (f32x4)0.0f;
+    for (int j = 0; j < RT; ++j) x[j][0] = x[j][1] = (f32x4)0.0f;
 #pragma unroll
     for (int st = 0; st < NS; ++st)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) x[u] = mma(k[u][st], q[st], x[u]);
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < RT; ++j) x[j][u] = mma(k[u][st], q[j][st], x[j][u]);
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto powers = [&](f32x4 (&x)[2]) {
+  auto powers = [&](f32x4 (&x)[2], int j) {
     float top = -__builtin_inff();
 #pragma unroll
     for (int u = 0; u < 2; ++u)
@@ -175,70 +184,80 @@ __global__ __launch_bounds__(64 * kPlainWaves, 2) void kda_attn_plain_kernel(Att
       for (int r = 0; r < 4; ++r) top = fmaxf(top, x[u][r]);
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
-    const float now = fmaxf(m, top), base = now == -__builtin_inff() ? 0.0f : now;
-    const float keep = __builtin_amdgcn_exp2f(m - base);
-    m = now;
-    l *= keep;
+    const float now = fmaxf(m[j], top), base = now == -__builtin_inff() ? 0.0f : now;
+    const float keep = __builtin_amdgcn_exp2f(m[j] - base);
+    m[j] = now;
+    l[j] *= keep;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         x[u][r] = __builtin_amdgcn_exp2f(x[u][r] - base);
-        l += x[u][r];
+        l[j] += x[u][r];
       }
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) o[t] *= keep;
+    for (int t = 0; t < NT; ++t) o[j][t] *= keep;
     return frag_from_tiles<float>(x[0], x[1], 1.0f);
   };
   int k0 = wave * kKeys;
   if (k0 < last) {
     keys(k0);
-    const IO* y = static_cast<const IO*>(p.q) + (size_t)(s.q0 + min(row, s.nq - 1)) * p.q_stride + (size_t)h * DK + 8 * g;
 #pragma unroll
-    for (int st = 0; st < NS; ++st) {
-      if (DK % 32 == 0 || 32 * st + 8 * g < DK) load_values<8>(y + 32 * st, q[st].v);
-      else q[st].zero();
+    for (int j = 0; j < RT; ++j) {
+      const int row = min(s.r0 + 16 * j + c, s.nq - 1);
+      const IO* y = static_cast<const IO*>(p.q) + (size_t)(s.q0 + row) * p.q_stride + (size_t)h * DK + 8 * g;
+#pragma unroll
+      for (int st = 0; st < NS; ++st) {
+        if (DK % 32 == 0 || 32 * st + 8 * g < DK) load_values<8>(y + 32 * st, q[j][st].v);
+        else q[j][st].zero();
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
     values(k0);
     __builtin_amdgcn_sched_barrier(0);
     // (waited for here: a wait inside the loop would wait for the tiles' loads too)
 #pragma unroll
-    for (int st = 0; st < NS; ++st)
+    for (int j = 0; j < RT; ++j)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) asm volatile("" : "+v"(q[st].v[e]));
-    f32x4 x[2];
+      for (int st = 0; st < NS; ++st)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) asm volatile("" : "+v"(q[j][st].v[e]));
+    f32x4 x[RT][2];
+    Frag<float> pt[RT];
     for (; k0 + kKeys <= least; k0 += kPlainWaves * kKeys) {  // tiles that every query sees whole
       scores(x);
       keys(k0 + kPlainWaves * kKeys);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) x[u] *= scale;
-      const Frag<float> pt = powers(x);
+      for (int j = 0; j < RT; ++j) {
+        x[j][0] *= scale, x[j][1] *= scale;
+        pt[j] = powers(x[j], j);
+      }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         Frag<float> a;
 #pragma unroll
         for (int e = 0; e < 8; ++e) a.v[e] = v[e][t];
-        o[t] = mma(a, pt, o[t]);
+#pragma unroll
+        for (int j = 0; j < RT; ++j) o[j][t] = mma(a, pt[j], o[j][t]);
       }
       __builtin_amdgcn_sched_barrier(0);
       values(k0 + kPlainWaves * kKeys);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (k0 < last) {  // one that is cut: the borders of 16 queries lie in two tiles at most, of two waves
+    if (k0 < last) {  // one that is cut: the borders of up to 32 queries lie in two tiles at most, of two waves
       scores(x);
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int j = 0; j < RT; ++j) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[u][r] = k0 + 16 * u + 4 * g + r >= limit ? -__builtin_inff() : x[u][r] * scale;
-      const Frag<float> pt = powers(x);
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) x[j][u][r] = k0 + 16 * u + 4 * g + r >= limit[j] ? -__builtin_inff() : x[j][u][r] * scale;
+        pt[j] = powers(x[j], j);
+      }
       // What no query sees is left out.  Values that are not finite must not reach, as 0 v, queries that do not see them:
       // they are left out too, and counted for each query that does see them: its outputs become NaN.
-      Frag<float> see;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) see.v[e] = k0 + 16 * (e / 4) + 4 * g + e % 4 < limit ? 1.0f : 0.0f;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         Frag<float> a, n;
@@ -250,24 +269,34 @@ __global__ __launch_bounds__(64 * kPlainWaves, 2) void kda_attn_plain_kernel(Att
           n.v[e] = there & !fine ? 1.0f : 0.0f;
           odd |= there & !fine;
         }
-        o[t] = mma(a, pt, o[t]);
-        if (__builtin_expect(__any(odd), 0)) {
-          const f32x4 y = mma(n, see, (f32x4)0.0f);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) o[t][r] = y[r] > 0.0f ? __builtin_nanf("") : o[t][r];
+        for (int j = 0; j < RT; ++j) o[j][t] = mma(a, pt[j], o[j][t]);
+        if (__builtin_expect(__any(odd), 0)) {
+#pragma unroll
+          for (int j = 0; j < RT; ++j) {
+            Frag<float> see;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) see.v[e] = k0 + 16 * (e / 4) + 4 * g + e % 4 < limit[j] ? 1.0f : 0.0f;
+            const f32x4 y = mma(n, see, (f32x4)0.0f);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[j][t][r] = y[r] > 0.0f ? __builtin_nanf("") : o[j][t][r];
+          }
         }
       }
     }
   }
 
   // join the waves
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
-  if (g == 0) sm[wave][c] = m, sl[wave][c] = l;
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
+  for (int j = 0; j < RT; ++j) {
+    l[j] += __shfl_xor(l[j], 16);
+    l[j] += __shfl_xor(l[j], 32);
+    if (g == 0) sm[wave][16 * j + c] = m[j], sl[wave][16 * j + c] = l[j];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) so[wave][c][NT * (4 * g + r) + t] = o[t][r];
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) so[wave][16 * j + c][NT * (4 * g + r) + t] = o[j][t][r];
+  }
   __syncthreads();
   for (int i = tid; i < kRows * DV / 4; i += 64 * kPlainWaves) {
     const int r = i / (DV / 4), e = 4 * (i % (DV / 4));
@@ -788,8 +817,16 @@ hipError_t launch_fast(const AttnParams& p, hipStream_t s) {
 
 template <typename IO, int DK, int DV>
 hipError_t launch_plain(const AttnParams& p, hipStream_t s) {
-  const unsigned tiles = tiles_of<kRows>(p);
-  hipLaunchKernelGGL((kda_attn_plain_kernel<IO, DK, DV>), grid_of(p, tiles), dim3(64 * kPlainWaves), 0, s, p, tiles);
+  // 32 queries a workgroup take half as much from the L2, but want long sequences, and enough workgroups.  Against 16, us,
+  // fp32: 3,000 tokens of 8 + 2 heads of 128 196 / 242, 1,000 (256 workgroups) 44 / 51, 512 behind 1,488 of 16 heads 78 / 106;
+  // 20 sequences of 500 196 / 201; 10 of 300 62 / 56, 300 (80 workgroups) 23 / 16; of 8 + 8 heads of 64, 8 of 600 55 / 57.
+  const unsigned half = tiles_of<32>(p);
+  if (p.total_k / p.N >= 512 && (unsigned long long)half * p.Hq >= 256) {
+    hipLaunchKernelGGL((kda_attn_plain_kernel<IO, DK, DV, 2>), grid_of(p, half), dim3(64 * kPlainWaves), 0, s, p, half);
+    return hipGetLastError();
+  }
+  const unsigned tiles = tiles_of<16>(p);
+  hipLaunchKernelGGL((kda_attn_plain_kernel<IO, DK, DV, 1>), grid_of(p, tiles), dim3(64 * kPlainWaves), 0, s, p, tiles);
   return hipGetLastError();
 }
 

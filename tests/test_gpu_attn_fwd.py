@@ -90,6 +90,37 @@ def test_prefixes(gpu, dtype, d, hq):
     assert not o[a:a + 5].any() and o[a + 5:a + 9].any() and not o[a + 9:a + 49].any()
 
 
+# Long sequences, and enough heads: on the fp32 matrix cores a workgroup takes 32 queries.
+@pytest.mark.parametrize("dtype,dk,dv", [(F, 128, 128), (F, 64, 128), (F, 128, 64), (F, 16, 16), (F, 32, 64), (F, 64, 32), (BF, 32, 16), (BF, 16, 128), (BF, 128, 32)])
+@pytest.mark.parametrize("lens,lens_k", [([601, 530, 705], None), ([1, 1500], None), ([40, 301, 5, 200], [900, 300, 700, 650]), ([544], [513])])
+def test_long_sequences(gpu, dtype, dk, dv, lens, lens_k):
+    q, k, v = _qkv(gpu, 16, sum(lens), sum(lens_k or lens), 16, 4, dk, dv, dtype)
+    _check(q, k, v, lens, lens_k)
+
+
+@pytest.mark.parametrize("dtype,d", [(F, 64), (F, 128), (BF, 32)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_long_sequences_with_values_that_are_not_finite(gpu, dtype, d, bad):
+    kda = _kda()
+    lens = [600, 530, 700]
+    q, k, v = _qkv(gpu, 17, 1830, 1830, 16, 2, d, d, dtype)
+    clean = kda.kda_attn_fwd(q, k, v, cu_seqlens=_cu(lens, gpu))
+    for t, begin, end in ((0, 0, 600), (599, 0, 600), (600, 600, 1130), (615, 600, 1130), (616, 600, 1130), (631, 600, 1130), (1000, 600, 1130), (1829, 1130, 1830)):
+        for x in (k, v):
+            y = x.clone()
+            y[t, 1, 3] = bad
+            o = kda.kda_attn_fwd(q, y if x is k else k, y if x is v else v, cu_seqlens=_cu(lens, gpu))
+            same = torch.ones(1830, dtype=torch.bool, device=gpu)
+            same[t:end] = False
+            assert torch.equal(o[:, :8], clean[:, :8]), "another head"
+            # (a tile without the values that are not finite: the same sums)
+            assert torch.equal(o[same], clean[same]), f"before token {t}"
+            if x is v:
+                assert not torch.isfinite(o[t:end, 8:, 3]).any()
+                o[t:end, 8:, 3] = clean[t:end, 8:, 3]
+                assert torch.equal(o, clean), "another channel"
+
+
 @pytest.mark.parametrize("dtype,hq", [(BF, 2), (F, 2), (BF, 140)])
 def test_long_keys(gpu, dtype, hq):
     q, k, v = _qkv(gpu, 5, 40, 5003, hq, 1, 128, 128, dtype)
