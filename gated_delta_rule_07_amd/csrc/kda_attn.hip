@@ -630,12 +630,12 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, unsi
 }
 
 // ---- the same for few queries ---------------------------------------------------------------
-// Where the workgroups above would not fill the compute units -- a short prompt, or a few new tokens behind a long
-// prefix -- a workgroup takes 32 queries, and each of its four waves every fourth tile of 32 keys, through two
+// Where the workgroups above would not fill the compute units -- a short prompt, one prompt of few heads, or a few new
+// tokens behind a long prefix -- a workgroup takes 32 queries, and each of its four waves every fourth tile of 32 keys, through two
 // buffers of its own in LDS: no barrier until the waves are joined.
 
 constexpr int kSplitWaves = 4, kSplitKeys = 32;
-constexpr unsigned kFewTiles = 256;  // workgroups of it that the card's compute units hold at once
+constexpr unsigned kFewTiles = 256;  // workgroups of it that fill the compute units
 
 template <int DK, int DV>
 __global__ __launch_bounds__(64 * kSplitWaves, 1) void kda_attn_split_kernel(AttnParams p, unsigned tiles) {
@@ -802,11 +802,16 @@ unsigned tiles_of(const AttnParams& p) {
 template <int DK, int DV>
 hipError_t launch_fast(const AttnParams& p, hipStream_t s) {
   constexpr int NW = 4;
-  // Waves that share the keys against waves that share the queries, us, heads of 128: 1,000 tokens of 8 heads (256 workgroups
-  // of the first kind) 14.2 / 24.4, 2,000 (504) 38 / 43, 4,000 95 / 78; 300 tokens of 32 heads (320) 15.3 / 11.1; behind 32,000
-  // cached ones 128 tokens of 32 heads (128) 262 / 577, 512 (512) 663 / 582.
+  // Waves that share 32 queries against waves that share the keys, with 128 queries.  By what is measured the
+  // first take 4.9 us + 7.1e-3 (600 + keys of a query) for each time that they fill the compute units, the second, while they
+  // do not fill them, 5 us + 18.5e-3 for each key of a sequence; with heads of 64 it is 3.5e-3 (400 + keys) and 12.5e-3.
+  // us, heads of 128: 77 tokens of 8 heads 6.4 / 7.3; 1,000 tokens of 16 heads 19 / 24, of 32 37 / 26; 3,000 of 8 49 / 59; 8
+  // sequences of 300 of 8 heads 21 / 12; behind 8,000 cached tokens 128 of 32 heads 64 / 148.  Heads of 64: 2,000 tokens of
+  // 16 heads 24 / 30, 8 sequences of 300 of 8 heads 10.9 / 8.3.
   const unsigned few = tiles_of<32>(p);
-  if ((unsigned long long)few * p.Hq <= kFewTiles) {
+  const long long groups = (long long)few * p.Hq, nq = p.total_q / p.N, nk = p.total_k / p.N, seen = nk - std::min(nq, nk) / 2;
+  constexpr int FIXED = 200 + (DK + DV) * 25 / 16, TIMES = 1178 - 2 * (DK + DV);  // 600 and 666 = 2.6 kFewTiles; 400 and 922
+  if (groups <= kFewTiles || groups * (FIXED + seen) <= TIMES * nk) {
     hipLaunchKernelGGL((kda_attn_split_kernel<DK, DV>), grid_of(p, few), dim3(64 * kSplitWaves), 0, s, p, few);
     return hipGetLastError();
   }

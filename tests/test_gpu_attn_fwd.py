@@ -127,6 +127,22 @@ def test_long_keys(gpu, dtype, hq):
     _check(q, k, v, [40], [5003])
 
 
+# Which kernel runs depends on heads and lengths: queries shared by waves, and keys.
+@pytest.mark.parametrize("hq,hk", [(700, 1), (24, 3)])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64), (64, 128), (128, 64)])
+@pytest.mark.parametrize("n,m", [(40, 2003), (257, 1000)])
+def test_long_keys_of_many_heads(gpu, hq, hk, dk, dv, n, m):
+    q, k, v = _qkv(gpu, 18, n, m, hq, hk, dk, dv, BF)
+    _check(q, k, v, [n], [m])
+
+
+@pytest.mark.parametrize("d,hq,hk", [(128, 8, 1), (128, 16, 4), (64, 8, 8), (64, 16, 2), (128, 40, 8)])
+def test_long_prompts(gpu, d, hq, hk):
+    q, k, v = _qkv(gpu, 19, 1300, 1300, hq, hk, d, d, BF)
+    _check(q, k, v, [1300])
+    _check(q, k, v, [1, 1000, 299])
+
+
 @pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 128), (F, 64)])
 def test_strides(gpu, dtype, d):
     """Slices of a fused projection's rows, an output between other rows, [B,T] forms."""
