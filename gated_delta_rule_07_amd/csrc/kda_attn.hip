@@ -802,9 +802,9 @@ unsigned tiles_of(const AttnParams& p) {
 template <int DK, int DV>
 hipError_t launch_fast(const AttnParams& p, hipStream_t s) {
   constexpr int NW = 4;
-  // Waves that share 32 queries against waves that share the keys, with 128 queries.  By what is measured the
-  // first take 4.9 us + 7.1e-3 (600 + keys of a query) for each time that they fill the compute units, the second, while they
-  // do not fill them, 5 us + 18.5e-3 for each key of a sequence; with heads of 64 it is 3.5e-3 (400 + keys) and 12.5e-3.
+  // Workgroups of 32 queries, whose waves divide the keys, against those of 128, whose waves divide the queries.  By what is
+  // measured the first take 4.9 us + 7.1e-3 (600 + keys of a query) for each time that they fill the compute units, the second,
+  // while they do not fill them, 5 us + 18.5e-3 for each key of a sequence; with heads of 64 it is 3.5e-3 (400 + keys) and 12.5e-3.
   // us, heads of 128: 77 tokens of 8 heads 6.4 / 7.3; 1,000 tokens of 16 heads 19 / 24, of 32 37 / 26; 3,000 of 8 49 / 59; 8
   // sequences of 300 of 8 heads 21 / 12; behind 8,000 cached tokens 128 of 32 heads 64 / 148.  Heads of 64: 2,000 tokens of
   // 16 heads 24 / 30, 8 sequences of 300 of 8 heads 10.9 / 8.3.

@@ -466,8 +466,9 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_decode_kernel(DecodePlan 
 // groups of lanes take the parts in turn, so that the parts of even a long unit are in flight together.
 template <int DV>
 __global__ __launch_bounds__(256) void kda_attn_join_kernel(DecodePlan a) {
-  constexpr int NL = DV / 4, NG = 256 / NL;
-  __shared__ float sf[256], sl[4];
+  constexpr int NL = DV / 4, NG = 256 / NL, AHEAD = 8;
+  constexpr int NP = (kWorkers + 255) / 256;  // parts of a thread
+  __shared__ float sf[256 * NP], st[4], sl[4];
   __shared__ __attribute__((aligned(16))) float sy[NG][DV];
   const int w0 = blockIdx.x, tid = threadIdx.x, lane = tid % 64, c = blockIdx.y, e = 4 * (tid % NL), gr = tid / NL;
   const Join j = a.joins[w0];
@@ -478,28 +479,42 @@ __global__ __launch_bounds__(256) void kda_attn_join_kernel(DecodePlan a) {
   if (tk >= p.K) return;
   // worker w0's part is its first or its second, the others' their first
   auto part = [&](int i) { return a.parts + (2 * (size_t)(w0 + i) + (i == 0 ? j.slot : 0)) * part_floats(DV); };
-  // every wave finds the maximum; thread i holds the weights of the parts i, i + 256, ..
-  float top = -__builtin_inff();
-  for (int i = lane; i < n; i += 64) top = fmaxf(top, part(i)[kAttnColumns * DV + c]);
+  // thread i has the maxima and sums of the parts i, i + 256, ..; the first outputs are on their way meanwhile
+  float most[NP], sums[NP];
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const int i = tid + 256 * k;
+    const float* x = part(min(i, n - 1)) + kAttnColumns * DV + c;
+    most[k] = i < n ? x[0] : -__builtin_inff();
+    sums[k] = i < n ? x[kAttnColumns] : 0.0f;
+  }
+  auto output = [&](int i) { return *reinterpret_cast<const f32x4*>(part(i) + c * DV + e); };
+  f32x4 first[AHEAD];
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) first[k] = output(min(gr + k * NG, n - 1));
+  float top = most[0];
+#pragma unroll
+  for (int k = 1; k < NP; ++k) top = fmaxf(top, most[k]);
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) top = fmaxf(top, __shfl_xor(top, m));
+  if (lane == 0) st[tid / 64] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(st[0], st[1]), fmaxf(st[2], st[3]));
   const float base = top == -__builtin_inff() ? 0.0f : top;
-  f32x4 y = (f32x4)0.0f;
   float sum = 0.0f;
-  for (int i0 = 0; i0 < n; i0 += 256) {
-    float f = 0.0f;
-    if (i0 + tid < n) {
-      const float* x = part(i0 + tid) + kAttnColumns * DV + c;
-      f = __builtin_amdgcn_exp2f(x[0] - base);
-      sum += f * x[kAttnColumns];
-    }
-    __syncthreads();
-    sf[tid] = f;
-    __syncthreads();
-    const int some = min(n - i0, 256);
-#pragma unroll 8
-    for (int i = gr; i < some; i += NG) y += sf[i] * *reinterpret_cast<const f32x4*>(part(i0 + i) + c * DV + e);
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const float f = __builtin_amdgcn_exp2f(most[k] - base);
+    sf[tid + 256 * k] = f;
+    sum += f * sums[k];
   }
+  __syncthreads();
+  f32x4 y = (f32x4)0.0f;
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k)
+    if (gr + k * NG < n) y += sf[gr + k * NG] * first[k];
+#pragma unroll 8
+  for (int i = gr + AHEAD * NG; i < n; i += NG) y += sf[i] * output(i);
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) sum += __shfl_xor(sum, m);
   if (lane == 0) sl[tid / 64] = sum;
