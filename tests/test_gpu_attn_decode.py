@@ -138,6 +138,13 @@ def test_long(gpu, cache, dtype):
     _check(gpu, lay, [70001, 3, 0, 5000, 129], dtype=dtype, o_dtype=F)
 
 
+@pytest.mark.parametrize("n", [2049, 8193, 32767, 65537, 75393, 140001])
+def test_units_that_many_workgroups_share(gpu, n):
+    """One head: up to 512 parts to join."""
+    kda = _kda()
+    _check(gpu, kda.KVLayout(E, 128, 1, 64, 64), [n], K=2, hq=2, seed=40)
+
+
 @pytest.mark.parametrize("wide", [False, True])
 def test_padding_and_rows(gpu, wide):
     lay = _kda().KVLayout(E, 16, 2, 64, 64)
