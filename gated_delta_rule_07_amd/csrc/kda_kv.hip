@@ -10,6 +10,11 @@
 // maximum and the cosines and sines (in LDS) serve all heads; a wave takes one head's keys or values.
 // Workgroups behind the pages turn the queries.  A lane holds two pieces of 8 values of a row, those
 // that turn together, so that a rotation exchanges nothing between lanes.
+// Angles are reduced in fp64, the rest is fp32; values are rounded once, to the page's or the output's type.
+// Measured: 65,536 tokens of 32 + 8 heads of 128 in 16 sequences onto e4m3 pages 290 us, 5.1 TB/s of the bytes that it cannot do
+// without and 5.9 of those it moves (rows of a page beyond the first 32 are fetched again for the codes, when the scale
+// is known; sharing a head among waves, so that all rows stay in registers, gains 2% there and costs 8% with few heads).  256
+// sequences of one token 10 us, one 3.3: the latency of lengths, table and page, and of the look for pages that others write.
 #include <algorithm>
 
 #include "kda_kv_device.h"
@@ -425,7 +430,8 @@ __device__ __forceinline__ void store32(char* p, const u32x4& a, const u32x4& b,
 }
 
 // A lane moves V values (16 bytes of the page) of a token's head: always the same ones, of one token after another.
-// Four neighbouring lanes always move neighbours of one row.
+// Four neighbouring lanes always move neighbours of one row.  Bound by memory: 70,001 tokens of 8 heads of 128, e4m3 to bf16, 91 us
+// (4.8 TB/s, two thirds of it stores; 16, 32 and 64 tokens a workgroup 6 to 17% slower); 517 tokens of 4 heads 4.9 us, latency.
 template <typename OUT, bool E4, bool PAST>
 __global__ __launch_bounds__(kThreads) void kda_kv_read_kernel(ReadParams p) {
   __shared__ int page[kReadTokens], slot[kReadTokens];
