@@ -7,7 +7,7 @@
 // Short ones are taken whole, a workgroup each.  Else the work is cut into granules of 128 keys, and every workgroup takes an
 // equal run of them, whatever the sequences' lengths: a run that holds a unit whole writes its output, others leave (o, m, l) in
 // the workspace for a second kernel.  Within a workgroup each wave streams its own 32-key tiles from
-// memory into registers, the next one's loads before this one's work -- no LDS and no barrier until a unit ends:
+// memory into registers -- no LDS and no barrier until a unit ends:
 //   S^T = K Q^T with a lane holding 16 bytes of a key's row; P^T as it comes out is the operand of
 //   O^T = V^T P^T, whose other operand wants 8 keys' values of one channel in a lane: a lane loads
 //   8 channels of 8 keys and transposes them in registers (byte permutes, then the conversion to bf16).
@@ -16,8 +16,9 @@
 // (With bf16 queries the probabilities are rounded to bf16; maxima, sums and outputs are fp32 always.)
 // Measured, 32 + 8 heads of 128 in e4m3: 256 sequences of up to 9,000 tokens 462 us (5.6 TB/s, where reads alone reach 5.2 to 6.3
 // and copies 5.4), 4 drafts behind 1,000,003 tokens 358 us (5.7), of which the second kernel takes 7 and 8; one sequence of 903
-// tokens of 8 + 2 heads of 64 9.4 us, bound by the latency of a chain of loads: lengths, page numbers, keys.  Vector instructions (conversions,
-// byte permutes) take 27% of the cycles, the matrix cores 7%.  Slower: three or four waves a SIMD (they spill), a third tile in flight.
+// tokens of 8 + 2 heads of 64 9.0 us, bound by the latency of a chain of loads: lengths, page numbers, keys.  Vector instructions (conversions,
+// byte permutes) take 27% of the cycles, the matrix cores 7%.  Slower: four waves a SIMD (they
+// spill), 768 workgroups that share the granules (374 and 484 us).
 #include <algorithm>
 
 #include "kda_kv_device.h"
@@ -109,11 +110,11 @@ __device__ __forceinline__ float column_max(float x) {
   return fmaxf(__builtin_bit_cast(float, c), __builtin_bit_cast(float, d));
 }
 
+// (three waves a SIMD where the registers do without spilling: 256 sequences of up to 300 tokens of 32 + 8 heads 36 us, 43 with two)
 template <int NW, int NT, bool E4, int DK, int DV>
-__global__ __launch_bounds__(64 * NW, 2) void kda_attn_decode_kernel(DecodePlan a) {
+__global__ __launch_bounds__(64 * NW, NW == kWaves && NT == 1 && E4 ? 3 : 2) void kda_attn_decode_kernel(DecodePlan a) {
   constexpr int kThreads = 64 * NW, kGranule = NW * kTile;
   using T = Tile<E4, DK, DV>;
-  constexpr int RING = 2;  // tiles of a wave in flight and in work
   constexpr int NM = DV / 16, NS = DK / 32;
   constexpr int ES = E4 ? 1 : 2, CW = 4 / ES;  // bytes of an element, elements of a dword
   __shared__ __attribute__((aligned(16))) float so[NW][kAttnColumns][DV + 4];
@@ -403,20 +404,13 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_decode_kernel(DecodePlan 
       }
     };
     int k0 = g0 * kGranule + kTile * wave;
-    T ring[RING];
-#pragma unroll
-    for (int i = 0; i + 1 < RING; ++i)
-      if (k0 + i * kGranule < kend) ring[i] = load(k0 + i * kGranule, pages_of(k0 + i * kGranule));
-    Pages pg = pages_of(k0 + (RING - 1) * kGranule);
-    while (k0 < kend) {
-#pragma unroll
-      for (int i = 0; i < RING; ++i) {
-        if (k0 + (RING - 1) * kGranule < kend) ring[(i + RING - 1) % RING] = load(k0 + (RING - 1) * kGranule, pg);
-        pg = pages_of(k0 + RING * kGranule);  // (a turn before their tile's loads need them)
-        compute(k0, ring[i]);
-        k0 += kGranule;
-        if (k0 >= kend) break;
-      }
+    // (the waves of a SIMD overlap one's loads with another's work: tiles loaded ahead take registers and make the code longer,
+    // and were slower: 447 against 431 us on 128 sequences of up to 6,000 tokens in bf16, 10.0 against 9.3 on one of 903)
+    Pages pg = pages_of(k0);
+    for (; k0 < kend; k0 += kGranule) {
+      T cur = load(k0, pg);
+      pg = pages_of(k0 + kGranule);  // (a turn before their tile's loads need them)
+      compute(k0, cur);
     }
 
     // join the waves
