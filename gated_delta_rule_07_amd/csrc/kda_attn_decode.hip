@@ -526,10 +526,14 @@ __global__ __launch_bounds__(256) void kda_attn_join_kernel(DecodePlan a) {
   store4(p, (((size_t)b * p.K + tk) * p.Hq + h * a.G + c2 % a.G) * DV + e, y * (sum == 0.0f ? 0.0f : 1.0f / sum));
 }
 
-// Whether a call takes its units whole, a workgroup each: no workspace and no second launch.  With 32 + 8 heads of 128 in
-// e4m3, whole against shared, us: 1 sequence (8 units) of 1,000 tokens 10.8 / 11.4, of 2,000 16.3 / 11.4; 16 sequences of
-// 2,000 17.8 / 22.0, of 4,000 33.0 / 30.1; 64 of 4,000 85.8 / 89.6, of 8,000 163 / 158; 256 of 300 to 9,000 480 / 464.
-bool takes_whole(long long tokens, long long units) { return tokens <= 1536 || (tokens <= 4096 && units >= 128); }
+// Whether a call takes its units whole, a workgroup each: no workspace and no second launch.  It knows what rows of the table
+// hold, not how long the sequences are: longer rows are shared, lest one long sequence among short ones be one workgroup's.
+// With 32 + 8 heads of 128 in e4m3, whole against shared, us: 1 sequence (8 units) of 1,000 tokens 11.7 / 12.5, of 1,500 14.5 /
+// 12.5; 4 of 1,000 11.7 / 13.4, of 1,500 15.2 / 14.3; 8 of 1,500 15.5 / 16.3, of 2,000 18.2 / 18.2; 16 of 2,000 18.9 / 23.6, of
+// 4,000 40 / 38; 20 of 4,000 41 / 47; 64 of 4,000 98 / 108; 256 of 300 to 9,000 510 / 508.
+bool takes_whole(long long tokens, long long units) {
+  return tokens <= 1280 || (tokens <= 2048 && units >= 64) || (tokens <= 4096 && units >= 128);
+}
 bool takes_whole(int B, int K, int Hq, int H, int page_tokens, int width) {
   return takes_whole((long long)page_tokens * width, (long long)B * columns(K, Hq / H) * H);
 }
