@@ -326,8 +326,8 @@ __global__ __launch_bounds__(64 * kPlainWaves, RT == 1 ? 2 : 1) void kda_attn_pl
 // LDS rows are dense; their 16-byte pieces are exchanged (xor with bits of the row) so that the lanes of a
 // read fall on different banks (no conflicts in the counters).
 // Probabilities are rounded to bf16 for the product with V and summed as rounded, in fp32; scores, maxima, sums and outputs are fp32.
-// Measured, 32 + 8 heads of 128: 16,384 tokens 2.05 ms (1.07 PFLOP/s, where a matrix product of 8192^3 reaches 1.25), 24,961 tokens
-// in 16 sequences 482 us (0.84).  Bound by the matrix cores and the exponentials beside them: the cores are busy 56% of the
+// Measured, 32 + 8 heads of 128: 16,384 tokens 2.02 ms (1.09 PFLOP/s, where a matrix product of 8192^3 reaches 1.25), 24,961 tokens
+// in 16 sequences 471 us (0.86).  Bound by the matrix cores and the exponentials beside them: the cores are busy 56% of the
 // cycles at a clock that the load holds at 1.8 GHz, vector instructions 43%, with two waves a SIMD to overlap them (256 registers
 // each).  The packed batch loses 6% to cut tiles and the rest to its 6,900 workgroups' first loads and last stores.
 // Slower: eight waves and 256 queries a workgroup (packed 620 us), scores a tile ahead of the probabilities (566).

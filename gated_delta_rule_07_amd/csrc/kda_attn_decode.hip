@@ -14,11 +14,11 @@
 // Codes convert to bf16 exactly; the page's scales multiply scores and probabilities instead.
 // fp32 queries are split into three bf16 terms, and so are their probabilities: 24 bits on bf16 matrix cores.
 // (With bf16 queries the probabilities are rounded to bf16; maxima, sums and outputs are fp32 always.)
-// Measured, 32 + 8 heads of 128 in e4m3: 256 sequences of up to 9,000 tokens 462 us (5.6 TB/s, where reads alone reach 5.2 to 6.3
-// and copies 5.4), 4 drafts behind 1,000,003 tokens 358 us (5.7), of which the second kernel takes 7 and 8; one sequence of 903
-// tokens of 8 + 2 heads of 64 9.0 us, bound by the latency of a chain of loads: lengths, page numbers, keys.  Vector instructions (conversions,
-// byte permutes) take 27% of the cycles, the matrix cores 7%.  Slower: four waves a SIMD (they
-// spill), 768 workgroups that share the granules (374 and 484 us).
+// Measured, 32 + 8 heads of 128 in e4m3: 256 sequences of up to 9,000 tokens 465 us (5.6 TB/s, where reads alone reach 5.2 to 6.3
+// and copies 5.4), 4 drafts behind 1,000,003 tokens 363 us (5.6), of which the second kernel takes 7 and 8; one sequence of 903
+// tokens of 8 + 2 heads of 64 8.9 us, bound by the latency of a chain of loads: lengths, page numbers, keys.  Vector
+// instructions (conversions, byte permutes) take 28% of the cycles, the matrix cores 7.5%.  Slower: four waves a SIMD (they
+// spill), 768 workgroups that share the granules (484 and 374 us).
 #include <algorithm>
 
 #include "kda_kv_device.h"
