@@ -143,6 +143,14 @@ def test_long_prompts(gpu, d, hq, hk):
     _check(q, k, v, [1, 1000, 299])
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 32), (F, 64)])
+@pytest.mark.parametrize("hq,hk", [(3, 3), (20, 5), (24, 6), (7, 7), (12, 12), (80, 80), (66, 3)])
+def test_heads_that_dies_share(gpu, dtype, d, hq, hk):
+    """Key heads that do not divide among eight: every tile of every head is somebody's."""
+    q, k, v = _qkv(gpu, 20, 711, 711, hq, hk, d, d, dtype)
+    _check(q, k, v, [3, 0, 500, 208])
+
+
 @pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 128), (F, 64)])
 def test_strides(gpu, dtype, d):
     """Slices of a fused projection's rows, an output between other rows, [B,T] forms."""
