@@ -55,6 +55,8 @@ kda_status stride_ok(long long* stride, int n, int H, int d, int e) {
   return *stride * e % 16 ? KDA_ERR_MISALIGNED : KDA_OK;
 }
 bool finite(float x) { return x - x == 0.0f; }
+// Decode counts a row's tokens in 32 bits, rounded up to runs of up to 256 and with a run ahead.
+bool decode_row_ok(int width, int pt) { return (long long)width * pt <= (1LL << 31) - 512; }
 
 }  // namespace
 
@@ -182,7 +184,7 @@ kda_status kda_attn_decode_plan(kda_dtype kv_dtype, int page_tokens, int width, 
   if (!kv_dtype_ok(raw_enum(kv_dtype))) return KDA_ERR_DTYPE;
   if (B < 1 || B > KDA_MAX_PAGED_SEQS || K < 1 || K > KDA_MAX_ATTN_TOKENS || width < 1 || !heads_ok(H_q, H_kv)) return KDA_ERR_SHAPE;
   if (!page_tokens_ok(page_tokens) || !head_dim_ok(d_k) || !head_dim_ok(d_v)) return KDA_ERR_UNSUPPORTED;
-  if ((long long)width * page_tokens >= (1LL << 31)) return KDA_ERR_SHAPE;
+  if (!decode_row_ok(width, page_tokens)) return KDA_ERR_SHAPE;
   if (!workspace_bytes) return KDA_ERR_NULL;
   *workspace_bytes = kda::attn_decode_workspace(B, K, H_q, H_kv, d_v, page_tokens, width);
   return KDA_OK;
@@ -198,7 +200,8 @@ kda_status kda_attn_decode(const void* q, kda_dtype q_dtype, float scale, const 
   const kda_status bad = cache_of(pool, raw_enum(kv_dtype), n_pages, page_tokens, table, n_rows, width, rows, B, H_kv, d_k, d_v, &c);
   if (bad != KDA_OK) return bad;
   // 32-bit counts: granules of 128 tokens over the sequences, and threads (a workgroup of up to 512 for each unit)
-  if ((long long)B * (((long long)width * page_tokens + 127) / 128) >= (1LL << 31) || (long long)B * K * H_q > (1LL << 22))
+  if (!decode_row_ok(width, page_tokens) || (long long)B * (((long long)width * page_tokens + 127) / 128) >= (1LL << 31) ||
+      (long long)B * K * H_q > (1LL << 22))
     return KDA_ERR_SHAPE;
   const size_t need = kda::attn_decode_workspace(B, K, H_q, H_kv, d_v, page_tokens, width);
   if (!q || !lens || !o || (need && !workspace)) return KDA_ERR_NULL;

@@ -706,7 +706,8 @@ kda_status kda_kv_read(const void* pool, kda_dtype kv_dtype, int n_pages, int pa
  *   workspace: device memory of workspace_bytes bytes (kda_attn_decode_plan), 16-byte aligned;
  *         its contents on entry do not matter.  NULL when the plan says 0.  Calls that may run
  *         at the same time need one each.                                   (written)
- *   B: 1 .. KDA_MAX_PAGED_SEQS, K: 1 .. KDA_MAX_ATTN_TOKENS, B * K * H_q <= 2^22
+ *   B: 1 .. KDA_MAX_PAGED_SEQS, K: 1 .. KDA_MAX_ATTN_TOKENS, B * K * H_q <= 2^22,
+ *   width * page_tokens <= 2^31 - 512 and B * (width * page_tokens / 128, rounded up) < 2^31
  *   (KDA_ERR_SHAPE).  The cache is read once for every 16 rows of queries that share a head
  *   (there are K * H_q / H_kv of them).
  *
