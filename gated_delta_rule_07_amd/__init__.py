@@ -5,6 +5,12 @@ Argument marshalling only: every step of the operator runs in the HIP kernels of
 ABI (``include/kda.h``).  PyTorch supplies device memory and the current HIP
 stream; nothing here computes any part of the recurrence, and there is no CPU
 fallback: if the library is missing the calls raise.
+
+Tensors that a call makes (outputs that are not given, workspaces) are memory of the
+stream that it runs on: ``stream``, or the current one.  As with any tensor made under
+``torch.cuda.stream(stream)``, a program that uses them on another stream orders its
+work behind the call, and drops them only when that work is done (or after
+``record_stream``).
 """
 from __future__ import annotations
 
@@ -201,7 +207,19 @@ def _stream(device, stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _prefill_prep(q, k, v, alpha, beta, S0, o, S_T, o_dtype, want_state):
+def _made(shape, dtype, device, stream, value=None):
+    """A new tensor for a call on `stream`, holding `value` throughout where that is given (by a fill on the stream).  It is
+    memory of that stream: a block of another one's could still be in use there, and would be used there again as soon as the
+    tensor is gone, while the call may still be writing it."""
+    if stream is not None and stream.cuda_stream != _raw_stream(device.index):
+        with torch.cuda.stream(stream):
+            return _made(shape, dtype, device, None, value)
+    if value is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return torch.full(shape, value, dtype=dtype, device=device)
+
+
+def _prefill_prep(q, k, v, alpha, beta, S0, o, S_T, o_dtype, want_state, stream):
     _check(q, "q")
     dev = q.device
     for t, n in ((k, "k"), (v, "v")):
@@ -221,13 +239,13 @@ def _prefill_prep(q, k, v, alpha, beta, S0, o, S_T, o_dtype, want_state):
         if S0.shape != (B, H, dk, dv):
             raise ValueError("libkda: S0 must be [B,H,d_k,d_v]")
     if o is None:
-        o = torch.empty(B, T, H, dv, device=dev, dtype=o_dtype)
+        o = _made((B, T, H, dv), o_dtype, dev, stream)
     else:
         _check(o, "o", None, dev)
         if o.shape != (B, T, H, dv):
             raise ValueError("libkda: o must be [B,T,H,d_v]")
     if want_state and S_T is None:
-        S_T = torch.empty(B, H, dk, dv, device=dev, dtype=torch.float32)
+        S_T = _made((B, H, dk, dv), torch.float32, dev, stream)
     elif S_T is not None:
         _check(S_T, "S_T", torch.float32, dev)
         if S_T.shape != (B, H, dk, dv):
@@ -245,7 +263,7 @@ def kda_chunk_fwd(q, k, v, alpha, beta, S0=None, *, chunk: int = 64, o=None, S_T
     ``o``).  ``S_T`` may be preallocated (it may be ``S0`` for an in-place update).
     """
     lib = load_library()
-    dev, (B, T, H, dk, dv), o, S_T = _prefill_prep(q, k, v, alpha, beta, S0, o, S_T, o_dtype, want_state)
+    dev, (B, T, H, dk, dv), o, S_T = _prefill_prep(q, k, v, alpha, beta, S0, o, S_T, o_dtype, want_state, stream)
     st = lib.kda_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _dtype_code(q), _ptr(alpha), _ptr(beta),
                            _ptr(S0), _ptr(o), _dtype_code(o), _ptr(S_T), B, T, H, dk, dv, int(chunk),
                            _stream(dev, stream))
@@ -265,11 +283,11 @@ def kda_chunk_fwd_snapshots(q, k, v, alpha, beta, S0=None, *, snap_tokens, chunk
     at most ``KDA_MAX_SNAPSHOTS`` of them.  Other arguments as ``kda_chunk_fwd``.
     """
     lib = load_library()
-    dev, (B, T, H, dk, dv), o, S_T = _prefill_prep(q, k, v, alpha, beta, S0, o, S_T, o_dtype, want_state)
+    dev, (B, T, H, dk, dv), o, S_T = _prefill_prep(q, k, v, alpha, beta, S0, o, S_T, o_dtype, want_state, stream)
     pos = [int(t) for t in snap_tokens]
     n = len(pos)
     if snaps is None:
-        snaps = torch.empty(B, H, n, dk, dv, device=dev, dtype=torch.float32)
+        snaps = _made((B, H, n, dk, dv), torch.float32, dev, stream)
     else:
         _check(snaps, "snaps", torch.float32, dev)
         if snaps.shape != (B, H, n, dk, dv):
@@ -305,13 +323,13 @@ def kda_chunk_fwd_varlen(q, k, v, alpha, beta, cu_seqlens, S0=None, *, chunk: in
         raise ValueError("libkda: S_T must be [N,H,d_k,d_v]")
     # the packed rows are one [1,total_T,...] batch for the shared checks
     dev, (_, T, H, dk, dv), o4, _ = _prefill_prep(q[None], k[None], v[None], alpha[None], beta[None], None,
-                                                  None if o is None else o[None], None, o_dtype, False)
+                                                  None if o is None else o[None], None, o_dtype, False, stream)
     if S0 is not None:
         _check(S0, "S0", torch.float32, dev)
         if S0.shape != (N, H, dk, dv):
             raise ValueError("libkda: S0 must be [N,H,d_k,d_v]")
     if want_state and S_T is None:
-        S_T = torch.empty(N, H, dk, dv, device=dev, dtype=torch.float32)
+        S_T = _made((N, H, dk, dv), torch.float32, dev, stream)
     elif S_T is not None:
         _check(S_T, "S_T", torch.float32, dev)
         if S_T.shape != (N, H, dk, dv):
@@ -330,7 +348,7 @@ def kda_chunk_fwd_gated(q, k, v, z, A, beta, S0=None, *, chunk: int = 64, o=None
     the kernels.  z: [B,T,H,d_k] in q's dtype; A: [H] fp32.  Returns ``(o, S_T)``;
     other arguments as ``kda_chunk_fwd``."""
     lib = load_library()
-    dev, (B, T, H, dk, dv), o, S_T = _prefill_prep(q, k, v, None, beta, S0, o, S_T, o_dtype, want_state)
+    dev, (B, T, H, dk, dv), o, S_T = _prefill_prep(q, k, v, None, beta, S0, o, S_T, o_dtype, want_state, stream)
     _check(z, "z", q.dtype, dev)
     _check(A, "A", torch.float32, dev)
     if z.shape != q.shape or A.shape != (H,):
@@ -366,10 +384,10 @@ def kda_chunk_fwd_split(q, k, v, alpha, beta, S0=None, *, parts: int = 0, num_cu
     workspace (a uint8 device tensor) is allocated here when not given.  Returns
     ``(o, S_T)``; other arguments as ``kda_chunk_fwd``."""
     lib = load_library()
-    dev, (B, T, H, dk, dv), o, S_T = _prefill_prep(q, k, v, alpha, beta, S0, o, S_T, o_dtype, want_state)
+    dev, (B, T, H, dk, dv), o, S_T = _prefill_prep(q, k, v, alpha, beta, S0, o, S_T, o_dtype, want_state, stream)
     n, need = kda_chunk_fwd_split_plan(q.dtype, B, T, H, dk, dv, chunk=chunk, parts=parts, num_cus=num_cus)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _made(need, torch.uint8, dev, stream)
     if workspace is not None:
         _check(workspace, "workspace", torch.uint8, dev)
     st = lib.kda_chunk_fwd_split(_ptr(q), _ptr(k), _ptr(v), _dtype_code(q), _ptr(alpha), _ptr(beta),
@@ -390,7 +408,7 @@ def kda_chunk_fwd_split_noalloc(q, k, v, alpha, beta, S0=None, *, parts: int = 0
     Calls that overlap on one GPU race.  Returns ``(o, S_T)``; other arguments as
     ``kda_chunk_fwd_split``."""
     lib = load_library()
-    dev, (B, T, H, dk, dv), o, S_T = _prefill_prep(q, k, v, alpha, beta, S0, o, S_T, o_dtype, want_state)
+    dev, (B, T, H, dk, dv), o, S_T = _prefill_prep(q, k, v, alpha, beta, S0, o, S_T, o_dtype, want_state, stream)
     st = lib.kda_chunk_fwd_split_noalloc(_ptr(q), _ptr(k), _ptr(v), _dtype_code(q), _ptr(alpha), _ptr(beta),
                                          _ptr(S0), _ptr(o), _dtype_code(o), _ptr(S_T), B, T, H, dk, dv, int(chunk),
                                          int(parts), int(num_cus), _stream(dev, stream))
@@ -419,7 +437,7 @@ def kda_decode_step_gated(q, k, v, z, A, beta, S, *, o=None, o_dtype=torch.float
     if S.shape != (B, H, dk, dv):
         raise ValueError("libkda: S must be [B,H,d_k,d_v]")
     if o is None:
-        o = torch.empty(B, H, dv, device=dev, dtype=o_dtype)
+        o = _made((B, H, dv), o_dtype, dev, stream)
     else:
         _check(o, "o", None, dev)
         if o.shape != (B, H, dv):
@@ -452,7 +470,7 @@ def kda_decode_step(q, k, v, alpha, beta, S, *, o=None, o_dtype=torch.float32, s
     if S.shape != (B, H, dk, dv):
         raise ValueError("libkda: S must be [B,H,d_k,d_v]")
     if o is None:
-        o = torch.empty(B, H, dv, device=dev, dtype=o_dtype)
+        o = _made((B, H, dv), o_dtype, dev, stream)
     else:
         _check(o, "o", None, dev)
         if o.shape != (B, H, dv):
@@ -487,13 +505,13 @@ def kda_decode_verify(q, k, v, alpha, beta, S, *, o=None, u=None, o_dtype=torch.
     if S.shape != (B, H, dk, dv):
         raise ValueError("libkda: S must be [B,H,d_k,d_v]")
     if o is None:
-        o = torch.empty(B, K, H, dv, device=dev, dtype=o_dtype)
+        o = _made((B, K, H, dv), o_dtype, dev, stream)
     else:
         _check(o, "o", None, dev)
         if o.shape != (B, K, H, dv):
             raise ValueError("libkda: o must be [B,K,H,d_v]")
     if u is None:
-        u = torch.empty(B, H, K, dv, device=dev, dtype=torch.float32)
+        u = _made((B, H, K, dv), torch.float32, dev, stream)
     else:
         _check(u, "u", torch.float32, dev)
         if u.shape != (B, H, K, dv):
@@ -607,15 +625,6 @@ def _may(t, name, dtype, index, shape):
     return None if t is None else _need(t, name, dtype, index, shape)
 
 
-def _filled(shape, dtype, device, value, stream):
-    """A new tensor for a call that may pass over some of its rows: `value` throughout, filled on the call's stream."""
-    if stream is None:
-        return torch.full(shape, value, dtype=dtype, device=device)
-    t = torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return t.fill_(value)
-
-
 def _io_code(t, name):
     """kda_dtype of a bf16 or fp32 tensor."""
     code = _CODES.get(t.dtype)
@@ -688,12 +697,12 @@ def kda_qk_norm(q, k=None, *, norm: str = "l2", q_weight=None, k_weight=None, ep
     if out_code is None:
         raise TypeError(f"libkda: outputs must be bfloat16 or float32, got {out_dtype}")
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        q_out = _made(q.shape, out_dtype, q.device, stream)
     qop, qos = _head_out(q_out, "q_out", q, dev, out_dtype)
     kop, kos = None, 0
     if k is not None:
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=out_dtype, device=k.device)
+            k_out = _made(k.shape, out_dtype, k.device, stream)
         kop, kos = _head_out(k_out, "k_out", k, dev, out_dtype)
     elif k_out is not None:
         raise ValueError("libkda: k_out without k")
@@ -724,9 +733,9 @@ def _move_list(moves, n_moves, room, t, stream):
     """moves (pairs of -1) and n_moves, made on t's device where they are not given, and their addresses."""
     dev = t.get_device()
     if moves is None:
-        moves = _filled((max(room, 1), 2), _I32, t.device, -1, stream)
+        moves = _made((max(room, 1), 2), _I32, t.device, stream, -1)
     if n_moves is None:
-        n_moves = torch.empty(1, dtype=_I32, device=t.device)
+        n_moves = _made(1, _I32, t.device, stream)
     rows = moves.shape[0] if _tensor(moves, "moves").dim() == 2 else 0
     mp, np_ = _need(moves, "moves", _I32, dev, (max(rows, room), 2)), _need(n_moves, "n_moves", _I32, dev, (1,))
     return moves, n_moves, mp, np_
@@ -759,9 +768,9 @@ def kda_cache_compact(table, ref, *, table_out=None, ref_out=None, moves=None, n
     ``table_out=table`` and ``ref_out=ref`` for an update in place; ``moves`` (room for n_pages // 2 pairs) is what
     ``kda_cache_copy`` has to carry out on each pool."""
     dev, R, W, P, tp, rp = _table(table, ref)
-    table_out = torch.empty_like(table) if table_out is None else table_out
-    ref_out = torch.empty_like(ref) if ref_out is None else ref_out
-    n_live = torch.empty(1, dtype=_I32, device=table.device) if n_live is None else n_live
+    table_out = _made((R, W), _I32, table.device, stream) if table_out is None else table_out
+    ref_out = _made((P,), _I32, ref.device, stream) if ref_out is None else ref_out
+    n_live = _made(1, _I32, table.device, stream) if n_live is None else n_live
     to, ro = _need(table_out, "table_out", _I32, dev, (R, W)), _need(ref_out, "ref_out", _I32, dev, (P,))
     moves, n_moves, mp, np_ = _move_list(moves, n_moves, max(P // 2, 1), table, stream)
     _run("kda_cache_compact", dev, stream, tp, rp, to, ro, mp, np_, _need(n_live, "n_live", _I32, dev, (1,)), R, W, P)
@@ -820,7 +829,7 @@ def kda_decode_step_paged(q, k, v, alpha, beta, pool, pages_in, pages_out=None, 
     P, poolp = _state_pool(pool, H, dk, dv, dev)
     ip, op = _need(pages_in, "pages_in", _I32, dev, (B,)), _may(pages_out, "pages_out", _I32, dev, (B,))
     if o is None:
-        o = _filled((B, H, dv), o_dtype, q.device, 0.0, stream)
+        o = _made((B, H, dv), o_dtype, q.device, stream, 0.0)
     odt = _tensor(o, "o").dtype
     _run("kda_decode_step_paged", dev, stream, qp, kp, vp, code, ap, zp, Ap, bp, poolp, P, ip, op,
          _need(o, "o", odt, dev, (B, H, dv)), _io_code(o, "o"), B, H, dk, dv)
@@ -851,10 +860,10 @@ def kda_tree_verify(q, k, v, alpha, beta, pool, pages, parents, n_nodes=None, *,
     whole = pages is None and n_nodes is None  # (every row is written)
     if o is None:
         shape = (B, K, H, dv)
-        o = torch.empty(shape, device=q.device, dtype=o_dtype) if whole else _filled(shape, o_dtype, q.device, 0.0, stream)
+        o = _made(shape, o_dtype, q.device, stream, None if whole else 0.0)
     if u is None:
         shape = (B, H, K, dv)
-        u = torch.empty(shape, device=q.device, dtype=_F32) if whole else _filled(shape, _F32, q.device, 0.0, stream)
+        u = _made(shape, _F32, q.device, stream, None if whole else 0.0)
     odt = _tensor(o, "o").dtype
     _run("kda_tree_verify", dev, stream, qp, kp, vp, code, ap, bp, poolp, P, pg, pa, nn, _need(o, "o", odt, dev, (B, K, H, dv)),
          _io_code(o, "o"), _need(u, "u", _F32, dev, (B, H, K, dv)), B, K, H, dk, dv)
@@ -967,7 +976,7 @@ def kda_attn_fwd(q, k, v, *, scale=None, cu_seqlens=None, cu_seqlens_k=None, o=N
     cp, ckp = _may(cu_seqlens, "cu_seqlens", _I32, dev, (N + 1,)), _may(cu_seqlens_k, "cu_seqlens_k", _I32, dev, (N + 1,))
     if o is None:
         shape, odt = (*q.shape[:-1], dv), dt if o_dtype is None else o_dtype
-        o = torch.empty(shape, dtype=odt, device=q.device) if cp is None else _filled(shape, odt, q.device, 0.0, stream)
+        o = _made(shape, odt, q.device, stream, None if cp is None else 0.0)
     op, _, _, _, os = _head_rows(_tensor(o, "o"), "o", o.dtype, dev)
     if o.shape != (*q.shape[:-1], dv):
         raise ValueError("libkda: o must be shaped like q, with v's head size")
@@ -1009,7 +1018,7 @@ def kda_kv_append(k, v, pool, layout, table, lens, *, rows=None, cu_seqlens=None
         if nq != n or dq != dk or q.dim() != 3:
             raise ValueError("libkda: q must be [n,H_q,d_k] of k's tokens")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dt, device=q.device) if cu_seqlens is None else _filled(q.shape, dt, q.device, 0.0, stream)
+            q_out = _made(q.shape, dt, q.device, stream, None if cu_seqlens is None else 0.0)
         qop, qos = _head_out(_tensor(q_out, "q_out"), "q_out", q, dev, dt)
     elif q_out is not None:
         raise ValueError("libkda: q_out without q")
@@ -1033,10 +1042,10 @@ def kda_kv_read(pool, layout, table, cu_seqlens, total: int, *, rows=None, start
     if out_dtype not in _CODES:
         raise TypeError(f"libkda: outputs must be bfloat16 or float32, got {out_dtype}")
     if k_out is None:
-        k_out = _filled((total, layout.H, layout.d_k), out_dtype if v_out is None else _tensor(v_out, "v_out").dtype, pool.device, 0.0, stream)
+        k_out = _made((total, layout.H, layout.d_k), out_dtype if v_out is None else _tensor(v_out, "v_out").dtype, pool.device, stream, 0.0)
     odt = _tensor(k_out, "k_out").dtype
     if v_out is None:
-        v_out = _filled((total, layout.H, layout.d_v), odt, pool.device, 0.0, stream)
+        v_out = _made((total, layout.H, layout.d_v), odt, pool.device, stream, 0.0)
     _run("kda_kv_read", dev, stream, *cache, sp, cp, _need(k_out, "k_out", odt, dev, (total, layout.H, layout.d_k)),
          _need(v_out, "v_out", odt, dev, (total, layout.H, layout.d_v)), _io_code(k_out, "k_out"), N, total, layout.H, layout.d_k, layout.d_v)
     return k_out, v_out
@@ -1073,19 +1082,14 @@ def kda_attn_decode(q, pool, layout, table, lens, *, rows=None, scale=None, o=No
     out = (*shape[:-1], layout.d_v)
     if o is None:
         odt = dt if o_dtype is None else o_dtype
-        o = torch.empty(out, dtype=odt, device=q.device) if rows is None else _filled(out, odt, q.device, 0.0, stream)
+        o = _made(out, odt, q.device, stream, None if rows is None else 0.0)
     need = kda_attn_decode_plan(layout, B, K, Hq, cache[6])
     wp, wn = None, 0
     if workspace is not None:
         wn = _tensor(workspace, "workspace").numel()
         wp = _need(workspace, "workspace", torch.uint8, dev, (wn,))
     elif need:
-        # (memory of the call's stream: a block that the allocator hands out on another one could still be in use there)
-        if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        else:
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _made(need, torch.uint8, q.device, stream)
         wp, wn = workspace.data_ptr(), need
     _run("kda_attn_decode", dev, stream, _need(q, "q", dt, dev, shape), _io_code(q, "q"), dk ** -0.5 if scale is None else scale,
          *cache, _need(lens, "lens", _I32, dev, (B,)), _need(o, "o", _tensor(o, "o").dtype, dev, out), _io_code(o, "o"), wp, wn,
