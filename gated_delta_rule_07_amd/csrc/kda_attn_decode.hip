@@ -13,11 +13,13 @@
 //   8 channels of 8 keys and transposes them in registers (byte permutes, then the conversion to bf16).
 // Codes convert to bf16 exactly; the page's scales multiply scores and probabilities instead.
 // fp32 queries are split into three bf16 terms, and so are their probabilities: 24 bits on bf16 matrix cores.
-// (With bf16 queries the probabilities are rounded to bf16; maxima, sums and outputs are fp32 always.)
+// With bf16 queries the probabilities are two bf16 terms, 16 bits: one took bf16 outputs from 0.17% of the definition, their own
+// rounding, to 0.23%.  Against one term long sequences take the same time, short ones up to 0.7 us more (4 of 1,000 tokens 12.0
+// us for 11.4, 8 of 2,000 19.1 for 18.1).  Maxima, sums and outputs are fp32 always.
 // Measured, 32 + 8 heads of 128 in e4m3: 256 sequences of up to 9,000 tokens 465 us (5.6 TB/s, where reads alone reach 5.2 to 6.3
-// and copies 5.4), 4 drafts behind 1,000,003 tokens 363 us (5.6), of which the second kernel takes 7 and 8; one sequence of 903
-// tokens of 8 + 2 heads of 64 8.9 us, bound by the latency of a chain of loads: lengths, page numbers, keys.  Vector
-// instructions (conversions, byte permutes) take 28% of the cycles, the matrix cores 7.5%.  Slower: four waves a SIMD (they
+// and copies 5.4), 4 drafts behind 1,000,003 tokens 362 us (5.6), of which the second kernel takes 7 and 8; one sequence of 903
+// tokens of 8 + 2 heads of 64 9.0 us, bound by the latency of a chain of loads: lengths, page numbers, keys.  Vector
+// instructions (conversions, byte permutes) take 32% of the cycles, the matrix cores 11%.  Slower: four waves a SIMD (they
 // spill), 768 workgroups that share the granules (484 and 374 us).
 #include <algorithm>
 
@@ -34,7 +36,6 @@ constexpr int kLeastRun = 2;      // granules a workgroup takes at least
 constexpr float kSlack = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 __host__ __device__ inline int columns(int K, int G) { return (K * G + kAttnColumns - 1) / kAttnColumns; }
 
@@ -110,12 +111,14 @@ __device__ __forceinline__ float column_max(float x) {
   return fmaxf(__builtin_bit_cast(float, c), __builtin_bit_cast(float, d));
 }
 
-// (three waves a SIMD where the registers do without spilling: 256 sequences of up to 300 tokens of 32 + 8 heads 36 us, 43 with two)
+// (at least three waves a SIMD are asked for where the registers do without spilling: 110 to 152 of them here; the instances that
+// are asked for two have up to 168 with bf16 queries, so three too, and up to 203 with fp32 ones)
 template <int NW, int NT, bool E4, int DK, int DV>
 __global__ __launch_bounds__(64 * NW, NW == kWaves && NT == 1 && E4 ? 3 : 2) void kda_attn_decode_kernel(DecodePlan a) {
   constexpr int kThreads = 64 * NW, kGranule = NW * kTile;
   using T = Tile<E4, DK, DV>;
   constexpr int NM = DV / 16, NS = DK / 32;
+  constexpr int NP = NT == 1 ? 2 : NT;         // bf16 terms of a probability
   constexpr int ES = E4 ? 1 : 2, CW = 4 / ES;  // bytes of an element, elements of a dword
   __shared__ __attribute__((aligned(16))) float so[NW][kAttnColumns][DV + 4];
   __shared__ float sm[NW][kAttnColumns], sl[NW][kAttnColumns];
@@ -323,7 +326,7 @@ __global__ __launch_bounds__(64 * NW, NW == kWaves && NT == 1 && E4 ? 3 : 2) voi
         for (int t = 0; t < NM; ++t) o[t] *= keep;
       }
       const float base = m == -__builtin_inff() ? 0.0f : m;
-      bf16x8 pt8[NT];
+      bf16x8 pt8[NP];
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -332,10 +335,10 @@ __global__ __launch_bounds__(64 * NW, NW == kWaves && NT == 1 && E4 ? 3 : 2) voi
           l += y;
           float z = y * cur.vs[u];
 #pragma unroll
-          for (int n3 = 0; n3 < NT; ++n3) {
+          for (int n3 = 0; n3 < NP; ++n3) {
             const __bf16 t = (__bf16)z;
             pt8[n3][4 * u + r] = t;
-            if (n3 + 1 < NT) z -= (float)t;
+            if (n3 + 1 < NP) z -= (float)t;
           }
         }
       // V^T: 8 keys of channel NV col + t in a lane, a dword of each key's channels at a time
@@ -399,7 +402,7 @@ __global__ __launch_bounds__(64 * NW, NW == kWaves && NT == 1 && E4 ? 3 : 2) voi
 #pragma unroll
         for (int e = 0; e < CW; ++e)
 #pragma unroll
-          for (int n3 = NT - 1; n3 >= 0; --n3)
+          for (int n3 = NP - 1; n3 >= 0; --n3)
             o[CW * i + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt[e], pt8[n3], o[CW * i + e], 0, 0, 0);
       }
     };
@@ -528,9 +531,9 @@ __global__ __launch_bounds__(256) void kda_attn_join_kernel(DecodePlan a) {
 
 // Whether a call takes its units whole, a workgroup each: no workspace and no second launch.  It knows what rows of the table
 // hold, not how long the sequences are: longer rows are shared, lest one long sequence among short ones be one workgroup's.
-// With 32 + 8 heads of 128 in e4m3, whole against shared, us: 1 sequence (8 units) of 1,000 tokens 11.7 / 12.5, of 1,500 14.5 /
-// 12.5; 4 of 1,000 11.7 / 13.4, of 1,500 15.2 / 14.3; 8 of 1,500 15.5 / 16.3, of 2,000 18.2 / 18.2; 16 of 2,000 18.9 / 23.6, of
-// 4,000 40 / 38; 20 of 4,000 41 / 47; 64 of 4,000 98 / 108; 256 of 300 to 9,000 510 / 508.
+// With 32 + 8 heads of 128 in e4m3, whole against shared, us: 1 sequence (8 units) of 1,000 tokens 11.7 / 12.3, of 1,500 15.1 /
+// 12.3; 4 of 1,000 12.0 / 12.9, of 1,500 15.6 / 14.1; 8 of 1,500 16.0 / 16.0, of 2,000 19.2 / 18.2; 16 of 2,000 19.4 / 22.9, of
+// 4,000 36.7 / 36.0; 20 of 4,000 38 / 45; 64 of 4,000 92 / 96; 256 of 300 to 9,000 512 / 471.
 bool takes_whole(long long tokens, long long units) {
   return tokens <= 1280 || (tokens <= 2048 && units >= 64) || (tokens <= 4096 && units >= 128);
 }

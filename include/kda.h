@@ -712,7 +712,7 @@ kda_status kda_kv_read(const void* pool, kda_dtype kv_dtype, int n_pages, int pa
  *   (there are K * H_q / H_kv of them).
  *
  * fp32 queries are multiplied as three bf16 terms, and so are their probabilities: results
- * are fp32's.  With bf16 queries the probabilities are rounded to bf16.  Errors: KDA_ERR_NULL (workspace needed),
+ * are fp32's.  With bf16 queries the probabilities are two bf16 terms (16 bits).  Errors: KDA_ERR_NULL (workspace needed),
  * KDA_ERR_SHAPE (workspace_bytes too small), KDA_ERR_ALIAS (o or workspace overlaps another array).
  */
 #define KDA_MAX_ATTN_TOKENS 16 /* most tokens of a sequence in one kda_attn_decode call */
