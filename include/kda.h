@@ -669,7 +669,7 @@ kda_status kda_kv_page_bytes(kda_dtype kv_dtype, int page_tokens, int H_kv, int 
  * of two >= 2^-100 that brings the largest finite of them to 448 or below; codes are y / s rounded
  * to nearest even, values that are not finite become NaN.  A page that holds earlier tokens of the
  * sequence (its place in the row before lens[b]) keeps its scale, or, where the new tokens need a
- * larger one, has their codes rounded to that one -- exact, but for values below 2^-14 of the largest.
+ * larger one, has their codes rounded to that one -- exact, but for values below 2^-13 of the largest.
  *
  * A token without a page (padding, an entry outside [0, n_pages), a place behind the row's end) is not
  * stored; its rows of q_out and k_out are written all the same.  Nor is, rather than let them
