@@ -78,7 +78,8 @@ __device__ __forceinline__ void store4(const AttnParams& p, size_t at, const f32
 // The fp32 matrix cores are slow enough for the operands to come straight from the caches into registers: a
 // workgroup takes 16 or 32 queries, each of its waves every fourth tile of 32 keys, and they are joined at the end.  So a
 // few queries behind a long prefix already fill many waves.  Measured: 391 queries of 8 heads of 64 / 128 behind 3 cached
-// prefixes 26 us (eight waves: 29.6), 3,000 tokens of 8 heads of 128 196 us (94 TFLOP/s of 154).  Bound by the matrix
+// prefixes 26 us (eight waves: 29.6), 3,000 tokens of 8 heads of 128 196 us (94 TFLOP/s of 154); bf16, 4,000 tokens of 8 heads of 32 106 us
+// (77 TFLOP/s), of 16 86 us (48).  Bound by the matrix
 // cores, of which a wave with a SIMD to itself fills three quarters, and by what a compute unit takes from the L2, 32 KB a tile.
 //   S^T = K Q^T: a lane holds 8 of every 32 values of a key's row;
 //   O^T = V^T P^T: a lane holds DV / 16 neighbouring channels of 8 keys, and tile t of the output is the t-th of them.
@@ -326,10 +327,12 @@ __global__ __launch_bounds__(64 * kPlainWaves, RT == 1 ? 2 : 1) void kda_attn_pl
 // LDS rows are dense; their 16-byte pieces are exchanged (xor with bits of the row) so that the lanes of a
 // read fall on different banks (no conflicts in the counters).
 // Probabilities are rounded to bf16 for the product with V and summed as rounded, in fp32; scores, maxima, sums and outputs are fp32.
-// Measured, 32 + 8 heads of 128: 16,384 tokens 2.02 ms (1.09 PFLOP/s, where a matrix product of 8192^3 reaches 1.25), 24,961 tokens
+// (bf16 outputs are then 0.18 to 0.21% off the definition, their own rounding alone 0.16%.  Probabilities in two bf16 terms, as decode
+// has them, are half as many products again: 16,384 tokens 2.87 ms for 2.07, the packed batch 631 us for 484.)
+// Measured, 32 + 8 heads of 128: 16,384 tokens 2.02 ms (1.09 PFLOP/s, where a matrix product of 8192^3 reaches 1.36), 24,961 tokens
 // in 16 sequences 471 us (0.86).  Bound by the matrix cores and the exponentials beside them: the cores are busy 56% of the
 // cycles at a clock that the load holds at 1.8 GHz, vector instructions 43%, with two waves a SIMD to overlap them (256 registers
-// each).  The packed batch loses 6% to cut tiles and the rest to its 6,900 workgroups' first loads and last stores.
+// each).  The packed batch loses 6% to cut tiles and the rest to the first loads and last stores of its 6,528 workgroups (of 6,752 launched).
 // Slower: eight waves and 256 queries a workgroup (packed 620 us), scores a tile ahead of the probabilities (566).
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -638,8 +641,9 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_kernel(AttnParams p, unsi
 // ---- the same for few queries ---------------------------------------------------------------
 // Where the workgroups above would not fill the compute units -- a short prompt, one prompt of few heads, or a few
 // new tokens behind a long prefix -- a workgroup takes 32 queries, and each of its four waves every fourth tile of 32 keys,
-// through two buffers of its own in LDS: no barrier until the waves are joined.  Bound by latency: 77 tokens of 8 heads of 64 5.1 us, and
-// behind 8,000 cached tokens 128 of 32 heads of 128 64 us (0.53 PFLOP/s).
+// through two buffers of its own in LDS: no barrier until the waves are joined.  Bound by latency: 77 tokens of 8 heads of 64 5.1 us.
+// 128 tokens of 32 heads of 128 behind 8,000 cached ones 64 us (0.26 PFLOP/s): 128 workgroups on 256 compute units, and with 131 KB of LDS
+// a workgroup one wave a SIMD, whose exponentials and products nothing overlaps.
 
 constexpr int kSplitWaves = 4, kSplitKeys = 32;
 constexpr unsigned kFewTiles = 256;  // workgroups of it that fill the compute units

@@ -18,7 +18,7 @@
 // us for 11.4, 8 of 2,000 19.1 for 18.1).  Maxima, sums and outputs are fp32 always.
 // Measured, 32 + 8 heads of 128 in e4m3: 256 sequences of up to 9,000 tokens 465 us (5.6 TB/s, where reads alone reach 5.2 to 6.3
 // and copies 5.4), 4 drafts behind 1,000,003 tokens 362 us (5.6), of which the second kernel takes 7 and 8; one sequence of 903
-// tokens of 8 + 2 heads of 64 9.0 us, bound by the latency of a chain of loads: lengths, page numbers, keys.  Vector
+// tokens of 8 + 2 heads of 64 9.0 us (fp32 queries: the 256 sequences 510 us, the one 10.0), bound by the latency of a chain of loads: lengths, page numbers, keys.  Vector
 // instructions (conversions, byte permutes) take 32% of the cycles, the matrix cores 11%.  Slower: four waves a SIMD (they
 // spill), 768 workgroups that share the granules (484 and 374 us).
 #include <algorithm>

@@ -576,7 +576,8 @@ kda_status kda_tree_commit(const void* k, kda_dtype qkv_dtype, const float* alph
 
 /* ---- attention layers beside the recurrent ones ----------------------------------------
  *
- * A hybrid model has an attention layer after every few recurrent ones.  Query head h
+ * A hybrid model has an attention layer after every few recurrent ones; these calls serve layers of plain
+ * grouped heads (keys and values of each head are cached, no latent form of them).  Query head h
  * attends with the keys and values of head h / (H_q / H_kv) (grouped heads; H_q a multiple
  * of H_kv), and its output is
  *     o = sum_j p_j v_j,    p = softmax over the j it sees of  scale * q . k_j.
@@ -601,7 +602,7 @@ kda_status kda_tree_commit(const void* k, kda_dtype qkv_dtype, const float* alph
  *   table      : [n_rows][width] int32, DEVICE memory, n_rows * width <= 2^26 and
  *                width * page_tokens < 2^31 (KDA_ERR_SHAPE)
  *   rows       : [N] int32, DEVICE memory, the table row of each sequence of the call, or
- *                NULL: row b.  A row outside [0, n_rows) is padding.
+ *                NULL: row b (N <= n_rows, KDA_ERR_SHAPE).  A row outside [0, n_rows) is padding.
  *   d_k, d_v   : 64 or 128 (KDA_ERR_UNSUPPORTED otherwise)
  * Lists in device memory that are wrong never make a kernel access memory out of range.
  * H_q, H_kv <= KDA_MAX_HEADS and tokens of a call <= KDA_MAX_CALL_TOKENS, else KDA_ERR_SHAPE.
@@ -670,6 +671,8 @@ kda_status kda_kv_page_bytes(kda_dtype kv_dtype, int page_tokens, int H_kv, int 
  * to nearest even, values that are not finite become NaN.  A page that holds earlier tokens of the
  * sequence (its place in the row before lens[b]) keeps its scale, or, where the new tokens need a
  * larger one, has their codes rounded to that one -- exact, but for values below 2^-13 of the largest.
+ * Tokens that are taken back (a smaller lens in the next call, as after rejected drafts) leave the scale and
+ * that rounding behind on a page that still holds others.
  *
  * A token without a page (padding, an entry outside [0, n_pages), a place behind the row's end) is not
  * stored; its rows of q_out and k_out are written all the same.  Nor is, rather than let them
