@@ -10,7 +10,7 @@
 // maximum and the cosines and sines (in LDS) serve all heads; a wave takes one head's keys or values.
 // Workgroups behind the pages turn the queries.  A lane holds two pieces of 8 values of a row, those
 // that turn together, so that a rotation exchanges nothing between lanes.
-// Angles are reduced in fp64, the rest is fp32; values are rounded once, to the page's or the output's type.
+// Cosines and sines are formed in fp64, the rest is fp32; values are rounded once, to the page's or the output's type.
 // Measured: 65,536 tokens of 32 + 8 heads of 128 in 16 sequences onto e4m3 pages 290 us, 5.1 TB/s of the bytes that it cannot do
 // without and 5.9 of those it moves (rows of a page beyond the first 32 are fetched again for the codes, when the scale
 // is known; sharing a head among waves, so that all rows stay in registers, gains 2% there and costs 8% with few heads).  256
@@ -45,12 +45,17 @@ __device__ __forceinline__ u32x4 bits_of(const f32x4& lo, const f32x4& hi) {
   return __builtin_bit_cast(u32x4, h);
 }
 
-// Cosine and sine of pos times a frequency in turns: the angle's reduction to a fraction of a turn in fp64.
+// Cosine and sine of pos times a frequency in turns, in fp64 and then rounded: the angle's distance x from the nearest quarter
+// turn, and the series about 0 (|x| <= pi / 4: what is left out is below 1.2e-10).  From an angle rounded to fp32 they would be more than a
+// step off, and with them more codes on the other side of a border. (The time is the same.)
 __device__ __forceinline__ float2 turn_of(double pos, double freq) {
-  const double turns = pos * freq;
-  float s, c;
-  sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
-  return float2{c, s};
+  const double turns = pos * freq, t = turns - rint(turns), quarter = rint(4.0 * t);
+  const double x = (t - 0.25 * quarter) * 6.283185307179586, y = x * x;
+  const double c = 1.0 + y * (-1.0 / 2 + y * (1.0 / 24 + y * (-1.0 / 720 + y * (1.0 / 40320 + y * (-1.0 / 3628800)))));
+  const double s = x * (1.0 + y * (-1.0 / 6 + y * (1.0 / 120 + y * (-1.0 / 5040 + y * (1.0 / 362880 + y * (-1.0 / 39916800))))));
+  const int q = (int)quarter;  // -2 .. 2
+  const float cf = (float)(q & 1 ? s : c), sf = (float)(q & 1 ? c : s);
+  return float2{q + 1 & 2 ? -cf : cf, q & 2 ? -sf : sf};
 }
 
 // The turns of nt tokens at positions pos(t) to turn[t][half]: a thread keeps to one frequency.

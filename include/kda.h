@@ -665,7 +665,7 @@ kda_status kda_kv_page_bytes(kda_dtype kv_dtype, int page_tokens, int H_kv, int 
  *   pool      : the pages' entries for the new tokens                  (written)
  *   N         : 1 .. KDA_MAX_PAGED_SEQS
  *
- * Angles are reduced in fp64, everything else is fp32; what goes to a bf16 page, q_out or k_out is
+ * Cosines and sines are formed in fp64, everything else is fp32; what goes to a bf16 page, q_out or k_out is
  * rounded once.  KDA_E4M3: each head's keys (values) on a page have the scale s, the smallest power
  * of two >= 2^-100 that brings the largest finite of them to 448 or below; codes are y / s rounded
  * to nearest even, values that are not finite become NaN.  A page that holds earlier tokens of the
